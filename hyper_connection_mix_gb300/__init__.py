@@ -5,4 +5,4 @@ The compute path is the C-ABI library libhcmix.so (hand-written CUDA kernels);
 package does not load the library; the first call into `binding` does, and it
 raises if the library is missing -- there is no CPU fallback.
 """
-__all__ = ["binding", "traffic"]
+__all__ = ["binding", "sublayer", "traffic"]

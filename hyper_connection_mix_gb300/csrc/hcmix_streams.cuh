@@ -1,0 +1,200 @@
+// Hyper-connection coefficients applied to the four residual streams of a row:
+// collapse (h = sum_i pre_i x_i), expand (x'_i = post_i y + sum_j comb_ij x_j)
+// and their gradients.  Every output element needs the same column of every
+// stream, so a thread takes one column vector of all of them and each operand
+// is read and written once.
+#pragma once
+
+#include "hcmix_vec.cuh"
+
+namespace hcmix {
+namespace sublayer {
+
+struct StreamsArgs {
+  const void *x, *y, *g, *add;  // streams; sublayer output; gradient; gradient to add
+  int64_t x_stride, y_stride, g_stride, add_stride;
+  const float *pre, *post, *comb;
+  void *out, *dy;
+  float *dpre, *dpost, *dcomb;
+  int64_t M, D;
+  int chunks;  // thread blocks across a row (forward kernels)
+};
+
+template <typename T, int kVec>
+__global__ void __launch_bounds__(256) hcmix_collapse_kernel(const StreamsArgs A) {
+  const int64_t row = blockIdx.x / A.chunks;
+  const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * blockDim.x + threadIdx.x) * kVec;
+  if (c >= A.D) return;
+  const T* x = static_cast<const T*>(A.x) + row * A.x_stride + c;
+  float h[kVec] = {};
+#pragma unroll
+  for (int i = 0; i < kStreams; ++i) {
+    float v[kVec];
+    load_f32<T, kVec>(x + i * A.D, v);
+    const float w = A.pre[row * kStreams + i];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) h[e] = fmaf(w, v[e], h[e]);
+  }
+  store_f32<T, kVec>(static_cast<T*>(A.out) + row * A.D + c, h);
+}
+
+template <typename T, int kVec>
+__global__ void __launch_bounds__(256) hcmix_expand_kernel(const StreamsArgs A) {
+  const int64_t row = blockIdx.x / A.chunks;
+  const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * blockDim.x + threadIdx.x) * kVec;
+  if (c >= A.D) return;
+  const T* x = static_cast<const T*>(A.x) + row * A.x_stride + c;
+  const float* comb = A.comb + row * kStreams * kStreams;
+  float v[kStreams][kVec], y[kVec];
+#pragma unroll
+  for (int j = 0; j < kStreams; ++j) load_f32<T, kVec>(x + j * A.D, v[j]);
+  load_f32<T, kVec>(static_cast<const T*>(A.y) + row * A.y_stride + c, y);
+#pragma unroll
+  for (int i = 0; i < kStreams; ++i) {
+    const float p = A.post[row * kStreams + i];
+    float o[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) o[e] = p * y[e];
+#pragma unroll
+    for (int j = 0; j < kStreams; ++j) {
+      const float w = comb[i * kStreams + j];
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) o[e] = fmaf(w, v[j][e], o[e]);
+    }
+    store_f32<T, kVec>(static_cast<T*>(A.out) + row * kStreams * A.D + i * A.D + c, o);
+  }
+}
+
+// One block a row: the row's four dot products need all of its columns.
+template <typename T, int kVec>
+__global__ void __launch_bounds__(1024) hcmix_collapse_backward_kernel(const StreamsArgs A) {
+  __shared__ float part[kStreams * 32];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
+  const T* g = static_cast<const T*>(A.g) + row * A.g_stride;
+  T* dx = static_cast<T*>(A.out) + row * kStreams * A.D;
+  float pre[kStreams], dot[kStreams] = {};
+#pragma unroll
+  for (int i = 0; i < kStreams; ++i) pre[i] = A.pre[row * kStreams + i];
+  for (int64_t c = (int64_t)threadIdx.x * kVec; c < A.D; c += blockDim.x * kVec) {
+    float dh[kVec];
+    load_f32<T, kVec>(g + c, dh);
+#pragma unroll
+    for (int i = 0; i < kStreams; ++i) {
+      float v[kVec], d[kVec] = {};
+      load_f32<T, kVec>(x + i * A.D + c, v);
+      if (A.add != nullptr)
+        load_f32<T, kVec>(static_cast<const T*>(A.add) + row * A.add_stride + i * A.D + c, d);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        dot[i] = fmaf(dh[e], v[e], dot[i]);
+        d[e] = fmaf(pre[i], dh[e], d[e]);
+      }
+      store_f32<T, kVec>(dx + i * A.D + c, d);
+    }
+  }
+  block_sum<kStreams>(dot, part);
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < kStreams; ++i) A.dpre[row * kStreams + i] = dot[i];
+  }
+}
+
+// One block a row, as above; 4 + 16 dot products.
+template <typename T, int kVec>
+__global__ void __launch_bounds__(512) hcmix_expand_backward_kernel(const StreamsArgs A) {
+  constexpr int kDots = kStreams + kStreams * kStreams;
+  __shared__ float part[kDots * 32];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
+  const T* y = static_cast<const T*>(A.y) + row * A.y_stride;
+  const T* g = static_cast<const T*>(A.g) + row * A.g_stride;
+  T* dx = static_cast<T*>(A.out) + row * kStreams * A.D;
+  T* dy = static_cast<T*>(A.dy) + row * A.D;
+  float post[kStreams], comb[kStreams][kStreams], dot[kDots] = {};
+#pragma unroll
+  for (int i = 0; i < kStreams; ++i) {
+    post[i] = A.post[row * kStreams + i];
+#pragma unroll
+    for (int j = 0; j < kStreams; ++j)
+      comb[i][j] = A.comb[(row * kStreams + i) * kStreams + j];
+  }
+  for (int64_t c = (int64_t)threadIdx.x * kVec; c < A.D; c += blockDim.x * kVec) {
+    float d[kStreams][kVec], v[kVec], o[kVec];
+#pragma unroll
+    for (int i = 0; i < kStreams; ++i) load_f32<T, kVec>(g + i * A.D + c, d[i]);
+    load_f32<T, kVec>(y + c, v);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      o[e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kStreams; ++i) {
+        o[e] = fmaf(post[i], d[i][e], o[e]);
+        dot[i] = fmaf(d[i][e], v[e], dot[i]);
+      }
+    }
+    store_f32<T, kVec>(dy + c, o);
+#pragma unroll
+    for (int j = 0; j < kStreams; ++j) {
+      load_f32<T, kVec>(x + j * A.D + c, v);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        o[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kStreams; ++i) {
+          o[e] = fmaf(comb[i][j], d[i][e], o[e]);
+          dot[kStreams + i * kStreams + j] =
+              fmaf(d[i][e], v[e], dot[kStreams + i * kStreams + j]);
+        }
+      }
+      store_f32<T, kVec>(dx + j * A.D + c, o);
+    }
+  }
+  block_sum<kDots>(dot, part);
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < kStreams; ++i) A.dpost[row * kStreams + i] = dot[i];
+#pragma unroll
+    for (int i = 0; i < kStreams * kStreams; ++i)
+      A.dcomb[row * kStreams * kStreams + i] = dot[kStreams + i];
+  }
+}
+
+enum class StreamsOp { kCollapse, kExpand, kCollapseBackward, kExpandBackward };
+
+template <typename T, int kVec>
+hcmix_status launch_streams(StreamsOp op, StreamsArgs A, cudaStream_t stream) {
+  const int64_t vecs = (A.D + kVec - 1) / kVec;
+  if (op == StreamsOp::kCollapse || op == StreamsOp::kExpand) {
+    A.chunks = (int)((vecs + 255) / 256);
+    const int threads = (int)((vecs + A.chunks - 1) / A.chunks + 31) / 32 * 32;
+    const int64_t blocks = A.M * A.chunks;
+    if (blocks >= ((int64_t)1 << 31)) return HCMIX_ERR_UNSUPPORTED;
+    if (op == StreamsOp::kCollapse)
+      hcmix_collapse_kernel<T, kVec><<<(unsigned)blocks, threads, 0, stream>>>(A);
+    else
+      hcmix_expand_kernel<T, kVec><<<(unsigned)blocks, threads, 0, stream>>>(A);
+    return launched();
+  }
+  const int threads = vecs >= 256 ? 256 : (int)(vecs + 31) / 32 * 32;
+  if (op == StreamsOp::kCollapseBackward)
+    hcmix_collapse_backward_kernel<T, kVec><<<(unsigned)A.M, threads, 0, stream>>>(A);
+  else
+    hcmix_expand_backward_kernel<T, kVec><<<(unsigned)A.M, threads, 0, stream>>>(A);
+  return launched();
+}
+
+inline hcmix_status run_streams(StreamsOp op, const StreamsArgs& A, hcmix_type type,
+                                cudaStream_t stream) {
+  const int n = size_of(type);
+  const bool wide = aligned_rows(A.x, A.x_stride, n) && aligned_rows(A.y, A.y_stride, n) &&
+                    aligned_rows(A.g, A.g_stride, n) && aligned_rows(A.add, A.add_stride, n) &&
+                    aligned_rows(A.out, A.D, n) && aligned_rows(A.dy, A.D, n);
+  return with_type(type, [&](auto t) {
+    using T = decltype(t);
+    return wide ? launch_streams<T, kWide<T>>(op, A, stream) : launch_streams<T, 1>(op, A, stream);
+  });
+}
+
+}  // namespace sublayer
+}  // namespace hcmix
