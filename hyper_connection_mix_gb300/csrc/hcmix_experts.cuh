@@ -41,12 +41,12 @@ inline size_t sort_smem(int E) { return ((size_t)sort_warps(E) * E + 2 * (size_t
 // rank is the number of lower lanes with its expert.
 __global__ void __launch_bounds__(1024) hcmix_expert_sort_kernel(const SortArgs A) {
   namespace cg = cooperative_groups;
-  extern __shared__ int smem[];
+  extern __shared__ int sort_shared[];
   const cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), cta = cluster.block_rank();
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int E = A.E;
-  int* count = smem;                // [warps][E]
+  int* count = sort_shared;         // [warps][E]
   int* total = count + warps * E;   // [E] this block's pairs of each expert
   int* start = total + E;           // [E] the block's first row of each expert
   int* scan = start + E;            // [warps] sums of the scan over experts

@@ -24,43 +24,64 @@ struct NormArgs {
   int blocks;  // partial rows of the weight's gradient
 };
 
-// kVec values of column c of a row: x itself, or sum_i pre[i] x_i.
+// kVec values of column c of a row, x itself or sum_i pre[i] x_i: first loaded,
+// then worked out.
+template <typename T, int kVec, bool kCollapse>
+struct NormSource {
+  Packed<T, kVec> s[kCollapse ? kStreams : 1];
+  __device__ __forceinline__ void load(const NormArgs& A, const T* x, int64_t c) {
+#pragma unroll
+    for (int i = 0; i < (kCollapse ? kStreams : 1); ++i)
+      s[i] = load_vec<T, kVec>(x + i * A.N + c);
+  }
+  __device__ __forceinline__ void values(const float* pre, float (&v)[kVec]) const {
+    s[0].unpack(v);
+    if constexpr (kCollapse) {
+      vmul(v, pre[0], v);
+#pragma unroll
+      for (int i = 1; i < kStreams; ++i) {
+        float t[kVec];
+        s[i].unpack(t);
+        vfma(v, pre[i], t, v);
+      }
+    }
+  }
+};
+
 template <typename T, int kVec, bool kCollapse>
 __device__ __forceinline__ void norm_source(const NormArgs& A, const T* x, const float* pre,
                                             int64_t c, float (&v)[kVec]) {
-  if constexpr (!kCollapse) {
-    load_f32<T, kVec>(x + c, v);
-  } else {
-    float s[kStreams][kVec];
+  NormSource<T, kVec, kCollapse> s;
+  s.load(A, x, c);
+  s.values(pre, v);
+}
+
+// Weight and bias of column c, ones and zeros where there are none.
+template <typename T, int kVec>
+__device__ __forceinline__ void norm_params(const NormArgs& A, int64_t c, float (&w)[kVec],
+                                            float (&b)[kVec]) {
 #pragma unroll
-    for (int i = 0; i < kStreams; ++i) load_f32<T, kVec>(x + i * A.N + c, s[i]);
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      v[e] = pre[0] * s[0][e];
-#pragma unroll
-      for (int i = 1; i < kStreams; ++i) v[e] = fmaf(pre[i], s[i][e], v[e]);
-    }
-  }
+  for (int e = 0; e < kVec; ++e) w[e] = 1.f, b[e] = 0.f;
+  if (A.weight != nullptr) load_param<T, kVec>(A.weight, A.p32, c, w);
+  if (A.bias != nullptr) load_param<T, kVec>(A.bias, A.p32, c, b);
 }
 
 template <typename T, int kVec>
 __device__ __forceinline__ void norm_apply(const NormArgs& A, int64_t row, int64_t c, float mean,
                                            float rstd, float (&v)[kVec]) {
   float w[kVec], b[kVec];
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) w[e] = 1.f, b[e] = 0.f;
-  if (A.weight != nullptr) load_param<T, kVec>(A.weight, A.p32, c, w);
-  if (A.bias != nullptr) load_param<T, kVec>(A.bias, A.p32, c, b);
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) v[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
+  norm_params<T, kVec>(A, c, w, b);
+  vadd(v, -mean, v);
+  vmul(v, rstd, v);
+  vfma(v, v, w, b);
   store_f32<T, kVec>(static_cast<T*>(A.y) + row * A.N + c, v);
 }
 
 // One block a row, the row in registers: kPer vectors a thread.  The mean is
 // taken first and the variance from the differences, so that a large mean
 // costs no digits.
-template <typename T, int kVec, int kPer, bool kCollapse>
-__global__ void __launch_bounds__(1024) hcmix_norm_kernel(const NormArgs A) {
+template <typename T, int kVec, int kPer, int kThreads, bool kCollapse>
+__global__ void __launch_bounds__(kThreads) hcmix_norm_kernel(const NormArgs A) {
   __shared__ float part[2][32];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
@@ -71,11 +92,17 @@ __global__ void __launch_bounds__(1024) hcmix_norm_kernel(const NormArgs A) {
   }
   float v[kPer][kVec];
   float sum[1] = {0.f};
+  NormSource<T, kVec, kCollapse> raw[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int64_t c = ((int64_t)k * blockDim.x + threadIdx.x) * kVec;
+    if (c < A.N) raw[k].load(A, x, c);
+  }
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int64_t c = ((int64_t)k * blockDim.x + threadIdx.x) * kVec;
     if (c < A.N) {
-      norm_source<T, kVec, kCollapse>(A, x, pre, c, v[k]);
+      raw[k].values(pre, v[k]);
     } else {
 #pragma unroll
       for (int e = 0; e < kVec; ++e) v[k][e] = 0.f;
@@ -152,16 +179,179 @@ __global__ void __launch_bounds__(512) hcmix_norm_wide_kernel(const NormArgs A) 
   }
 }
 
+// Resident blocks that take rows b, b + blocks, ... through a ring of `stages`
+// rows in shared memory.  Each thread copies the vectors that it will read itself
+// (cp.async), so no barrier stands between the copies and their use, and what
+// belongs to its columns (weight, bias, sums over rows) stays in registers.
+// kRows: source rows of a stage (streams, or x and dy), source(i) the first
+// element of the i-th for a row, `width` elements each.
+template <typename T, int kVec, int kPer, int kRows>
+struct Ring {
+  using V = Packed<T, kVec>;
+  V* mine;
+  int stages, stage;
+  __device__ __forceinline__ Ring(unsigned char* smem, int n)
+      : mine(reinterpret_cast<V*>(smem) + threadIdx.x), stages(n), stage(0) {}
+  static __device__ __forceinline__ int64_t column(int k) {
+    return ((int64_t)k * blockDim.x + threadIdx.x) * kVec;
+  }
+  __device__ __forceinline__ V* at(int s, int i, int k) const {
+    return mine + ((s * kRows + i) * kPer + k) * (int)blockDim.x;
+  }
+  // Starts the copy of a row into stage s; `valid` false: an empty group, which
+  // keeps the count.
+  template <typename Source>
+  __device__ __forceinline__ void fetch(bool valid, int s, int64_t width, Source&& source) const {
+    if (valid) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const T* from = source(i);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (column(k) < width) async_copy(at(s, i, k), from + column(k));
+      }
+    }
+    async_commit();
+  }
+  // The stage to refill while this row is worked on: the one read a row ago.
+  __device__ __forceinline__ int refill() const { return stage == 0 ? stages - 1 : stage - 1; }
+  __device__ __forceinline__ void wait() const { async_wait(stages); }
+  __device__ __forceinline__ const V& read(int i, int k) const { return *at(stage, i, k); }
+  __device__ __forceinline__ void advance() {
+    if (++stage == stages) stage = 0;
+  }
+};
+
+constexpr int kSms = 152;
+constexpr size_t kRingBytes = 200 * 1024;  // of all blocks of a multiprocessor
+
+struct RingPlan {
+  int threads, stages, each;  // each: blocks a multiprocessor
+  size_t smem;
+};
+
+// `each` blocks of `most` threads fit a multiprocessor; smaller ones in proportion.
+inline RingPlan ring_plan(int64_t vecs, int per, int most, int each, int rows, int vec_bytes) {
+  RingPlan p;
+  p.threads = (int)((vecs + per - 1) / per + 31) / 32 * 32;
+  p.each = each * most / p.threads;
+  p.each = p.each > 16 ? 16 : p.each;
+  const size_t stage = (size_t)rows * per * p.threads * vec_bytes;
+  p.stages = (int)(kRingBytes / p.each / stage);
+  p.stages = p.stages > 8 ? 8 : p.stages < 2 ? 2 : p.stages;
+  p.smem = p.stages * stage;
+  return p;
+}
+
+// The norm of 16-byte vectors through the ring.
+template <typename T, int kVec, int kPer, int kThreads, int kBlocks, bool kCollapse>
+__global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_ring_kernel(const NormArgs A,
+                                                                            int stages) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float part[2][32];
+  constexpr int kRows = kCollapse ? kStreams : 1;
+  using R = Ring<T, kVec, kPer, kRows>;
+  R ring(smem, stages);
+  const auto fetch = [&](int64_t row, int s) {
+    ring.fetch(row < A.M, s, A.N,
+               [&](int i) { return static_cast<const T*>(A.x) + row * A.x_stride + i * A.N; });
+  };
+  int64_t next = blockIdx.x;
+  for (int s = 0; s < stages - 1; ++s, next += gridDim.x) fetch(next, s);
+  float w[kPer][kVec], b[kPer][kVec];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    if (R::column(k) < A.N) norm_params<T, kVec>(A, R::column(k), w[k], b[k]);
+  const float inv = 1.f / (float)A.N;
+  for (int64_t row = blockIdx.x; row < A.M; row += gridDim.x, next += gridDim.x) {
+    float pre[kStreams] = {};
+    if constexpr (kCollapse) {
+#pragma unroll
+      for (int i = 0; i < kStreams; ++i) pre[i] = A.pre[row * kStreams + i];
+    }
+    fetch(next, ring.refill());
+    ring.wait();
+    float v[kPer][kVec];
+    Acc acc;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (R::column(k) < A.N) {
+        NormSource<T, kVec, kCollapse> raw;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) raw.s[i] = ring.read(i, k);
+        raw.values(pre, v[k]);
+        acc.add(v[k]);
+      }
+    }
+    float sum[1] = {acc.sum()};
+    block_sum<1>(sum, part[0]);
+    const float mean = sum[0] * inv;
+    Acc square;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (R::column(k) < A.N) {
+        if (kCollapse && A.h != nullptr)
+          store_f32<T, kVec>(static_cast<T*>(A.h) + row * A.N + R::column(k), v[k]);
+        vadd(v[k], -mean, v[k]);
+        square.add(v[k], v[k]);
+      }
+    }
+    float sq[1] = {square.sum()};
+    block_sum<1>(sq, part[1]);
+    const float rstd = 1.f / sqrtf(sq[0] * inv + A.eps);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (R::column(k) < A.N) {
+        vmul(v[k], rstd, v[k]);
+        vfma(v[k], v[k], w[k], b[k]);
+        store_f32<T, kVec>(static_cast<T*>(A.y) + row * A.N + R::column(k), v[k]);
+      }
+    }
+    if (threadIdx.x == 0) {
+      if (A.mean != nullptr) A.mean[row] = mean;
+      if (A.rstd != nullptr) A.rstd[row] = rstd;
+    }
+    ring.advance();
+  }
+}
+
+template <typename T, int kVec, int kPer, int kThreads, int kBlocks, bool kCollapse>
+hcmix_status launch_norm_ring(const NormArgs& A, int64_t vecs, cudaStream_t stream) {
+  const RingPlan p =
+      ring_plan(vecs, kPer, kThreads, kBlocks, kCollapse ? kStreams : 1, kVec * (int)sizeof(T));
+  const auto kernel = hcmix_norm_ring_kernel<T, kVec, kPer, kThreads, kBlocks, kCollapse>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) !=
+      cudaSuccess)
+    return HCMIX_ERR_CUDA;
+  const int64_t blocks = A.M < kSms * p.each ? A.M : kSms * p.each;
+  kernel<<<(unsigned)blocks, p.threads, p.smem, stream>>>(A, p.stages);
+  return launched();
+}
+
+// The variant goes by type, alignment and width, never by the number of rows: a
+// row's result is the same bits in a call of one row and of many.
 template <typename T, int kVec, bool kCollapse>
 hcmix_status launch_norm(const NormArgs& A, cudaStream_t stream) {
-  constexpr int kMost = kVec == 1 ? 16 : 4;  // vectors a thread: at most 32 values
+  // vectors a thread and threads of the usual block: what a thread loads before it
+  // adds anything up (four streams' worth when collapsing) has to fit its registers
+  constexpr int kMost = (kVec == 1 ? 16 : 4) / (kCollapse ? 2 : 1);
+  constexpr int kThreads = kCollapse ? 512 : 256;
   const int64_t vecs = (A.N + kVec - 1) / kVec;
   const unsigned grid = (unsigned)A.M;
   const auto threads = [&](int per) { return (unsigned)((vecs + per - 1) / per + 31) / 32 * 32; };
-  if (vecs <= 256)
-    hcmix_norm_kernel<T, kVec, 1, kCollapse><<<grid, threads(1), 0, stream>>>(A);
-  else if (vecs <= 1024 * kMost)
-    hcmix_norm_kernel<T, kVec, kMost, kCollapse><<<grid, threads(kMost), 0, stream>>>(A);
+  if constexpr (kVec > 1) {
+    if (vecs <= 256) return launch_norm_ring<T, kVec, 1, 256, 4, kCollapse>(A, vecs, stream);
+    if (vecs <= 640) return launch_norm_ring<T, kVec, 2, 320, 2, kCollapse>(A, vecs, stream);
+    if (vecs <= 1024) return launch_norm_ring<T, kVec, 2, 512, 1, kCollapse>(A, vecs, stream);
+  } else {
+    if (vecs <= kThreads * kMost) {
+      hcmix_norm_kernel<T, kVec, kMost, kThreads, kCollapse>
+          <<<grid, threads(kMost), 0, stream>>>(A);
+      return launched();
+    }
+  }
+  if (vecs <= 1024 * kMost)
+    hcmix_norm_kernel<T, kVec, kMost, 1024, kCollapse><<<grid, threads(kMost), 0, stream>>>(A);
   else
     hcmix_norm_wide_kernel<T, kVec, kCollapse><<<grid, 512, 0, stream>>>(A);
   return launched();
@@ -247,38 +437,201 @@ __global__ void __launch_bounds__(kColumnThreads) hcmix_norm_columns_kernel(cons
   }
 }
 
-// The partial rows added in order.
-__global__ void __launch_bounds__(256) hcmix_norm_join_kernel(const NormArgs A) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= 2 * A.N) return;
+// dx and the partial sums of the weight's and bias's gradient in one pass over x
+// and dy, through the ring; the one barrier a row is that of the row's two sums.
+// A thread keeps dweight and dbias of its columns in registers.  With one vector
+// a thread (kPer 1) weight, (x - mean) rstd and dy weight stay there too; with
+// more they are read and worked out again, from L1 and the stage.
+template <typename T, int kVec, int kPer, int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_backward_kernel(const NormArgs A,
+                                                                                int stages) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float part[2][2 * 32];
+  constexpr bool kKeep = kPer == 1;
+  using R = Ring<T, kVec, kPer, 2>;
+  R ring(smem, stages);
+  const auto fetch = [&](int64_t row, int s) {
+    ring.fetch(row < A.M, s, A.N, [&](int i) {
+      return i == 0 ? static_cast<const T*>(A.x) + row * A.x_stride
+                    : static_cast<const T*>(A.dy) + row * A.dy_stride;
+    });
+  };
+  int64_t next = blockIdx.x;
+  for (int s = 0; s < stages - 1; ++s, next += gridDim.x) fetch(next, s);
+  float dw[kPer][kVec] = {}, db[kPer][kVec] = {}, w[kVec];
+  const auto load_weight = [&](int k) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) w[e] = 1.f;
+    if (A.weight != nullptr && R::column(k) < A.N)
+      load_param<T, kVec>(A.weight, A.p32, R::column(k), w);
+  };
+  if (kKeep) load_weight(0);
+  const float inv = 1.f / (float)A.N;
+  int odd = 0;
+  float next_mean = A.mean[blockIdx.x], next_rstd = A.rstd[blockIdx.x];
+  for (int64_t row = blockIdx.x; row < A.M; row += gridDim.x, next += gridDim.x, odd ^= 1) {
+    const float mean = next_mean, rstd = next_rstd;
+    if (row + gridDim.x < A.M) {
+      next_mean = A.mean[row + gridDim.x];
+      next_rstd = A.rstd[row + gridDim.x];
+    }
+    fetch(next, ring.refill());
+    ring.wait();
+    float xh[kVec], g[kVec], t[kVec];
+    const auto load_row = [&](int k) {
+      ring.read(0, k).unpack(xh);
+      ring.read(1, k).unpack(g);
+      if (!kKeep) load_weight(k);
+      vadd(xh, -mean, xh);
+      vmul(xh, rstd, xh);
+      vmul(t, g, w);
+    };
+    Acc acc[2];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (R::column(k) < A.N) {
+        load_row(k);
+        vfma(dw[k], g, xh, dw[k]);
+        vadd(db[k], g, db[k]);
+        acc[0].add(t);
+        acc[1].add(t, xh);
+      }
+    }
+    float sum[2] = {acc[0].sum(), acc[1].sum()};
+    block_sum<2>(sum, part[odd]);  // two rows apart, a barrier lies between the uses
+    const float c1 = sum[0] * inv, c2 = sum[1] * inv;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (R::column(k) < A.N) {
+        if (!kKeep) load_row(k);
+        vadd(t, -c1, t);
+        vfma(t, -c2, xh, t);
+        vmul(t, rstd, t);
+        store_f32<T, kVec>(static_cast<T*>(A.dx) + row * A.N + R::column(k), t);
+      }
+    }
+    ring.advance();
+  }
+  launch_dependents();
+  float* out = A.part + (int64_t)blockIdx.x * 2 * A.N;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (R::column(k) < A.N) {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        out[R::column(k) + e] = dw[k][e];
+        out[A.N + R::column(k) + e] = db[k][e];
+      }
+    }
+  }
+}
+
+// The partial rows added up: 32 columns a block, 16 groups of rows, each group's
+// rows and then the groups in order.
+constexpr int kJoinGroups = 16;
+
+__global__ void __launch_bounds__(32 * kJoinGroups) hcmix_norm_join_kernel(const NormArgs A) {
+  __shared__ float part[kJoinGroups][32];
+  const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  dependency_wait();
   float s = 0.f;
-  for (int b = 0; b < A.blocks; ++b) s += A.part[(int64_t)b * 2 * A.N + c];
+  if (c < 2 * A.N) {
+#pragma unroll 8
+    for (int b = group; b < A.blocks; b += kJoinGroups) s += A.part[(int64_t)b * 2 * A.N + c];
+  }
+  part[group][lane] = s;
+  __syncthreads();
+  if (group != 0 || c >= 2 * A.N) return;
+  for (int i = 1; i < kJoinGroups; ++i) s += part[i][lane];
   (c < A.N ? A.dweight[c] : A.dbias[c - A.N]) = s;
 }
 
-constexpr int kMostPartials = 64;
+// How a backward call runs.
+struct NormPlan {
+  int variant;  // of launch_norm_backward; 0: dx and the column sums by separate kernels
+  int blocks;   // partial rows of the column sums
+  RingPlan ring;
+};
 
-inline int norm_partials(int64_t M) { return (int)(M < kMostPartials ? M : kMostPartials); }
+// The same for every call of a size and type, so that the workspace can be sized
+// before the operands are known; rows of 16-byte vectors (`wide`) go through the
+// ring, and so do unaligned fp32 ones, element by element.
+inline NormPlan norm_plan(int size, bool wide, int64_t M, int64_t N) {
+  NormPlan p = {};
+  const int vec = wide ? 16 / size : 1;
+  const int64_t vecs = (N + vec - 1) / vec;
+  const int per[5] = {0, 1, 1, 2, 4}, most[5] = {0, 256, 768, 640, 640}, each[5] = {0, 3, 1, 1, 1};
+  if (vec * size >= 4 && M > 0)
+    for (int v = 1; v < 5 && p.variant == 0; ++v)
+      if (vecs <= per[v] * most[v]) p.variant = v;
+  if (p.variant == 0) {
+    p.blocks = (int)(M < 64 ? M : 64);
+    return p;
+  }
+  const int v = p.variant;
+  p.ring = ring_plan(vecs, per[v], most[v], each[v], 2, vec * size);
+  p.blocks = (int)(M < kSms * p.ring.each ? M : kSms * p.ring.each);
+  return p;
+}
 
-inline size_t norm_workspace(int64_t M, int64_t N) {
-  return ((size_t)norm_partials(M) * 2 * (size_t)N * 4 + 255) / 256 * 256;
+// The larger of the two alignments' needs.
+inline size_t norm_workspace(int size, int64_t M, int64_t N) {
+  const int a = norm_plan(size, true, M, N).blocks, b = norm_plan(size, false, M, N).blocks;
+  return ((size_t)(a > b ? a : b) * 2 * (size_t)N * 4 + 255) / 256 * 256;
+}
+
+template <typename T, int kVec, int kPer, int kThreads, int kBlocks>
+hcmix_status launch_norm_backward_ring(const NormArgs& A, const RingPlan& p, cudaStream_t stream) {
+  const auto kernel = hcmix_norm_backward_kernel<T, kVec, kPer, kThreads, kBlocks>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) !=
+      cudaSuccess)
+    return HCMIX_ERR_CUDA;
+  kernel<<<A.blocks, p.threads, p.smem, stream>>>(A, p.stages);
+  return launched();
+}
+
+// The join may be set up while the kernel before it still runs (it waits for its
+// memory itself).
+inline hcmix_status launch_join(const NormArgs& A, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((2 * A.N + 31) / 32));
+  cfg.blockDim = dim3(32 * kJoinGroups);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, hcmix_norm_join_kernel, A) != cudaSuccess) return HCMIX_ERR_CUDA;
+  return launched();
 }
 
 template <typename T, int kVec>
 hcmix_status launch_norm_backward(NormArgs A, cudaStream_t stream) {
-  if (A.M > 0) {
+  const NormPlan p = norm_plan(sizeof(T), kVec > 1, A.M, A.N);
+  A.blocks = p.blocks;
+  hcmix_status st = HCMIX_OK;
+  if (A.dweight == nullptr || p.variant == 0) {
     const int64_t vecs = (A.N + kVec - 1) / kVec;
     const unsigned threads = vecs >= 256 ? 256 : (unsigned)(vecs + 31) / 32 * 32;
-    hcmix_norm_dx_kernel<T, kVec><<<(unsigned)A.M, threads, 0, stream>>>(A);
+    if (A.M > 0) hcmix_norm_dx_kernel<T, kVec><<<(unsigned)A.M, threads, 0, stream>>>(A);
+    if (A.dweight == nullptr) return launched();
+    const int64_t per = (int64_t)kColumnThreads * kVec;
+    if (p.blocks > 0)
+      hcmix_norm_columns_kernel<T, kVec>
+          <<<dim3((unsigned)((A.N + per - 1) / per), p.blocks), kColumnThreads, 0, stream>>>(A);
+  } else if constexpr (kVec * sizeof(T) >= 4) {
+    switch (p.variant) {
+      case 1: st = launch_norm_backward_ring<T, kVec, 1, 256, 3>(A, p.ring, stream); break;
+      case 2: st = launch_norm_backward_ring<T, kVec, 1, 768, 1>(A, p.ring, stream); break;
+      case 3: st = launch_norm_backward_ring<T, kVec, 2, 640, 1>(A, p.ring, stream); break;
+      default: st = launch_norm_backward_ring<T, kVec, 4, 640, 1>(A, p.ring, stream); break;
+    }
   }
-  if (A.dweight == nullptr) return launched();
-  A.blocks = norm_partials(A.M);
-  const int64_t per = (int64_t)kColumnThreads * kVec;
-  if (A.blocks > 0)
-    hcmix_norm_columns_kernel<T, kVec>
-        <<<dim3((unsigned)((A.N + per - 1) / per), A.blocks), kColumnThreads, 0, stream>>>(A);
-  hcmix_norm_join_kernel<<<(unsigned)((2 * A.N + 255) / 256), 256, 0, stream>>>(A);
-  return launched();
+  if (st != HCMIX_OK) return st;
+  st = launched();
+  return st == HCMIX_OK ? launch_join(A, stream) : st;
 }
 
 inline hcmix_status run_norm_backward(const NormArgs& A, hcmix_type type, cudaStream_t stream) {

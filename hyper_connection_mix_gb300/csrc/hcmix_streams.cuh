@@ -32,8 +32,7 @@ __global__ void __launch_bounds__(256) hcmix_collapse_kernel(const StreamsArgs A
     float v[kVec];
     load_f32<T, kVec>(x + i * A.D, v);
     const float w = A.pre[row * kStreams + i];
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) h[e] = fmaf(w, v[e], h[e]);
+    vfma(h, w, v, h);
   }
   store_f32<T, kVec>(static_cast<T*>(A.out) + row * A.D + c, h);
 }
@@ -53,56 +52,61 @@ __global__ void __launch_bounds__(256) hcmix_expand_kernel(const StreamsArgs A) 
   for (int i = 0; i < kStreams; ++i) {
     const float p = A.post[row * kStreams + i];
     float o[kVec];
+    vmul(o, p, y);
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) o[e] = p * y[e];
-#pragma unroll
-    for (int j = 0; j < kStreams; ++j) {
-      const float w = comb[i * kStreams + j];
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) o[e] = fmaf(w, v[j][e], o[e]);
-    }
+    for (int j = 0; j < kStreams; ++j) vfma(o, comb[i * kStreams + j], v[j], o);
     store_f32<T, kVec>(static_cast<T*>(A.out) + row * kStreams * A.D + i * A.D + c, o);
   }
 }
 
 // One block a row: the row's four dot products need all of its columns.
 template <typename T, int kVec>
-__global__ void __launch_bounds__(1024) hcmix_collapse_backward_kernel(const StreamsArgs A) {
+__global__ void __launch_bounds__(256) hcmix_collapse_backward_kernel(const StreamsArgs A) {
   __shared__ float part[kStreams * 32];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
   const T* g = static_cast<const T*>(A.g) + row * A.g_stride;
+  const T* add = static_cast<const T*>(A.add) + row * A.add_stride;
   T* dx = static_cast<T*>(A.out) + row * kStreams * A.D;
-  float pre[kStreams], dot[kStreams] = {};
+  float pre[kStreams];
+  Acc dot[kStreams];
 #pragma unroll
   for (int i = 0; i < kStreams; ++i) pre[i] = A.pre[row * kStreams + i];
   for (int64_t c = (int64_t)threadIdx.x * kVec; c < A.D; c += blockDim.x * kVec) {
+    Packed<T, kVec> px[kStreams], pa[kStreams];
+    const Packed<T, kVec> pg = load_vec<T, kVec>(g + c);
+#pragma unroll
+    for (int i = 0; i < kStreams; ++i) px[i] = load_vec<T, kVec>(x + i * A.D + c);
+    if (A.add != nullptr) {
+#pragma unroll
+      for (int i = 0; i < kStreams; ++i) pa[i] = load_vec<T, kVec>(add + i * A.D + c);
+    }
     float dh[kVec];
-    load_f32<T, kVec>(g + c, dh);
+    pg.unpack(dh);
 #pragma unroll
     for (int i = 0; i < kStreams; ++i) {
-      float v[kVec], d[kVec] = {};
-      load_f32<T, kVec>(x + i * A.D + c, v);
-      if (A.add != nullptr)
-        load_f32<T, kVec>(static_cast<const T*>(A.add) + row * A.add_stride + i * A.D + c, d);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        dot[i] = fmaf(dh[e], v[e], dot[i]);
-        d[e] = fmaf(pre[i], dh[e], d[e]);
+      float v[kVec], d[kVec];
+      px[i].unpack(v);
+      dot[i].add(dh, v);
+      if (A.add != nullptr) {
+        pa[i].unpack(d);
+        vfma(d, pre[i], dh, d);
+      } else {
+        vmul(d, pre[i], dh);
       }
       store_f32<T, kVec>(dx + i * A.D + c, d);
     }
   }
-  block_sum<kStreams>(dot, part);
-  if (threadIdx.x == 0) {
+  float sums[kStreams];
 #pragma unroll
-    for (int i = 0; i < kStreams; ++i) A.dpre[row * kStreams + i] = dot[i];
-  }
+  for (int i = 0; i < kStreams; ++i) sums[i] = dot[i].sum();
+  const float total = block_sums<kStreams>(sums, part);
+  if (threadIdx.x < kStreams) A.dpre[row * kStreams + threadIdx.x] = total;
 }
 
 // One block a row, as above; 4 + 16 dot products.
 template <typename T, int kVec>
-__global__ void __launch_bounds__(512) hcmix_expand_backward_kernel(const StreamsArgs A) {
+__global__ void __launch_bounds__(256, 2) hcmix_expand_backward_kernel(const StreamsArgs A) {
   constexpr int kDots = kStreams + kStreams * kStreams;
   __shared__ float part[kDots * 32];
   const int64_t row = blockIdx.x;
@@ -111,7 +115,8 @@ __global__ void __launch_bounds__(512) hcmix_expand_backward_kernel(const Stream
   const T* g = static_cast<const T*>(A.g) + row * A.g_stride;
   T* dx = static_cast<T*>(A.out) + row * kStreams * A.D;
   T* dy = static_cast<T*>(A.dy) + row * A.D;
-  float post[kStreams], comb[kStreams][kStreams], dot[kDots] = {};
+  float post[kStreams], comb[kStreams][kStreams];
+  Acc dot[kDots];
 #pragma unroll
   for (int i = 0; i < kStreams; ++i) {
     post[i] = A.post[row * kStreams + i];
@@ -120,44 +125,39 @@ __global__ void __launch_bounds__(512) hcmix_expand_backward_kernel(const Stream
       comb[i][j] = A.comb[(row * kStreams + i) * kStreams + j];
   }
   for (int64_t c = (int64_t)threadIdx.x * kVec; c < A.D; c += blockDim.x * kVec) {
-    float d[kStreams][kVec], v[kVec], o[kVec];
+    Packed<T, kVec> pg[kStreams], px[kStreams];
 #pragma unroll
-    for (int i = 0; i < kStreams; ++i) load_f32<T, kVec>(g + i * A.D + c, d[i]);
-    load_f32<T, kVec>(y + c, v);
+    for (int i = 0; i < kStreams; ++i) pg[i] = load_vec<T, kVec>(g + i * A.D + c);
+    const Packed<T, kVec> py = load_vec<T, kVec>(y + c);
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      o[e] = 0.f;
+    for (int i = 0; i < kStreams; ++i) px[i] = load_vec<T, kVec>(x + i * A.D + c);
+    float d[kStreams][kVec], v[kVec], o[kVec] = {};
+    py.unpack(v);
 #pragma unroll
-      for (int i = 0; i < kStreams; ++i) {
-        o[e] = fmaf(post[i], d[i][e], o[e]);
-        dot[i] = fmaf(d[i][e], v[e], dot[i]);
-      }
+    for (int i = 0; i < kStreams; ++i) {
+      pg[i].unpack(d[i]);
+      vfma(o, post[i], d[i], o);
+      dot[i].add(d[i], v);
     }
     store_f32<T, kVec>(dy + c, o);
 #pragma unroll
     for (int j = 0; j < kStreams; ++j) {
-      load_f32<T, kVec>(x + j * A.D + c, v);
+      px[j].unpack(v);
+      vmul(o, comb[0][j], d[0]);
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        o[e] = 0.f;
+      for (int i = 1; i < kStreams; ++i) vfma(o, comb[i][j], d[i], o);
 #pragma unroll
-        for (int i = 0; i < kStreams; ++i) {
-          o[e] = fmaf(comb[i][j], d[i][e], o[e]);
-          dot[kStreams + i * kStreams + j] =
-              fmaf(d[i][e], v[e], dot[kStreams + i * kStreams + j]);
-        }
-      }
+      for (int i = 0; i < kStreams; ++i) dot[kStreams + i * kStreams + j].add(d[i], v);
       store_f32<T, kVec>(dx + j * A.D + c, o);
     }
   }
-  block_sum<kDots>(dot, part);
-  if (threadIdx.x == 0) {
+  float sums[kDots];
 #pragma unroll
-    for (int i = 0; i < kStreams; ++i) A.dpost[row * kStreams + i] = dot[i];
-#pragma unroll
-    for (int i = 0; i < kStreams * kStreams; ++i)
-      A.dcomb[row * kStreams * kStreams + i] = dot[kStreams + i];
-  }
+  for (int i = 0; i < kDots; ++i) sums[i] = dot[i].sum();
+  const float total = block_sums<kDots>(sums, part);
+  const int t = threadIdx.x;
+  if (t < kStreams) A.dpost[row * kStreams + t] = total;
+  else if (t < kDots) A.dcomb[row * kStreams * kStreams + t - kStreams] = total;
 }
 
 enum class StreamsOp { kCollapse, kExpand, kCollapseBackward, kExpandBackward };
@@ -176,7 +176,9 @@ hcmix_status launch_streams(StreamsOp op, StreamsArgs A, cudaStream_t stream) {
       hcmix_expand_kernel<T, kVec><<<(unsigned)blocks, threads, 0, stream>>>(A);
     return launched();
   }
-  const int threads = vecs >= 256 ? 256 : (int)(vecs + 31) / 32 * 32;
+  // as many equal steps through the row as blocks of 256 threads need
+  const int64_t steps = (vecs + 255) / 256;
+  const int threads = (int)((vecs + steps - 1) / steps + 31) / 32 * 32;
   if (op == StreamsOp::kCollapseBackward)
     hcmix_collapse_backward_kernel<T, kVec><<<(unsigned)A.M, threads, 0, stream>>>(A);
   else

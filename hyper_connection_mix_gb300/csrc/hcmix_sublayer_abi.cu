@@ -103,7 +103,7 @@ hcmix_status hc_mix_layer_norm(const void* x, int64_t x_stride, hcmix_type type,
 
 size_t hc_mix_layer_norm_workspace_bytes(hcmix_type type, int64_t M, int64_t N) {
   if (check_shape(M, N) != HCMIX_OK || !valid_type(type)) return 0;
-  return norm_workspace(M, N);
+  return norm_workspace(size_of(type), M, N);
 }
 
 hcmix_status hc_mix_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x,
@@ -126,7 +126,7 @@ hcmix_status hc_mix_layer_norm_backward(const void* dy, int64_t dy_stride, const
   }
   if (dweight != nullptr) {
     if (!aligned(dweight, 4) || !aligned(dbias, 4)) return HCMIX_ERR_ALIGNMENT;
-    const size_t need = norm_workspace(M, N);
+    const size_t need = norm_workspace(size_of(type), M, N);
     if (need > 0) {
       if (workspace == nullptr) return HCMIX_ERR_INVALID_ARG;
       if (!aligned(workspace, 256)) return HCMIX_ERR_ALIGNMENT;

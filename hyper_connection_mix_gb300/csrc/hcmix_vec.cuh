@@ -42,25 +42,198 @@ __device__ __forceinline__ __half from_f32<__half>(float v) {
 template <typename T>
 constexpr int kWide = 16 / (int)sizeof(T);
 
+// Two elements of a 16-bit type and their values.
+__device__ __forceinline__ float2 pair_to_f32(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+__device__ __forceinline__ float2 pair_to_f32(__half2 v) { return __half22float2(v); }
+__device__ __forceinline__ void pair_from_f32(__nv_bfloat162& p, float a, float b) {
+  p = __floats2bfloat162_rn(a, b);
+}
+__device__ __forceinline__ void pair_from_f32(__half2& p, float a, float b) {
+  p = __floats2half2_rn(a, b);
+}
+template <typename T>
+struct PairOf;
+template <>
+struct PairOf<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+};
+template <>
+struct PairOf<__half> {
+  using type = __half2;
+};
+
 // kVec elements as they lie in memory, and their values.
 template <typename T, int kVec>
 struct alignas(kVec * sizeof(T)) Packed {
   T e[kVec];
   __device__ __forceinline__ void unpack(float (&v)[kVec]) const {
+    if constexpr (sizeof(T) == 2 && kVec % 2 == 0) {
+      using P = typename PairOf<T>::type;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = to_f32(e[i]);
+      for (int i = 0; i < kVec; i += 2) {
+        const float2 f = pair_to_f32(reinterpret_cast<const P*>(e)[i / 2]);
+        v[i] = f.x;
+        v[i + 1] = f.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] = to_f32(e[i]);
+    }
   }
   __device__ __forceinline__ void pack(const float (&v)[kVec]) {
+    if constexpr (sizeof(T) == 2 && kVec % 2 == 0) {
+      using P = typename PairOf<T>::type;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) e[i] = from_f32<T>(v[i]);
+      for (int i = 0; i < kVec; i += 2)
+        pair_from_f32(reinterpret_cast<P*>(e)[i / 2], v[i], v[i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) e[i] = from_f32<T>(v[i]);
+    }
   }
 };
 
+// Elementwise arithmetic on vectors, two fp32 at a time where there are two.
+template <int N>
+__device__ __forceinline__ void vfma(float (&d)[N], const float (&a)[N], const float (&b)[N],
+                                     const float (&c)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 r = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]),
+                                  make_float2(c[i], c[i + 1]));
+      d[i] = r.x;
+      d[i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = fmaf(a[i], b[i], c[i]);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void vfma(float (&d)[N], float a, const float (&b)[N],
+                                     const float (&c)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 r = __ffma2_rn(make_float2(a, a), make_float2(b[i], b[i + 1]),
+                                  make_float2(c[i], c[i + 1]));
+      d[i] = r.x;
+      d[i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = fmaf(a, b[i], c[i]);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void vmul(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 r = __fmul2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+      d[i] = r.x;
+      d[i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = a[i] * b[i];
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void vmul(float (&d)[N], float a, const float (&b)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 r = __fmul2_rn(make_float2(a, a), make_float2(b[i], b[i + 1]));
+      d[i] = r.x;
+      d[i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = a * b[i];
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void vadd(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 r = __fadd2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+      d[i] = r.x;
+      d[i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = a[i] + b[i];
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void vadd(float (&d)[N], float a, const float (&b)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 r = __fadd2_rn(make_float2(a, a), make_float2(b[i], b[i + 1]));
+      d[i] = r.x;
+      d[i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = a + b[i];
+  }
+}
+
+// Sums over vectors run in two chains, the elements' parities.
+struct Acc {
+  float v[2] = {0.f, 0.f};
+  template <int N>
+  __device__ __forceinline__ void add(const float (&a)[N]) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float2 r = __fadd2_rn(make_float2(v[0], v[1]), make_float2(a[i], a[i + 1]));
+        v[0] = r.x;
+        v[1] = r.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[0] += a[i];
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void add(const float (&a)[N], const float (&b)[N]) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float2 r = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]),
+                                    make_float2(v[0], v[1]));
+        v[0] = r.x;
+        v[1] = r.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[0] = fmaf(a[i], b[i], v[0]);
+    }
+  }
+  __device__ __forceinline__ float sum() const { return v[0] + v[1]; }
+};
+
+// Streamed operands are read once and not kept in L1, which is left to what every
+// row uses (weights, coefficients).
 template <typename T, int kVec>
 __device__ __forceinline__ Packed<T, kVec> load_vec(const T* p) {
   Packed<T, kVec> r;
   if constexpr (sizeof(T) * kVec == 16) {
-    *reinterpret_cast<uint4*>(&r) = *reinterpret_cast<const uint4*>(p);
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    *reinterpret_cast<uint4*>(&r) = v;
   } else {
     r = *reinterpret_cast<const Packed<T, kVec>*>(p);
   }
@@ -92,11 +265,32 @@ __device__ __forceinline__ void store_f32(T* p, const float (&v)[kVec]) {
 template <typename T, int kVec>
 __device__ __forceinline__ void load_param(const void* p, bool p32, int64_t at, float (&v)[kVec]) {
   if (p32) {
+    const float* f = static_cast<const float*>(p) + at;
+    if (kVec % 4 == 0 && reinterpret_cast<uintptr_t>(f) % 16 == 0) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = static_cast<const float*>(p)[at + i];
+      for (int i = 0; i < kVec; i += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(f + i);
+        v[i] = q.x;
+        if constexpr (kVec % 4 == 0) {
+          v[i + 1] = q.y;
+          v[i + 2] = q.z;
+          v[i + 3] = q.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] = f[i];
+    }
   } else {
+    const T* t = static_cast<const T*>(p) + at;
+    if (kVec > 1 && reinterpret_cast<uintptr_t>(t) % 16 == 0) {
+      Packed<T, kVec> r;
+      r = *reinterpret_cast<const Packed<T, kVec>*>(t);
+      r.unpack(v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = to_f32(static_cast<const T*>(p)[at + i]);
+      for (int i = 0; i < kVec; ++i) v[i] = to_f32(t[i]);
+    }
   }
 }
 
@@ -106,21 +300,130 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sums of kN values over the block, in every thread.  The block is whole
-// warps; `part` holds kN * 32 floats and is free again at the next barrier.
+// Warp sums of kN <= 32 values at once.  At each step a lane keeps one half of
+// the values, adding the other lane's, and gives the other half away, so kN values
+// take about kN shuffles instead of 5 kN.  Lane l ends with the sum of value
+// warp_sums_index(l); kN is padded to the next power of two.
+template <int kN>
+constexpr int kPadded = kN <= 1 ? 1 : 2 * kPadded<(kN + 1) / 2>;
+template <>
+constexpr int kPadded<1> = 1;
+
+template <int kN>
+__device__ __forceinline__ float warp_sums(const float (&in)[kN]) {
+  constexpr int kP = kPadded<kN>;
+  float v[kP];
+#pragma unroll
+  for (int i = 0; i < kP; ++i) v[i] = i < kN ? in[i] : 0.f;
+  const int lane = threadIdx.x % 32;
+  int o = 16;
+#pragma unroll
+  for (int n = kP / 2; n > 0; n /= 2, o /= 2) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool upper = lane & o;
+      const float keep = upper ? v[i + n] : v[i], give = upper ? v[i] : v[i + n];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+#pragma unroll
+  for (; o > 0; o /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
+}
+
+// The value whose sum lane l holds: its top log2(kP) bits, the first step's bit
+// the value's highest.
+template <int kN>
+__device__ __forceinline__ int warp_sums_index(int lane) {
+  constexpr int kP = kPadded<kN>;
+  return lane / (32 / kP);
+}
+
+// Sums of kN values over the block: thread i < kN returns value i's (the others
+// nothing of use).  The block is whole warps; `part` holds 32 * kN floats.
+template <int kN>
+__device__ __forceinline__ float block_sums(const float (&v)[kN], float* part) {
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int kEach = 32 / kPadded<kN>;  // lanes that hold the same sum
+  const float s = warp_sums<kN>(v);
+  const int i = warp_sums_index<kN>(lane);
+  if (lane % kEach == 0 && i < kN) part[warp * kN + i] = s;
+  __syncthreads();
+  float t = 0.f;
+  if (threadIdx.x < kN)
+    for (int w = 0; w < warps; ++w) t += part[w * kN + threadIdx.x];
+  return t;
+}
+
+// Sums of kN (1 or 2) values over the block, in every thread.  `part` holds
+// 32 * kN floats and is free again at the next barrier.
 template <int kN>
 __device__ __forceinline__ void block_sum(float (&v)[kN], float* part) {
-#pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = warp_sum(v[i]);
+  static_assert(kN <= 2, "");
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (warps == 1) return;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) part[i * 32 + warp] = v[i];
+  const float s = warp_sums<kN>(v);
+  if (warps == 1) {
+    v[0] = __shfl_sync(0xffffffffu, s, 0);
+    if constexpr (kN == 2) v[1] = __shfl_sync(0xffffffffu, s, 16);
+    return;
   }
+  if (lane % (32 / kN) == 0) part[(lane / 16) * 32 + warp] = s;
   __syncthreads();
+  if constexpr (kN == 1) {
+    v[0] = warp_sum(lane < warps ? part[lane] : 0.f);
+  } else {
+    // half a warp adds up each value
+    const float* mine = part + (lane & 16) * 2;
+    const int l = lane & 15;
+    float t = l < warps ? mine[l] : 0.f;
+    if (l + 16 < warps) t += mine[l + 16];
 #pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = warp_sum(lane < warps ? part[i * 32 + lane] : 0.f);
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    v[0] = __shfl_sync(0xffffffffu, t, 0);
+    v[1] = __shfl_sync(0xffffffffu, t, 16);
+  }
+}
+
+// ---- asynchronous copies into shared memory, completed for the copying thread
+// by async_wait; one vector each
+
+template <typename V, typename T>
+__device__ __forceinline__ void async_copy(V* dst, const T* src) {
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (sizeof(V) == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(src), "n"(sizeof(V))
+                 : "memory");
+}
+
+__device__ __forceinline__ void async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Waits until at most stages - 1 of the thread's newest groups are in flight.
+__device__ __forceinline__ void async_wait(int stages) {
+  switch (stages) {
+    case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 7: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+  }
+}
+
+// ---- programmatic dependent launch: the next kernel's blocks may start once all
+// of this grid's have called launch_dependents (or ended); dependency_wait, in
+// that kernel, returns when this grid has ended and its memory can be seen.
+
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ void dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---- host side
