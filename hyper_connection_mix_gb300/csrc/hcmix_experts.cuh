@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(256) hcmix_expert_combine_backward_kernel(cons
       store_f32<T, kVec>(dys + c, g);
     }
   }
-  block_sum<1>(dot, part);
+  block_sums_all<1>(dot, part);
   if (threadIdx.x == 0 && pair < pairs) A.dweights[pair] = dot[0];
   zero_tail<T, kVec>(A, pair, gridDim.x, c0, step);
 }

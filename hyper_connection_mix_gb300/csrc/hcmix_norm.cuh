@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) hcmix_norm_kernel(const NormArgs A) 
     for (int e = 0; e < kVec; ++e) sum[0] += v[k][e];
   }
   const float inv = 1.f / (float)A.N;
-  block_sum<1>(sum, part[0]);
+  block_sums_all<1>(sum, part[0]);
   const float mean = sum[0] * inv;
   float sq[1] = {0.f};
 #pragma unroll
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) hcmix_norm_kernel(const NormArgs A) 
       for (int e = 0; e < kVec; ++e) sq[0] = fmaf(v[k][e] - mean, v[k][e] - mean, sq[0]);
     }
   }
-  block_sum<1>(sq, part[1]);
+  block_sums_all<1>(sq, part[1]);
   const float rstd = 1.f / sqrtf(sq[0] * inv + A.eps);
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
@@ -159,14 +159,14 @@ __global__ void __launch_bounds__(512) hcmix_norm_wide_kernel(const NormArgs A) 
     for (int e = 0; e < kVec; ++e) sum[0] += v[e];
   }
   const float inv = 1.f / (float)A.N;
-  block_sum<1>(sum, part[0]);
+  block_sums_all<1>(sum, part[0]);
   const float mean = sum[0] * inv;
   for (int64_t c = c0; c < A.N; c += step) {
     norm_source<T, kVec, kCollapse>(A, x, pre, c, v);
 #pragma unroll
     for (int e = 0; e < kVec; ++e) sq[0] = fmaf(v[e] - mean, v[e] - mean, sq[0]);
   }
-  block_sum<1>(sq, part[1]);
+  block_sums_all<1>(sq, part[1]);
   const float rstd = 1.f / sqrtf(sq[0] * inv + A.eps);
   for (int64_t c = c0; c < A.N; c += step) {
     norm_source<T, kVec, kCollapse>(A, x, pre, c, v);
@@ -179,55 +179,63 @@ __global__ void __launch_bounds__(512) hcmix_norm_wide_kernel(const NormArgs A) 
   }
 }
 
-// Resident blocks that take rows b, b + blocks, ... through a ring of `stages`
-// rows in shared memory.  Each thread copies the vectors that it will read itself
-// (cp.async), so no barrier stands between the copies and their use, and what
-// belongs to its columns (weight, bias, sums over rows) stays in registers.
-// kRows: source rows of a stage (streams, or x and dy), source(i) the first
-// element of the i-th for a row, `width` elements each.
-template <typename T, int kVec, int kPer, int kRows>
+// Resident blocks take groups of rows b, b + blocks, ... through a ring of
+// kStages groups in shared memory.  Each thread copies the vectors that it will
+// read itself (cp.async), so no barrier stands between the copies and their use,
+// and what belongs to its columns (weight, bias, sums over rows) stays in
+// registers.  A group is kRows source rows (streams; x and dy of several rows).
+template <typename T, int kVec, int kPer, int kRows, int kStages>
 struct Ring {
   using V = Packed<T, kVec>;
-  V* mine;
-  int stages, stage;
-  __device__ __forceinline__ Ring(unsigned char* smem, int n)
-      : mine(reinterpret_cast<V*>(smem) + threadIdx.x), stages(n), stage(0) {}
-  static __device__ __forceinline__ int64_t column(int k) {
-    return ((int64_t)k * blockDim.x + threadIdx.x) * kVec;
-  }
-  __device__ __forceinline__ V* at(int s, int i, int k) const {
-    return mine + ((s * kRows + i) * kPer + k) * (int)blockDim.x;
-  }
-  // Starts the copy of a row into stage s; `valid` false: an empty group, which
-  // keeps the count.
-  template <typename Source>
-  __device__ __forceinline__ void fetch(bool valid, int s, int64_t width, Source&& source) const {
-    if (valid) {
+  unsigned char* mine;
+  int pitch;  // bytes from one of the thread's vectors to its next
+  int at;     // byte offset of the stage that is read
+  int columns, first, step;  // the thread's columns: first + k * step, below columns
+  __device__ __forceinline__ Ring(unsigned char* smem, int64_t width)
+      : mine(smem + threadIdx.x * sizeof(V)),
+        pitch(blockDim.x * sizeof(V)),
+        at(0),
+        columns((int)width),
+        first(threadIdx.x * kVec),
+        step(blockDim.x * kVec) {}
+  __device__ __forceinline__ bool has(int k) const { return first + k * step < columns; }
+  __device__ __forceinline__ int column(int k) const { return first + k * step; }
+  __device__ __forceinline__ int group() const { return kRows * kPer * pitch; }
+  // Starts the copy of source row i, given its first element, into the stage at
+  // byte offset `to`.
+  __device__ __forceinline__ void copy(int to, int i, const T* row) const {
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const T* from = source(i);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-          if (column(k) < width) async_copy(at(s, i, k), from + column(k));
-      }
-    }
-    async_commit();
+    for (int k = 0; k < kPer; ++k)
+      if (has(k))
+        async_copy(reinterpret_cast<V*>(mine + to + (i * kPer + k) * pitch), row + column(k));
   }
-  // The stage to refill while this row is worked on: the one read a row ago.
-  __device__ __forceinline__ int refill() const { return stage == 0 ? stages - 1 : stage - 1; }
-  __device__ __forceinline__ void wait() const { async_wait(stages); }
-  __device__ __forceinline__ const V& read(int i, int k) const { return *at(stage, i, k); }
+  // The stage to refill while this group is worked on: the one read a group ago.
+  __device__ __forceinline__ int refill() const {
+    return at == 0 ? (kStages - 1) * group() : at - group();
+  }
+  __device__ __forceinline__ const V& read(int i, int k) const {
+    return *reinterpret_cast<const V*>(mine + at + (i * kPer + k) * pitch);
+  }
   __device__ __forceinline__ void advance() {
-    if (++stage == stages) stage = 0;
+    at += group();
+    if (at == kStages * group()) at = 0;
   }
 };
 
 constexpr int kSms = 152;
-constexpr size_t kRingBytes = 200 * 1024;  // of all blocks of a multiprocessor
+
+// Stages that fit a multiprocessor with kBlocks blocks of kThreads threads: 200 KB,
+// from two to eight.
+template <int kRows, int kPer, int kThreads, int kBlocks>
+constexpr int kRingFit = 200 * 1024 / (kBlocks * kRows * kPer * kThreads * 16);
+template <int kRows, int kPer, int kThreads, int kBlocks>
+constexpr int kRingStages = kRingFit<kRows, kPer, kThreads, kBlocks> > 8   ? 8
+                            : kRingFit<kRows, kPer, kThreads, kBlocks> < 2 ? 2
+                                : kRingFit<kRows, kPer, kThreads, kBlocks>;
 
 struct RingPlan {
-  int threads, stages, each;  // each: blocks a multiprocessor
-  size_t smem;
+  int threads, each;  // each: blocks a multiprocessor
+  size_t stage;       // bytes
 };
 
 // `each` blocks of `most` threads fit a multiprocessor; smaller ones in proportion.
@@ -236,46 +244,50 @@ inline RingPlan ring_plan(int64_t vecs, int per, int most, int each, int rows, i
   p.threads = (int)((vecs + per - 1) / per + 31) / 32 * 32;
   p.each = each * most / p.threads;
   p.each = p.each > 16 ? 16 : p.each;
-  const size_t stage = (size_t)rows * per * p.threads * vec_bytes;
-  p.stages = (int)(kRingBytes / p.each / stage);
-  p.stages = p.stages > 8 ? 8 : p.stages < 2 ? 2 : p.stages;
-  p.smem = p.stages * stage;
+  p.stage = (size_t)rows * per * p.threads * vec_bytes;
   return p;
 }
 
 // The norm of 16-byte vectors through the ring.
 template <typename T, int kVec, int kPer, int kThreads, int kBlocks, bool kCollapse>
-__global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_ring_kernel(const NormArgs A,
-                                                                            int stages) {
+__global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_ring_kernel(const NormArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float part[2][32];
   constexpr int kRows = kCollapse ? kStreams : 1;
-  using R = Ring<T, kVec, kPer, kRows>;
-  R ring(smem, stages);
-  const auto fetch = [&](int64_t row, int s) {
-    ring.fetch(row < A.M, s, A.N,
-               [&](int i) { return static_cast<const T*>(A.x) + row * A.x_stride + i * A.N; });
-  };
+  constexpr int kStages = kRingStages<kRows, kPer, kThreads, kBlocks>;
+  Ring<T, kVec, kPer, kRows, kStages> ring(smem, A.N);
+  const T* from = static_cast<const T*>(A.x) + blockIdx.x * A.x_stride;
+  const int64_t jump = gridDim.x * A.x_stride;
   int64_t next = blockIdx.x;
-  for (int s = 0; s < stages - 1; ++s, next += gridDim.x) fetch(next, s);
+  const auto fetch = [&](int to) {
+    if (next < A.M) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) ring.copy(to, i, from + i * A.N);
+    }
+    async_commit();  // an empty group past the last row keeps the count
+    next += gridDim.x;
+    from += jump;
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) fetch(s * ring.group());
   float w[kPer][kVec], b[kPer][kVec];
 #pragma unroll
   for (int k = 0; k < kPer; ++k)
-    if (R::column(k) < A.N) norm_params<T, kVec>(A, R::column(k), w[k], b[k]);
+    if (ring.has(k)) norm_params<T, kVec>(A, ring.column(k), w[k], b[k]);
   const float inv = 1.f / (float)A.N;
-  for (int64_t row = blockIdx.x; row < A.M; row += gridDim.x, next += gridDim.x) {
+  for (int64_t row = blockIdx.x; row < A.M; row += gridDim.x) {
     float pre[kStreams] = {};
     if constexpr (kCollapse) {
 #pragma unroll
       for (int i = 0; i < kStreams; ++i) pre[i] = A.pre[row * kStreams + i];
     }
-    fetch(next, ring.refill());
-    ring.wait();
+    fetch(ring.refill());
+    async_wait<kStages - 1>();
     float v[kPer][kVec];
     Acc acc;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      if (R::column(k) < A.N) {
+      if (ring.has(k)) {
         NormSource<T, kVec, kCollapse> raw;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) raw.s[i] = ring.read(i, k);
@@ -284,27 +296,27 @@ __global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_ring_kernel(cons
       }
     }
     float sum[1] = {acc.sum()};
-    block_sum<1>(sum, part[0]);
+    block_sums_all<1>(sum, part[0]);
     const float mean = sum[0] * inv;
     Acc square;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      if (R::column(k) < A.N) {
+      if (ring.has(k)) {
         if (kCollapse && A.h != nullptr)
-          store_f32<T, kVec>(static_cast<T*>(A.h) + row * A.N + R::column(k), v[k]);
+          store_f32<T, kVec>(static_cast<T*>(A.h) + row * A.N + ring.column(k), v[k]);
         vadd(v[k], -mean, v[k]);
         square.add(v[k], v[k]);
       }
     }
     float sq[1] = {square.sum()};
-    block_sum<1>(sq, part[1]);
+    block_sums_all<1>(sq, part[1]);
     const float rstd = 1.f / sqrtf(sq[0] * inv + A.eps);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      if (R::column(k) < A.N) {
+      if (ring.has(k)) {
         vmul(v[k], rstd, v[k]);
         vfma(v[k], v[k], w[k], b[k]);
-        store_f32<T, kVec>(static_cast<T*>(A.y) + row * A.N + R::column(k), v[k]);
+        store_f32<T, kVec>(static_cast<T*>(A.y) + row * A.N + ring.column(k), v[k]);
       }
     }
     if (threadIdx.x == 0) {
@@ -317,14 +329,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_ring_kernel(cons
 
 template <typename T, int kVec, int kPer, int kThreads, int kBlocks, bool kCollapse>
 hcmix_status launch_norm_ring(const NormArgs& A, int64_t vecs, cudaStream_t stream) {
-  const RingPlan p =
-      ring_plan(vecs, kPer, kThreads, kBlocks, kCollapse ? kStreams : 1, kVec * (int)sizeof(T));
+  constexpr int kRows = kCollapse ? kStreams : 1;
+  const RingPlan p = ring_plan(vecs, kPer, kThreads, kBlocks, kRows, kVec * (int)sizeof(T));
+  const size_t smem = kRingStages<kRows, kPer, kThreads, kBlocks> * p.stage;
   const auto kernel = hcmix_norm_ring_kernel<T, kVec, kPer, kThreads, kBlocks, kCollapse>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) !=
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return HCMIX_ERR_CUDA;
   const int64_t blocks = A.M < kSms * p.each ? A.M : kSms * p.each;
-  kernel<<<(unsigned)blocks, p.threads, p.smem, stream>>>(A, p.stages);
+  kernel<<<(unsigned)blocks, p.threads, smem, stream>>>(A);
   return launched();
 }
 
@@ -395,7 +408,7 @@ __global__ void __launch_bounds__(512) hcmix_norm_dx_kernel(const NormArgs A) {
       sum[1] = fmaf(t, (v[e] - mean) * rstd, sum[1]);
     }
   }
-  block_sum<2>(sum, part);
+  block_sums_all<2>(sum, part);
   const float inv = 1.f / (float)A.N;
   const float c1 = sum[0] * inv, c2 = sum[1] * inv;
   for (int64_t c = c0; c < A.N; c += step) {
@@ -438,76 +451,111 @@ __global__ void __launch_bounds__(kColumnThreads) hcmix_norm_columns_kernel(cons
 }
 
 // dx and the partial sums of the weight's and bias's gradient in one pass over x
-// and dy, through the ring; the one barrier a row is that of the row's two sums.
-// A thread keeps dweight and dbias of its columns in registers.  With one vector
-// a thread (kPer 1) weight, (x - mean) rstd and dy weight stay there too; with
-// more they are read and worked out again, from L1 and the stage.
-template <typename T, int kVec, int kPer, int kThreads, int kBlocks>
-__global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_backward_kernel(const NormArgs A,
-                                                                                int stages) {
+// and dy, through the ring; a block works on kGroup rows at a time, with one
+// barrier for all their sums.  A thread keeps dweight and dbias of its columns in
+// registers.  With one vector a thread (kPer 1) weight, (x - mean) rstd and
+// dy weight stay there too; with more they are read and worked out again, from
+// L1 and the stage.
+template <typename T, int kVec, int kPer, int kGroup, int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_backward_kernel(const NormArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float part[2][2 * 32];
+  __shared__ float part[2][2 * kGroup * 32];
   constexpr bool kKeep = kPer == 1;
-  using R = Ring<T, kVec, kPer, 2>;
-  R ring(smem, stages);
-  const auto fetch = [&](int64_t row, int s) {
-    ring.fetch(row < A.M, s, A.N, [&](int i) {
-      return i == 0 ? static_cast<const T*>(A.x) + row * A.x_stride
-                    : static_cast<const T*>(A.dy) + row * A.dy_stride;
-    });
+  constexpr int kKept = kKeep ? kGroup : 1;
+  constexpr int kStages = kRingStages<2 * kGroup, kPer, kThreads, kBlocks>;
+  Ring<T, kVec, kPer, 2 * kGroup, kStages> ring(smem, A.N);
+  const T* x = static_cast<const T*>(A.x) + blockIdx.x * kGroup * A.x_stride;
+  const T* dy = static_cast<const T*>(A.dy) + blockIdx.x * kGroup * A.dy_stride;
+  const int64_t x_jump = gridDim.x * kGroup * A.x_stride;
+  const int64_t dy_jump = gridDim.x * kGroup * A.dy_stride;
+  const int M = (int)A.M, jump = gridDim.x * kGroup;
+  int64_t next = blockIdx.x * kGroup;
+  const auto fetch = [&](int to) {
+#pragma unroll
+    for (int r = 0; r < kGroup; ++r) {
+      if (next + r < M) {
+        ring.copy(to, 2 * r, x + r * A.x_stride);
+        ring.copy(to, 2 * r + 1, dy + r * A.dy_stride);
+      }
+    }
+    async_commit();  // an empty group past the last row keeps the count
+    next += jump;
+    x += x_jump;
+    dy += dy_jump;
   };
-  int64_t next = blockIdx.x;
-  for (int s = 0; s < stages - 1; ++s, next += gridDim.x) fetch(next, s);
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) fetch(s * ring.group());
   float dw[kPer][kVec] = {}, db[kPer][kVec] = {}, w[kVec];
   const auto load_weight = [&](int k) {
 #pragma unroll
     for (int e = 0; e < kVec; ++e) w[e] = 1.f;
-    if (A.weight != nullptr && R::column(k) < A.N)
-      load_param<T, kVec>(A.weight, A.p32, R::column(k), w);
+    if (A.weight != nullptr && ring.has(k))
+      load_param<T, kVec>(A.weight, A.p32, ring.column(k), w);
   };
   if (kKeep) load_weight(0);
   const float inv = 1.f / (float)A.N;
   int odd = 0;
-  float next_mean = A.mean[blockIdx.x], next_rstd = A.rstd[blockIdx.x];
-  for (int64_t row = blockIdx.x; row < A.M; row += gridDim.x, next += gridDim.x, odd ^= 1) {
-    const float mean = next_mean, rstd = next_rstd;
-    if (row + gridDim.x < A.M) {
-      next_mean = A.mean[row + gridDim.x];
-      next_rstd = A.rstd[row + gridDim.x];
-    }
-    fetch(next, ring.refill());
-    ring.wait();
-    float xh[kVec], g[kVec], t[kVec];
-    const auto load_row = [&](int k) {
-      ring.read(0, k).unpack(xh);
-      ring.read(1, k).unpack(g);
-      if (!kKeep) load_weight(k);
-      vadd(xh, -mean, xh);
-      vmul(xh, rstd, xh);
-      vmul(t, g, w);
-    };
-    Acc acc[2];
+  float next_mean[kGroup], next_rstd[kGroup];
+  const auto fetch_stats = [&](int64_t row) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (R::column(k) < A.N) {
-        load_row(k);
-        vfma(dw[k], g, xh, dw[k]);
-        vadd(db[k], g, db[k]);
-        acc[0].add(t);
-        acc[1].add(t, xh);
+    for (int r = 0; r < kGroup; ++r) {
+      if (row + r < M) {
+        next_mean[r] = A.mean[row + r];
+        next_rstd[r] = A.rstd[row + r];
       }
     }
-    float sum[2] = {acc[0].sum(), acc[1].sum()};
-    block_sum<2>(sum, part[odd]);  // two rows apart, a barrier lies between the uses
-    const float c1 = sum[0] * inv, c2 = sum[1] * inv;
+  };
+  fetch_stats(next - (int64_t)(kStages - 1) * jump);
+  for (int64_t row = blockIdx.x * kGroup; row < M; row += jump, odd ^= 1) {
+    float mean[kGroup], rstd[kGroup];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (R::column(k) < A.N) {
-        if (!kKeep) load_row(k);
-        vadd(t, -c1, t);
-        vfma(t, -c2, xh, t);
-        vmul(t, rstd, t);
-        store_f32<T, kVec>(static_cast<T*>(A.dx) + row * A.N + R::column(k), t);
+    for (int r = 0; r < kGroup; ++r) mean[r] = next_mean[r], rstd[r] = next_rstd[r];
+    fetch_stats(row + jump);
+    fetch(ring.refill());
+    async_wait<kStages - 1>();
+    float xh[kKept][kVec], t[kKept][kVec], g[kVec];
+    const auto load_row = [&](int r, int k) {
+      const int q = kKeep ? r : 0;
+      ring.read(2 * r, k).unpack(xh[q]);
+      ring.read(2 * r + 1, k).unpack(g);
+      if (!kKeep) load_weight(k);
+      vadd(xh[q], -mean[r], xh[q]);
+      vmul(xh[q], rstd[r], xh[q]);
+      vmul(t[q], g, w);
+    };
+    float sums[2 * kGroup];
+#pragma unroll
+    for (int r = 0; r < kGroup; ++r) {
+      Acc acc[2];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        if (ring.has(k) && row + r < M) {
+          const int q = kKeep ? r : 0;
+          load_row(r, k);
+          vfma(dw[k], g, xh[q], dw[k]);
+          vadd(db[k], g, db[k]);
+          acc[0].add(t[q]);
+          acc[1].add(t[q], xh[q]);
+        }
+      }
+      sums[2 * r] = acc[0].sum();
+      sums[2 * r + 1] = acc[1].sum();
+    }
+    // two groups apart, a barrier lies between the uses of `part`
+    block_sums_all<2 * kGroup>(sums, part[odd]);
+#pragma unroll
+    for (int r = 0; r < kGroup; ++r) {
+      const float c1 = sums[2 * r] * inv, c2 = sums[2 * r + 1] * inv;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        if (ring.has(k) && row + r < M) {
+          const int q = kKeep ? r : 0;
+          if (!kKeep) load_row(r, k);
+          vadd(t[q], -c1, t[q]);
+          vfma(t[q], -c2, xh[q], t[q]);
+          vmul(t[q], rstd[r], t[q]);
+          store_f32<T, kVec>(static_cast<T*>(A.dx) + (row + r) * A.N + ring.column(k), t[q]);
+        }
       }
     }
     ring.advance();
@@ -516,11 +564,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_backward_kernel(
   float* out = A.part + (int64_t)blockIdx.x * 2 * A.N;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    if (R::column(k) < A.N) {
+    if (ring.has(k)) {
+      // the workspace is aligned, and so are whole vectors' columns
+      constexpr int kQuad = kVec % 4 == 0 ? 4 : 1;
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        out[R::column(k) + e] = dw[k][e];
-        out[A.N + R::column(k) + e] = db[k][e];
+      for (int e = 0; e < kVec; e += kQuad) {
+        float q[kQuad], p[kQuad];
+#pragma unroll
+        for (int i = 0; i < kQuad; ++i) q[i] = dw[k][e + i], p[i] = db[k][e + i];
+        store_f32<float, kQuad>(out + ring.column(k) + e, q);
+        store_f32<float, kQuad>(out + A.N + ring.column(k) + e, p);
       }
     }
   }
@@ -561,7 +614,8 @@ inline NormPlan norm_plan(int size, bool wide, int64_t M, int64_t N) {
   NormPlan p = {};
   const int vec = wide ? 16 / size : 1;
   const int64_t vecs = (N + vec - 1) / vec;
-  const int per[5] = {0, 1, 1, 2, 4}, most[5] = {0, 256, 768, 640, 640}, each[5] = {0, 3, 1, 1, 1};
+  const int per[5] = {0, 1, 1, 2, 4}, most[5] = {0, 256, 640, 640, 640}, each[5] = {0, 3, 1, 1, 1};
+  const int group[5] = {0, 2, 2, 1, 1};  // rows at a time
   if (vec * size >= 4 && M > 0)
     for (int v = 1; v < 5 && p.variant == 0; ++v)
       if (vecs <= per[v] * most[v]) p.variant = v;
@@ -570,8 +624,9 @@ inline NormPlan norm_plan(int size, bool wide, int64_t M, int64_t N) {
     return p;
   }
   const int v = p.variant;
-  p.ring = ring_plan(vecs, per[v], most[v], each[v], 2, vec * size);
-  p.blocks = (int)(M < kSms * p.ring.each ? M : kSms * p.ring.each);
+  p.ring = ring_plan(vecs, per[v], most[v], each[v], 2 * group[v], vec * size);
+  const int64_t groups = (M + group[v] - 1) / group[v];
+  p.blocks = (int)(groups < kSms * p.ring.each ? groups : kSms * p.ring.each);
   return p;
 }
 
@@ -581,13 +636,14 @@ inline size_t norm_workspace(int size, int64_t M, int64_t N) {
   return ((size_t)(a > b ? a : b) * 2 * (size_t)N * 4 + 255) / 256 * 256;
 }
 
-template <typename T, int kVec, int kPer, int kThreads, int kBlocks>
+template <typename T, int kVec, int kPer, int kGroup, int kThreads, int kBlocks>
 hcmix_status launch_norm_backward_ring(const NormArgs& A, const RingPlan& p, cudaStream_t stream) {
-  const auto kernel = hcmix_norm_backward_kernel<T, kVec, kPer, kThreads, kBlocks>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) !=
+  const size_t smem = kRingStages<2 * kGroup, kPer, kThreads, kBlocks> * p.stage;
+  const auto kernel = hcmix_norm_backward_kernel<T, kVec, kPer, kGroup, kThreads, kBlocks>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return HCMIX_ERR_CUDA;
-  kernel<<<A.blocks, p.threads, p.smem, stream>>>(A, p.stages);
+  kernel<<<A.blocks, p.threads, smem, stream>>>(A);
   return launched();
 }
 
@@ -623,10 +679,10 @@ hcmix_status launch_norm_backward(NormArgs A, cudaStream_t stream) {
           <<<dim3((unsigned)((A.N + per - 1) / per), p.blocks), kColumnThreads, 0, stream>>>(A);
   } else if constexpr (kVec * sizeof(T) >= 4) {
     switch (p.variant) {
-      case 1: st = launch_norm_backward_ring<T, kVec, 1, 256, 3>(A, p.ring, stream); break;
-      case 2: st = launch_norm_backward_ring<T, kVec, 1, 768, 1>(A, p.ring, stream); break;
-      case 3: st = launch_norm_backward_ring<T, kVec, 2, 640, 1>(A, p.ring, stream); break;
-      default: st = launch_norm_backward_ring<T, kVec, 4, 640, 1>(A, p.ring, stream); break;
+      case 1: st = launch_norm_backward_ring<T, kVec, 1, 2, 256, 3>(A, p.ring, stream); break;
+      case 2: st = launch_norm_backward_ring<T, kVec, 1, 2, 640, 1>(A, p.ring, stream); break;
+      case 3: st = launch_norm_backward_ring<T, kVec, 2, 1, 640, 1>(A, p.ring, stream); break;
+      default: st = launch_norm_backward_ring<T, kVec, 4, 1, 640, 1>(A, p.ring, stream); break;
     }
   }
   if (st != HCMIX_OK) return st;

@@ -355,33 +355,26 @@ __device__ __forceinline__ float block_sums(const float (&v)[kN], float* part) {
   return t;
 }
 
-// Sums of kN (1 or 2) values over the block, in every thread.  `part` holds
-// 32 * kN floats and is free again at the next barrier.
+// Sums of kN values over the block, in every thread, by warp_sums twice: `part`
+// holds 32 * kN floats and is free again at the next barrier.
 template <int kN>
-__device__ __forceinline__ void block_sum(float (&v)[kN], float* part) {
-  static_assert(kN <= 2, "");
+__device__ __forceinline__ void block_sums_all(float (&v)[kN], float* part) {
+  static_assert(kPadded<kN> == kN && kN <= 32, "");
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const float s = warp_sums<kN>(v);
-  if (warps == 1) {
-    v[0] = __shfl_sync(0xffffffffu, s, 0);
-    if constexpr (kN == 2) v[1] = __shfl_sync(0xffffffffu, s, 16);
-    return;
-  }
-  if (lane % (32 / kN) == 0) part[(lane / 16) * 32 + warp] = s;
-  __syncthreads();
-  if constexpr (kN == 1) {
-    v[0] = warp_sum(lane < warps ? part[lane] : 0.f);
-  } else {
-    // half a warp adds up each value
-    const float* mine = part + (lane & 16) * 2;
-    const int l = lane & 15;
-    float t = l < warps ? mine[l] : 0.f;
-    if (l + 16 < warps) t += mine[l + 16];
+  constexpr int kEach = 32 / kN;  // lanes that hold the same sum
+  float s = warp_sums<kN>(v);
+  if (warps > 1) {
+    if (lane % kEach == 0) part[warp * kN + lane / kEach] = s;
+    __syncthreads();
+    // kEach lanes share a value's partials, value i's lanes from i * kEach on
+    const int i = lane / kEach;
+    s = 0.f;
+    for (int w = lane % kEach; w < warps; w += kEach) s += part[w * kN + i];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    v[0] = __shfl_sync(0xffffffffu, t, 0);
-    v[1] = __shfl_sync(0xffffffffu, t, 16);
+    for (int o = kEach / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = __shfl_sync(0xffffffffu, s, i * kEach);
 }
 
 // ---- asynchronous copies into shared memory, completed for the copying thread
@@ -401,17 +394,10 @@ __device__ __forceinline__ void async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// Waits until at most stages - 1 of the thread's newest groups are in flight.
-__device__ __forceinline__ void async_wait(int stages) {
-  switch (stages) {
-    case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    case 6: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    case 7: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-  }
+// Waits until at most kLeft of the thread's newest groups are in flight.
+template <int kLeft>
+__device__ __forceinline__ void async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 // ---- programmatic dependent launch: the next kernel's blocks may start once all
