@@ -12,76 +12,112 @@ namespace sublayer {
 
 struct SortArgs {
   const void* ids;
-  int wide_ids;  // int64
-  int64_t n;     // pairs
+  int64_t n;  // pairs
   int E;
   int32_t *offsets, *slots, *source;
 };
 
 constexpr int kMostExperts = 4096;
 constexpr int kSortCounters = 32 * 1024;  // warps * experts, 128 KB
-constexpr int kSortCluster = 8;
+// Pairs that one block sorts: 512 take it 3.3 us and 1024 4.7 us, a cluster 3.9 us.
+constexpr int64_t kSortAlone = 512;
+// Blocks of the cluster that sorts more.  The scattered stores of source, one sector
+// a pair, are shared out over them: 32768 pairs of 128 experts take 16 blocks 7.7 us
+// (8 blocks, before the loops were rolled, 10.3 us).  Each holds a row of totals for
+// every block, 64 KB in all.
+inline int sort_blocks(int64_t n, int64_t E) { return n <= kSortAlone ? 1 : E <= 1024 ? 16 : 4; }
 
+template <typename Id>
 __device__ __forceinline__ int expert_of(const SortArgs& A, int64_t i) {
-  const int64_t e = A.wide_ids ? static_cast<const int64_t*>(A.ids)[i]
-                               : static_cast<const int32_t*>(A.ids)[i];
-  return e >= 0 && e < A.E ? (int)e : -1;
+  const int64_t e = static_cast<const Id*>(A.ids)[i];
+  return e >= 0 && e < A.E ? (int)e : A.E;  // A.E: of none
 }
 
-inline int sort_warps(int E) {
-  const int w = kSortCounters / E;
-  return w > 32 ? 32 : w;
+// The lanes whose key is this lane's, keys below 2^bits: a ballot for each bit.
+// (__match_any_sync takes about 230 cycles of a sub-partition each, ballots of 8
+// bits about 50.)
+__device__ __forceinline__ unsigned same_key(int key, int bits) {
+  unsigned same = 0xffffffffu;
+  for (int b = 0; b < bits; ++b, key >>= 1) {
+    const bool set = key & 1;
+    const unsigned v = __ballot_sync(0xffffffffu, set);
+    same &= set ? v : ~v;
+  }
+  return same;
 }
 
-inline size_t sort_smem(int E) { return ((size_t)sort_warps(E) * E + 2 * (size_t)E + 64) * 4; }
-
-// One cluster sorts all pairs: each of its warps takes a contiguous range of
-// them, counts its experts, and after the counts of the warps before it are
-// known walks its range again and places each pair.  Within 32 pairs a pair's
-// rank is the number of lower lanes with its expert.
+// One cluster sorts all pairs.  Each of its warps takes a contiguous range of
+// them and walks it in batches of 32, counting its experts in shared memory: a
+// pair's rank in its warp is the count so far and the lower lanes with its expert.
+// When the counts of the warps and blocks before are known, every pair has its
+// place; until then the ranks wait in slots.
+//
+// Every phase runs once or a few times, so the time is that of latencies, fetching
+// the code among them: the loops stay rolled.
+template <typename Id>
 __global__ void __launch_bounds__(1024) hcmix_expert_sort_kernel(const SortArgs A) {
+  begin_kernel();
   namespace cg = cooperative_groups;
   extern __shared__ int sort_shared[];
   const cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), cta = cluster.block_rank();
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int E = A.E;
-  int* count = sort_shared;         // [warps][E]
-  int* total = count + warps * E;   // [E] this block's pairs of each expert
-  int* start = total + E;           // [E] the block's first row of each expert
+  const int E = A.E, bits = 32 - __clz(E);  // of the keys 0 .. E
+  int* count = sort_shared;         // [warps][E], then the counts of the warps before
+  int* totals = count + warps * E;  // [ctas][E] the blocks' pairs of each expert
+  int* start = totals + ctas * E;   // [E] the block's first row of each expert
   int* scan = start + E;            // [warps] sums of the scan over experts
 
-  for (int i = threadIdx.x; i < warps * E; i += blockDim.x) count[i] = 0;
-  __syncthreads();
   const int64_t ranges = (int64_t)ctas * warps;
   const int64_t span = ((A.n + ranges - 1) / ranges + 31) / 32 * 32;
   const int64_t first = ((int64_t)cta * warps + warp) * span;
   const int64_t last = first + span < A.n ? first + span : A.n;
+  const auto key_at = [&](int64_t i) { return i < last ? expert_of<Id>(A, i) : E; };
+  int key = key_at(first + lane);
+  for (int i = threadIdx.x; i < warps * E; i += blockDim.x) count[i] = 0;
+  __syncthreads();
   int* mine = count + warp * E;
   for (int64_t i = first + lane; i - lane < last; i += 32) {
-    const int e = i < last ? expert_of(A, i) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && __ffs(same) - 1 == lane) mine[e] += __popc(same);
+    const int next = key_at(i + 32);
+    const unsigned same = same_key(key, bits);
+    const int lower = __popc(same & ((1u << lane) - 1));
+    const int so_far = key < E ? mine[key] : 0;
     __syncwarp();
+    if (lower == 0 && key < E) mine[key] = so_far + __popc(same);
+    __syncwarp();
+    if (i < last) A.slots[i] = so_far + lower;
+    key = next;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int s = 0;
+#pragma unroll 4
     for (int w = 0; w < warps; ++w) {
       const int c = count[w * E + e];
       count[w * E + e] = s;
       s += c;
     }
-    total[e] = s;
+    for (int b = 0; b < ctas; ++b) cluster.map_shared_rank(totals, b)[cta * E + e] = s;
   }
-  cluster.sync();
-  // start[e] = the pairs of all experts before e, and those of e in earlier blocks
+  // after this no block touches another's memory
+  if (ctas > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+  // start[e] = the pairs of all experts before e, and those of e in earlier blocks:
+  // a thread takes `per` neighbouring experts
   const int per = (E + blockDim.x - 1) / blockDim.x;
+  const int e0 = threadIdx.x * per, e1 = e0 + per < E ? e0 + per : E;
   int sum = 0;
-  for (int q = 0; q < per; ++q) {
-    const int e = threadIdx.x * per + q;
-    if (e < E)
-      for (int b = 0; b < ctas; ++b) sum += cluster.map_shared_rank(total, b)[e];
+  for (int e = e0; e < e1; ++e) {
+    int here = 0;
+#pragma unroll 4
+    for (int b = 0; b < ctas; ++b) {
+      if (b == cta) start[e] = here;
+      here += totals[b * E + e];
+    }
+    totals[e] = here;  // the expert's pairs in all blocks
+    sum += here;
   }
   int before = sum;
 #pragma unroll
@@ -93,64 +129,49 @@ __global__ void __launch_bounds__(1024) hcmix_expert_sort_kernel(const SortArgs 
   __syncthreads();
   int all = 0;
   before -= sum;
-  for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += scan[w];
-    all += scan[w];
+  const int with_experts = (E + 32 * per - 1) / (32 * per);  // warps
+  for (int w = 0; w < with_experts; ++w) {
+    const int t = scan[w];
+    if (w < warp) before += t;
+    all += t;
   }
-  for (int q = 0; q < per; ++q) {
-    const int e = threadIdx.x * per + q;
-    if (e >= E) break;
+  for (int e = e0; e < e1; ++e) {
+    start[e] += before;
     if (cta == 0) A.offsets[e] = before;
-    int here = before;
-    for (int b = 0; b < ctas; ++b) {
-      const int t = cluster.map_shared_rank(total, b)[e];
-      if (b < cta) here += t;
-      before += t;
-    }
-    start[e] = here;
+    before += totals[e];
   }
   if (cta == 0 && threadIdx.x == 0) A.offsets[E] = all;
   __syncthreads();
-  for (int64_t i = first + lane; i - lane < last; i += 32) {
-    const int e = i < last ? expert_of(A, i) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0) {
-      const int place = start[e] + mine[e] + __popc(same & ((1u << lane) - 1));
-      A.slots[i] = place;
-      A.source[place] = (int)i;
-    } else if (i < last) {
-      A.slots[i] = -1;
-    }
-    __syncwarp();
-    if (e >= 0 && __ffs(same) - 1 == lane) mine[e] += __popc(same);
-    __syncwarp();
+#pragma unroll 2
+  for (int64_t i = first + lane; i < last; i += 32) {
+    const int e = key_at(i);
+    const int place = e < E ? start[e] + mine[e] + A.slots[i] : -1;
+    A.slots[i] = place;
+    if (place >= 0) A.source[place] = (int)i;
   }
   for (int64_t r = all + (int64_t)cta * blockDim.x + threadIdx.x; r < A.n;
        r += (int64_t)ctas * blockDim.x)
     A.source[r] = -1;
-  cluster.sync();  // the other blocks may still read this one's totals
 }
 
-inline hcmix_status run_sort(const SortArgs& A, cudaStream_t stream) {
-  const size_t smem = sort_smem(A.E);
-  if (cudaFuncSetAttribute(hcmix_expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
+template <typename Id>
+hcmix_status launch_sort(const SortArgs& A, cudaStream_t stream) {
+  const int ctas = sort_blocks(A.n, A.E);
+  // a warp for each 32 pairs, as far as there are, so that few pairs need few counters
+  int64_t warps = (A.n + 32 * ctas - 1) / (32 * ctas);
+  const int most = kSortCounters / A.E < 32 ? kSortCounters / A.E : 32;
+  warps = warps < 4 ? 4 : warps > most ? most : warps;
+  const size_t smem = (((size_t)warps + ctas + 1) * A.E + 32) * 4;
+  if (ctas > 8 && cudaFuncSetAttribute(hcmix_expert_sort_kernel<Id>,
+                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                      cudaSuccess)
     return HCMIX_ERR_CUDA;
-  const int ctas = A.n <= 4096 ? 1 : kSortCluster;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(sort_warps(A.E) * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, hcmix_expert_sort_kernel, A) != cudaSuccess) return HCMIX_ERR_CUDA;
-  return launched();
+  return launch(hcmix_expert_sort_kernel<Id>, dim3(ctas), (unsigned)warps * 32, smem, stream, A,
+                ctas);
+}
+
+inline hcmix_status run_sort(const SortArgs& A, bool wide_ids, cudaStream_t stream) {
+  return wide_ids ? launch_sort<int64_t>(A, stream) : launch_sort<int32_t>(A, stream);
 }
 
 // ---------------------------------------------------------------- rows
@@ -183,6 +204,7 @@ __device__ __forceinline__ void zero_tail(const RowsArgs& A, int64_t b, int64_t 
 // A token's row is read once and written to each of its slots.
 template <typename T, int kVec>
 __global__ void __launch_bounds__(256) hcmix_expert_dispatch_kernel(const RowsArgs A) {
+  begin_kernel();
   const int64_t t = blockIdx.x / A.chunks;
   const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * blockDim.x + threadIdx.x) * kVec;
   if (c >= A.D) return;
@@ -196,6 +218,7 @@ __global__ void __launch_bounds__(256) hcmix_expert_dispatch_kernel(const RowsAr
 
 template <typename T, int kVec>
 __global__ void __launch_bounds__(256) hcmix_expert_combine_kernel(const RowsArgs A) {
+  begin_kernel();
   const int64_t t = blockIdx.x / A.chunks;
   const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * blockDim.x + threadIdx.x) * kVec;
   if (c >= A.D) return;
@@ -215,6 +238,7 @@ __global__ void __launch_bounds__(256) hcmix_expert_combine_kernel(const RowsArg
 // One block a pair.  dy[t] comes from L2 for all but the first of a token's pairs.
 template <typename T, int kVec>
 __global__ void __launch_bounds__(256) hcmix_expert_combine_backward_kernel(const RowsArgs A) {
+  begin_kernel();
   __shared__ float part[32];
   const int64_t pair = blockIdx.x, pairs = A.T * A.k;
   const int64_t c0 = (int64_t)threadIdx.x * kVec, step = (int64_t)blockDim.x * kVec;
@@ -250,19 +274,17 @@ hcmix_status launch_rows(RowsOp op, RowsArgs A, cudaStream_t stream) {
   const int64_t vecs = (A.D + kVec - 1) / kVec;
   if (op == RowsOp::kCombineBackward) {
     const unsigned threads = vecs >= 256 ? 256 : (unsigned)(vecs + 31) / 32 * 32;
-    hcmix_expert_combine_backward_kernel<T, kVec>
-        <<<(unsigned)(A.T * A.k > 0 ? A.T * A.k : 1), threads, 0, stream>>>(A);
-    return launched();
+    const int64_t blocks = A.T * A.k > 0 ? A.T * A.k : 1;
+    return launch(hcmix_expert_combine_backward_kernel<T, kVec>, dim3((unsigned)blocks), threads, 0,
+                  stream, A);
   }
   A.chunks = (int)((vecs + 255) / 256);
   const int threads = (int)((vecs + A.chunks - 1) / A.chunks + 31) / 32 * 32;
   const int64_t blocks = A.T * A.chunks;
   if (blocks >= ((int64_t)1 << 31)) return HCMIX_ERR_UNSUPPORTED;
-  if (op == RowsOp::kDispatch)
-    hcmix_expert_dispatch_kernel<T, kVec><<<(unsigned)blocks, threads, 0, stream>>>(A);
-  else
-    hcmix_expert_combine_kernel<T, kVec><<<(unsigned)blocks, threads, 0, stream>>>(A);
-  return launched();
+  return launch(op == RowsOp::kDispatch ? hcmix_expert_dispatch_kernel<T, kVec>
+                                        : hcmix_expert_combine_kernel<T, kVec>,
+                dim3((unsigned)blocks), threads, 0, stream, A);
 }
 
 inline hcmix_status run_rows(RowsOp op, const RowsArgs& A, hcmix_type type, cudaStream_t stream) {

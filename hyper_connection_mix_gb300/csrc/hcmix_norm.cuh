@@ -82,6 +82,7 @@ __device__ __forceinline__ void norm_apply(const NormArgs& A, int64_t row, int64
 // costs no digits.
 template <typename T, int kVec, int kPer, int kThreads, bool kCollapse>
 __global__ void __launch_bounds__(kThreads) hcmix_norm_kernel(const NormArgs A) {
+  begin_kernel();
   __shared__ float part[2][32];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
@@ -143,6 +144,7 @@ __global__ void __launch_bounds__(kThreads) hcmix_norm_kernel(const NormArgs A) 
 // from L2.
 template <typename T, int kVec, bool kCollapse>
 __global__ void __launch_bounds__(512) hcmix_norm_wide_kernel(const NormArgs A) {
+  begin_kernel();
   __shared__ float part[2][32];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
@@ -251,6 +253,7 @@ inline RingPlan ring_plan(int64_t vecs, int per, int most, int each, int rows, i
 // The norm of 16-byte vectors through the ring.
 template <typename T, int kVec, int kPer, int kThreads, int kBlocks, bool kCollapse>
 __global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_ring_kernel(const NormArgs A) {
+  begin_kernel();
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float part[2][32];
   constexpr int kRows = kCollapse ? kStreams : 1;
@@ -332,13 +335,9 @@ hcmix_status launch_norm_ring(const NormArgs& A, int64_t vecs, cudaStream_t stre
   constexpr int kRows = kCollapse ? kStreams : 1;
   const RingPlan p = ring_plan(vecs, kPer, kThreads, kBlocks, kRows, kVec * (int)sizeof(T));
   const size_t smem = kRingStages<kRows, kPer, kThreads, kBlocks> * p.stage;
-  const auto kernel = hcmix_norm_ring_kernel<T, kVec, kPer, kThreads, kBlocks, kCollapse>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
-    return HCMIX_ERR_CUDA;
   const int64_t blocks = A.M < kSms * p.each ? A.M : kSms * p.each;
-  kernel<<<(unsigned)blocks, p.threads, smem, stream>>>(A);
-  return launched();
+  return launch(hcmix_norm_ring_kernel<T, kVec, kPer, kThreads, kBlocks, kCollapse>,
+                dim3((unsigned)blocks), p.threads, smem, stream, A);
 }
 
 // The variant goes by type, alignment and width, never by the number of rows: a
@@ -350,24 +349,21 @@ hcmix_status launch_norm(const NormArgs& A, cudaStream_t stream) {
   constexpr int kMost = (kVec == 1 ? 16 : 4) / (kCollapse ? 2 : 1);
   constexpr int kThreads = kCollapse ? 512 : 256;
   const int64_t vecs = (A.N + kVec - 1) / kVec;
-  const unsigned grid = (unsigned)A.M;
+  const dim3 grid((unsigned)A.M);
   const auto threads = [&](int per) { return (unsigned)((vecs + per - 1) / per + 31) / 32 * 32; };
   if constexpr (kVec > 1) {
     if (vecs <= 256) return launch_norm_ring<T, kVec, 1, 256, 4, kCollapse>(A, vecs, stream);
     if (vecs <= 640) return launch_norm_ring<T, kVec, 2, 320, 2, kCollapse>(A, vecs, stream);
     if (vecs <= 1024) return launch_norm_ring<T, kVec, 2, 512, 1, kCollapse>(A, vecs, stream);
   } else {
-    if (vecs <= kThreads * kMost) {
-      hcmix_norm_kernel<T, kVec, kMost, kThreads, kCollapse>
-          <<<grid, threads(kMost), 0, stream>>>(A);
-      return launched();
-    }
+    if (vecs <= kThreads * kMost)
+      return launch(hcmix_norm_kernel<T, kVec, kMost, kThreads, kCollapse>, grid, threads(kMost), 0,
+                    stream, A);
   }
   if (vecs <= 1024 * kMost)
-    hcmix_norm_kernel<T, kVec, kMost, 1024, kCollapse><<<grid, threads(kMost), 0, stream>>>(A);
-  else
-    hcmix_norm_wide_kernel<T, kVec, kCollapse><<<grid, 512, 0, stream>>>(A);
-  return launched();
+    return launch(hcmix_norm_kernel<T, kVec, kMost, 1024, kCollapse>, grid, threads(kMost), 0,
+                  stream, A);
+  return launch(hcmix_norm_wide_kernel<T, kVec, kCollapse>, grid, 512, 0, stream, A);
 }
 
 inline hcmix_status run_norm(const NormArgs& A, hcmix_type type, bool collapse,
@@ -388,6 +384,7 @@ inline hcmix_status run_norm(const NormArgs& A, hcmix_type type, bool collapse,
 // dx, one block a row.
 template <typename T, int kVec>
 __global__ void __launch_bounds__(512) hcmix_norm_dx_kernel(const NormArgs A) {
+  begin_kernel();
   __shared__ float part[2 * 32];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
@@ -428,6 +425,7 @@ constexpr int kColumnThreads = 128;
 // from b * kColumnThreads * kVec and rows s, s + slabs, ...
 template <typename T, int kVec>
 __global__ void __launch_bounds__(kColumnThreads) hcmix_norm_columns_kernel(const NormArgs A) {
+  begin_kernel();
   const int64_t c = ((int64_t)blockIdx.x * kColumnThreads + threadIdx.x) * kVec;
   if (c >= A.N) return;
   float dw[kVec] = {}, db[kVec] = {};
@@ -458,6 +456,7 @@ __global__ void __launch_bounds__(kColumnThreads) hcmix_norm_columns_kernel(cons
 // L1 and the stage.
 template <typename T, int kVec, int kPer, int kGroup, int kThreads, int kBlocks>
 __global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_backward_kernel(const NormArgs A) {
+  begin_kernel();
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float part[2][2 * kGroup * 32];
   constexpr bool kKeep = kPer == 1;
@@ -560,7 +559,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_backward_kernel(
     }
     ring.advance();
   }
-  launch_dependents();
   float* out = A.part + (int64_t)blockIdx.x * 2 * A.N;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
@@ -584,10 +582,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_backward_kernel(
 constexpr int kJoinGroups = 16;
 
 __global__ void __launch_bounds__(32 * kJoinGroups) hcmix_norm_join_kernel(const NormArgs A) {
+  begin_kernel();
   __shared__ float part[kJoinGroups][32];
   const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  dependency_wait();
   float s = 0.f;
   if (c < 2 * A.N) {
 #pragma unroll 8
@@ -639,28 +637,8 @@ inline size_t norm_workspace(int size, int64_t M, int64_t N) {
 template <typename T, int kVec, int kPer, int kGroup, int kThreads, int kBlocks>
 hcmix_status launch_norm_backward_ring(const NormArgs& A, const RingPlan& p, cudaStream_t stream) {
   const size_t smem = kRingStages<2 * kGroup, kPer, kThreads, kBlocks> * p.stage;
-  const auto kernel = hcmix_norm_backward_kernel<T, kVec, kPer, kGroup, kThreads, kBlocks>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
-    return HCMIX_ERR_CUDA;
-  kernel<<<A.blocks, p.threads, smem, stream>>>(A);
-  return launched();
-}
-
-// The join may be set up while the kernel before it still runs (it waits for its
-// memory itself).
-inline hcmix_status launch_join(const NormArgs& A, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((2 * A.N + 31) / 32));
-  cfg.blockDim = dim3(32 * kJoinGroups);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, hcmix_norm_join_kernel, A) != cudaSuccess) return HCMIX_ERR_CUDA;
-  return launched();
+  return launch(hcmix_norm_backward_kernel<T, kVec, kPer, kGroup, kThreads, kBlocks>,
+                dim3(A.blocks), p.threads, smem, stream, A);
 }
 
 template <typename T, int kVec>
@@ -671,12 +649,13 @@ hcmix_status launch_norm_backward(NormArgs A, cudaStream_t stream) {
   if (A.dweight == nullptr || p.variant == 0) {
     const int64_t vecs = (A.N + kVec - 1) / kVec;
     const unsigned threads = vecs >= 256 ? 256 : (unsigned)(vecs + 31) / 32 * 32;
-    if (A.M > 0) hcmix_norm_dx_kernel<T, kVec><<<(unsigned)A.M, threads, 0, stream>>>(A);
-    if (A.dweight == nullptr) return launched();
+    if (A.M > 0)
+      st = launch(hcmix_norm_dx_kernel<T, kVec>, dim3((unsigned)A.M), threads, 0, stream, A);
+    if (st != HCMIX_OK || A.dweight == nullptr) return st;
     const int64_t per = (int64_t)kColumnThreads * kVec;
     if (p.blocks > 0)
-      hcmix_norm_columns_kernel<T, kVec>
-          <<<dim3((unsigned)((A.N + per - 1) / per), p.blocks), kColumnThreads, 0, stream>>>(A);
+      st = launch(hcmix_norm_columns_kernel<T, kVec>,
+                  dim3((unsigned)((A.N + per - 1) / per), p.blocks), kColumnThreads, 0, stream, A);
   } else if constexpr (kVec * sizeof(T) >= 4) {
     switch (p.variant) {
       case 1: st = launch_norm_backward_ring<T, kVec, 1, 2, 256, 3>(A, p.ring, stream); break;
@@ -686,8 +665,8 @@ hcmix_status launch_norm_backward(NormArgs A, cudaStream_t stream) {
     }
   }
   if (st != HCMIX_OK) return st;
-  st = launched();
-  return st == HCMIX_OK ? launch_join(A, stream) : st;
+  return launch(hcmix_norm_join_kernel, dim3((unsigned)((2 * A.N + 31) / 32)), 32 * kJoinGroups, 0,
+                stream, A);
 }
 
 inline hcmix_status run_norm_backward(const NormArgs& A, hcmix_type type, cudaStream_t stream) {

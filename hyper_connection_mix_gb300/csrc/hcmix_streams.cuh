@@ -22,6 +22,7 @@ struct StreamsArgs {
 
 template <typename T, int kVec>
 __global__ void __launch_bounds__(256) hcmix_collapse_kernel(const StreamsArgs A) {
+  begin_kernel();
   const int64_t row = blockIdx.x / A.chunks;
   const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * blockDim.x + threadIdx.x) * kVec;
   if (c >= A.D) return;
@@ -39,6 +40,7 @@ __global__ void __launch_bounds__(256) hcmix_collapse_kernel(const StreamsArgs A
 
 template <typename T, int kVec>
 __global__ void __launch_bounds__(256) hcmix_expand_kernel(const StreamsArgs A) {
+  begin_kernel();
   const int64_t row = blockIdx.x / A.chunks;
   const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * blockDim.x + threadIdx.x) * kVec;
   if (c >= A.D) return;
@@ -62,6 +64,7 @@ __global__ void __launch_bounds__(256) hcmix_expand_kernel(const StreamsArgs A) 
 // One block a row: the row's four dot products need all of its columns.
 template <typename T, int kVec>
 __global__ void __launch_bounds__(256) hcmix_collapse_backward_kernel(const StreamsArgs A) {
+  begin_kernel();
   __shared__ float part[kStreams * 32];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
@@ -107,6 +110,7 @@ __global__ void __launch_bounds__(256) hcmix_collapse_backward_kernel(const Stre
 // One block a row, as above; 4 + 16 dot products.
 template <typename T, int kVec>
 __global__ void __launch_bounds__(256, 2) hcmix_expand_backward_kernel(const StreamsArgs A) {
+  begin_kernel();
   constexpr int kDots = kStreams + kStreams * kStreams;
   __shared__ float part[kDots * 32];
   const int64_t row = blockIdx.x;
@@ -170,20 +174,16 @@ hcmix_status launch_streams(StreamsOp op, StreamsArgs A, cudaStream_t stream) {
     const int threads = (int)((vecs + A.chunks - 1) / A.chunks + 31) / 32 * 32;
     const int64_t blocks = A.M * A.chunks;
     if (blocks >= ((int64_t)1 << 31)) return HCMIX_ERR_UNSUPPORTED;
-    if (op == StreamsOp::kCollapse)
-      hcmix_collapse_kernel<T, kVec><<<(unsigned)blocks, threads, 0, stream>>>(A);
-    else
-      hcmix_expand_kernel<T, kVec><<<(unsigned)blocks, threads, 0, stream>>>(A);
-    return launched();
+    return launch(op == StreamsOp::kCollapse ? hcmix_collapse_kernel<T, kVec>
+                                             : hcmix_expand_kernel<T, kVec>,
+                  dim3((unsigned)blocks), threads, 0, stream, A);
   }
   // as many equal steps through the row as blocks of 256 threads need
   const int64_t steps = (vecs + 255) / 256;
   const int threads = (int)((vecs + steps - 1) / steps + 31) / 32 * 32;
-  if (op == StreamsOp::kCollapseBackward)
-    hcmix_collapse_backward_kernel<T, kVec><<<(unsigned)A.M, threads, 0, stream>>>(A);
-  else
-    hcmix_expand_backward_kernel<T, kVec><<<(unsigned)A.M, threads, 0, stream>>>(A);
-  return launched();
+  return launch(op == StreamsOp::kCollapseBackward ? hcmix_collapse_backward_kernel<T, kVec>
+                                                   : hcmix_expand_backward_kernel<T, kVec>,
+                dim3((unsigned)A.M), threads, 0, stream, A);
 }
 
 inline hcmix_status run_streams(StreamsOp op, const StreamsArgs& A, hcmix_type type,

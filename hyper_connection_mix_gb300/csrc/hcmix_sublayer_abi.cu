@@ -241,8 +241,8 @@ hcmix_status hc_mix_expert_sort(const void* ids, int id_bytes, int64_t T, int64_
     return HCMIX_ERR_INVALID_ARG;
   if (!aligned(ids, id_bytes) || !aligned(offsets, 4) || !aligned(slots, 4) || !aligned(source, 4))
     return HCMIX_ERR_ALIGNMENT;
-  SortArgs A = {ids, id_bytes == 8, T * k, (int)E, offsets, slots, source};
-  return run_sort(A, as_stream(stream));
+  SortArgs A = {ids, T * k, (int)E, offsets, slots, source};
+  return run_sort(A, id_bytes == 8, as_stream(stream));
 }
 
 hcmix_status hc_mix_expert_dispatch(const void* x, int64_t x_stride, hcmix_type type, int64_t T,

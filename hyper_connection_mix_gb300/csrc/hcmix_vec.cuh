@@ -43,7 +43,11 @@ template <typename T>
 constexpr int kWide = 16 / (int)sizeof(T);
 
 // Two elements of a 16-bit type and their values.
-__device__ __forceinline__ float2 pair_to_f32(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+__device__ __forceinline__ float2 pair_to_f32(__nv_bfloat162 v) {
+  // a bf16's bits are the upper half of its fp32's
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&v);
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 __device__ __forceinline__ float2 pair_to_f32(__half2 v) { return __half22float2(v); }
 __device__ __forceinline__ void pair_from_f32(__nv_bfloat162& p, float a, float b) {
   p = __floats2bfloat162_rn(a, b);
@@ -400,15 +404,12 @@ __device__ __forceinline__ void async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// ---- programmatic dependent launch: the next kernel's blocks may start once all
-// of this grid's have called launch_dependents (or ended); dependency_wait, in
-// that kernel, returns when this grid has ended and its memory can be seen.
-
-__device__ __forceinline__ void launch_dependents() {
+// ---- programmatic dependent launch.  Every sublayer kernel is launched so that
+// its blocks may be set up while the grid before it in the stream still runs, and
+// begins with this: the next grid may be set up, and nothing is read or written
+// before the grid before this one has ended and its memory can be seen.
+__device__ __forceinline__ void begin_kernel() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-__device__ __forceinline__ void dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
@@ -431,8 +432,32 @@ inline hcmix_status with_type(hcmix_type t, F&& f) {
   return HCMIX_ERR_INVALID_ARG;
 }
 
-inline hcmix_status launched() {
-  return cudaGetLastError() == cudaSuccess ? HCMIX_OK : HCMIX_ERR_CUDA;
+// Launches a kernel that starts with begin_kernel(); `cluster` blocks a cluster.
+template <typename Args>
+inline hcmix_status launch(void (*kernel)(const Args), dim3 grid, unsigned threads, size_t smem,
+                           cudaStream_t stream, const Args& args, unsigned cluster = 1) {
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem) != cudaSuccess)
+    return HCMIX_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args) != cudaSuccess) {
+    cudaGetLastError();
+    return HCMIX_ERR_CUDA;
+  }
+  return HCMIX_OK;
 }
 
 }  // namespace sublayer
