@@ -166,7 +166,7 @@ hcmix_status launch_sort(const SortArgs& A, cudaStream_t stream) {
                                        cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
                       cudaSuccess)
     return HCMIX_ERR_CUDA;
-  return launch(hcmix_expert_sort_kernel<Id>, dim3(ctas), (unsigned)warps * 32, smem, stream, A,
+  return launch(hcmix_expert_sort_kernel<Id>, dim3(ctas), dim3((unsigned)warps * 32), smem, stream, A,
                 ctas);
 }
 
@@ -188,112 +188,118 @@ struct RowsArgs {
   int chunks;
 };
 
-// Rows from offsets[E] on carry no pair: block `b` of `blocks` zeroes its share
-// of them, in its columns.
+// Rows from offsets[E] on carry no pair: worker `b` of `workers` zeroes its share of
+// them, in its columns c, c + step, ... below `end`.
 template <typename T, int kVec>
-__device__ __forceinline__ void zero_tail(const RowsArgs& A, int64_t b, int64_t blocks, int64_t c,
-                                          int64_t step) {
+__device__ __forceinline__ void zero_tail(const RowsArgs& A, int64_t b, int64_t workers, int64_t c,
+                                          int step, int64_t end) {
   if (A.offsets == nullptr) return;
   int64_t used = A.offsets[A.E];
   if (used < 0) used = 0;
   const float zero[kVec] = {};
-  for (int64_t r = used + b; r < A.rows; r += blocks)
-    for (int64_t q = c; q < A.D; q += step) store_f32<T, kVec>(static_cast<T*>(A.out) + r * A.D + q, zero);
+  for (int64_t r = used + b; r < A.rows; r += workers)
+    for (int64_t q = c; q < end; q += step)
+      store_f32<T, kVec>(static_cast<T*>(A.out) + r * A.D + q, zero);
 }
 
 // A token's row is read once and written to each of its slots.
-template <typename T, int kVec>
+template <typename T, int kVec, int kU>
 __global__ void __launch_bounds__(256) hcmix_expert_dispatch_kernel(const RowsArgs A) {
   begin_kernel();
   const int64_t t = blockIdx.x / A.chunks;
-  const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * blockDim.x + threadIdx.x) * kVec;
+  const int step = blockDim.x * kVec;
+  const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * kU * blockDim.x + threadIdx.x) * kVec;
   if (c >= A.D) return;
-  const Packed<T, kVec> v = load_vec<T, kVec>(static_cast<const T*>(A.x) + t * A.x_stride + c);
+  Cols<T, kVec, kU> v;
+  v.load(static_cast<const T*>(A.x) + t * A.x_stride, c, step, A.D);
   for (int64_t j = 0; j < A.k; ++j) {
     const int64_t s = A.slots[t * A.k + j];
-    if (s >= 0 && s < A.rows) store_vec<T, kVec>(static_cast<T*>(A.out) + s * A.D + c, v);
+    if (s >= 0 && s < A.rows) v.store(static_cast<T*>(A.out) + s * A.D, c, step, A.D);
   }
-  zero_tail<T, kVec>(A, t, A.T, c, A.D);
+  const int64_t end = c + kU * step < A.D ? c + kU * step : A.D;
+  zero_tail<T, kVec>(A, t, A.T, c, step, end);
 }
 
-template <typename T, int kVec>
+template <typename T, int kVec, int kU>
 __global__ void __launch_bounds__(256) hcmix_expert_combine_kernel(const RowsArgs A) {
   begin_kernel();
   const int64_t t = blockIdx.x / A.chunks;
-  const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * blockDim.x + threadIdx.x) * kVec;
+  const int step = blockDim.x * kVec;
+  const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * kU * blockDim.x + threadIdx.x) * kVec;
   if (c >= A.D) return;
-  float sum[kVec] = {};
+  float sum[kU * kVec] = {};
+#pragma unroll 4
   for (int64_t j = 0; j < A.k; ++j) {
     const int64_t s = A.slots[t * A.k + j];
     if (s < 0 || s >= A.rows) continue;
     const float w = A.weights != nullptr ? A.weights[t * A.k + j] : 1.f;
-    float v[kVec];
-    load_f32<T, kVec>(static_cast<const T*>(A.ys) + s * A.ys_stride + c, v);
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) sum[e] = fmaf(w, v[e], sum[e]);
+    float v[kU * kVec];
+    load_cols<T, kVec, kU>(static_cast<const T*>(A.ys) + s * A.ys_stride, c, step, A.D, v);
+    vfma(sum, w, v, sum);
   }
-  store_f32<T, kVec>(static_cast<T*>(A.out) + t * A.D + c, sum);
+  store_cols<T, kVec, kU>(static_cast<T*>(A.out) + t * A.D, c, step, A.D, sum);
 }
 
-// One block a pair.  dy[t] comes from L2 for all but the first of a token's pairs.
-template <typename T, int kVec>
-__global__ void __launch_bounds__(256) hcmix_expert_combine_backward_kernel(const RowsArgs A) {
+// A warp takes a pair: its one dot product needs no other warp.  The block's warps
+// take the pairs of neighbouring tokens, so dy[t] comes from L1 for all but the
+// first of a token's pairs.
+constexpr int kPairWarps = 8;
+
+template <typename T, int kVec, int kU>
+__global__ void __launch_bounds__(32 * kPairWarps) hcmix_expert_combine_backward_kernel(
+    const RowsArgs A) {
   begin_kernel();
-  __shared__ float part[32];
-  const int64_t pair = blockIdx.x, pairs = A.T * A.k;
-  const int64_t c0 = (int64_t)threadIdx.x * kVec, step = (int64_t)blockDim.x * kVec;
+  const int lane = threadIdx.x % 32, step = 32 * kVec;
+  const int64_t pairs = A.T * A.k;
+  const int64_t pair = (int64_t)blockIdx.x * kPairWarps + threadIdx.x / 32;
   const int64_t s = pair < pairs ? A.slots[pair] : -1;
-  float dot[1] = {0.f};
+  Acc dot;
   if (s >= 0 && s < A.rows) {
     const int64_t t = pair / A.k;
     const float w = A.weights[pair];
     const T* dy = static_cast<const T*>(A.x) + t * A.x_stride;
     const T* ys = static_cast<const T*>(A.ys) + s * A.ys_stride;
     T* dys = static_cast<T*>(A.out) + s * A.D;
-    for (int64_t c = c0; c < A.D; c += step) {
-      float g[kVec], v[kVec];
-      load_f32<T, kVec>(dy + c, g);
-      load_f32<T, kVec>(ys + c, v);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        dot[0] = fmaf(g[e], v[e], dot[0]);
-        g[e] *= w;
-      }
-      store_f32<T, kVec>(dys + c, g);
+#pragma unroll 4
+    for (int64_t c = lane * kVec; c < A.D; c += kU * step) {
+      float g[kU * kVec], v[kU * kVec];
+      load_cached_cols<T, kVec, kU>(dy, c, step, A.D, g);
+      load_cols<T, kVec, kU>(ys, c, step, A.D, v);
+      dot.add(g, v);
+      vmul(g, w, g);
+      store_cols<T, kVec, kU>(dys, c, step, A.D, g);
     }
   }
-  block_sums_all<1>(dot, part);
-  if (threadIdx.x == 0 && pair < pairs) A.dweights[pair] = dot[0];
-  zero_tail<T, kVec>(A, pair, gridDim.x, c0, step);
+  const float total = warp_sum(dot.sum());
+  if (lane == 0 && pair < pairs) A.dweights[pair] = total;
+  zero_tail<T, kVec>(A, pair, (int64_t)gridDim.x * kPairWarps, lane * kVec, step, A.D);
 }
 
 enum class RowsOp { kDispatch, kCombine, kCombineBackward };
 
-template <typename T, int kVec>
+template <typename T, int kVec, int kU>
 hcmix_status launch_rows(RowsOp op, RowsArgs A, cudaStream_t stream) {
-  const int64_t vecs = (A.D + kVec - 1) / kVec;
   if (op == RowsOp::kCombineBackward) {
-    const unsigned threads = vecs >= 256 ? 256 : (unsigned)(vecs + 31) / 32 * 32;
-    const int64_t blocks = A.T * A.k > 0 ? A.T * A.k : 1;
-    return launch(hcmix_expert_combine_backward_kernel<T, kVec>, dim3((unsigned)blocks), threads, 0,
-                  stream, A);
+    int64_t blocks = (A.T * A.k + kPairWarps - 1) / kPairWarps;
+    blocks = blocks > 0 ? blocks : 1;
+    return launch(hcmix_expert_combine_backward_kernel<T, kVec, kU>, dim3((unsigned)blocks),
+                  dim3(32 * kPairWarps), 0, stream, A);
   }
-  A.chunks = (int)((vecs + 255) / 256);
-  const int threads = (int)((vecs + A.chunks - 1) / A.chunks + 31) / 32 * 32;
+  const int64_t shares = (A.D + kVec * kU - 1) / (kVec * kU);
+  A.chunks = (int)((shares + 255) / 256);
+  const unsigned threads = (unsigned)((shares + A.chunks - 1) / A.chunks + 31) / 32 * 32;
   const int64_t blocks = A.T * A.chunks;
   if (blocks >= ((int64_t)1 << 31)) return HCMIX_ERR_UNSUPPORTED;
-  return launch(op == RowsOp::kDispatch ? hcmix_expert_dispatch_kernel<T, kVec>
-                                        : hcmix_expert_combine_kernel<T, kVec>,
-                dim3((unsigned)blocks), threads, 0, stream, A);
+  return launch(op == RowsOp::kDispatch ? hcmix_expert_dispatch_kernel<T, kVec, kU>
+                                        : hcmix_expert_combine_kernel<T, kVec, kU>,
+                dim3((unsigned)blocks), dim3(threads), 0, stream, A);
 }
 
 inline hcmix_status run_rows(RowsOp op, const RowsArgs& A, hcmix_type type, cudaStream_t stream) {
-  const int n = size_of(type);
-  const bool wide = aligned_rows(A.x, A.x_stride, n) && aligned_rows(A.ys, A.ys_stride, n) &&
-                    aligned_rows(A.out, A.D, n);
-  return with_type(type, [&](auto t) {
-    using T = decltype(t);
-    return wide ? launch_rows<T, kWide<T>>(op, A, stream) : launch_rows<T, 1>(op, A, stream);
+  const int bytes =
+      vector_bytes(size_of(type), {{A.x, A.x_stride}, {A.ys, A.ys_stride}, {A.out, A.D}});
+  return with_vector(type, bytes, [&](auto t, auto vec, auto u) {
+    return launch_rows<decltype(t), decltype(vec)::value, decltype(u)::value>(op, A, stream);
   });
 }
 

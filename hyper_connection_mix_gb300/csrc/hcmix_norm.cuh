@@ -1,4 +1,9 @@
 // Layer norm forward (of a plain row, or of the collapsed streams) and backward.
+//
+// Resident blocks take rows in turn through a ring of rows in shared memory, copied
+// ahead of their use; what belongs to a thread's columns (weight, bias, sums over
+// rows) stays in its registers.  Rows too wide for that are passed over several
+// times.
 #pragma once
 
 #include "hcmix_vec.cuh"
@@ -24,128 +29,29 @@ struct NormArgs {
   int blocks;  // partial rows of the weight's gradient
 };
 
-// kVec values of column c of a row, x itself or sum_i pre[i] x_i: first loaded,
-// then worked out.
+// v = x itself, or sum_i pre[i] x_i, of the loaded vectors.
 template <typename T, int kVec, bool kCollapse>
-struct NormSource {
-  Packed<T, kVec> s[kCollapse ? kStreams : 1];
-  __device__ __forceinline__ void load(const NormArgs& A, const T* x, int64_t c) {
-#pragma unroll
-    for (int i = 0; i < (kCollapse ? kStreams : 1); ++i)
-      s[i] = load_vec<T, kVec>(x + i * A.N + c);
-  }
-  __device__ __forceinline__ void values(const float* pre, float (&v)[kVec]) const {
-    s[0].unpack(v);
-    if constexpr (kCollapse) {
-      vmul(v, pre[0], v);
-#pragma unroll
-      for (int i = 1; i < kStreams; ++i) {
-        float t[kVec];
-        s[i].unpack(t);
-        vfma(v, pre[i], t, v);
-      }
-    }
-  }
-};
-
-template <typename T, int kVec, bool kCollapse>
-__device__ __forceinline__ void norm_source(const NormArgs& A, const T* x, const float* pre,
-                                            int64_t c, float (&v)[kVec]) {
-  NormSource<T, kVec, kCollapse> s;
-  s.load(A, x, c);
-  s.values(pre, v);
-}
-
-// Weight and bias of column c, ones and zeros where there are none.
-template <typename T, int kVec>
-__device__ __forceinline__ void norm_params(const NormArgs& A, int64_t c, float (&w)[kVec],
-                                            float (&b)[kVec]) {
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) w[e] = 1.f, b[e] = 0.f;
-  if (A.weight != nullptr) load_param<T, kVec>(A.weight, A.p32, c, w);
-  if (A.bias != nullptr) load_param<T, kVec>(A.bias, A.p32, c, b);
-}
-
-template <typename T, int kVec>
-__device__ __forceinline__ void norm_apply(const NormArgs& A, int64_t row, int64_t c, float mean,
-                                           float rstd, float (&v)[kVec]) {
-  float w[kVec], b[kVec];
-  norm_params<T, kVec>(A, c, w, b);
-  vadd(v, -mean, v);
-  vmul(v, rstd, v);
-  vfma(v, v, w, b);
-  store_f32<T, kVec>(static_cast<T*>(A.y) + row * A.N + c, v);
-}
-
-// One block a row, the row in registers: kPer vectors a thread.  The mean is
-// taken first and the variance from the differences, so that a large mean
-// costs no digits.
-template <typename T, int kVec, int kPer, int kThreads, bool kCollapse>
-__global__ void __launch_bounds__(kThreads) hcmix_norm_kernel(const NormArgs A) {
-  begin_kernel();
-  __shared__ float part[2][32];
-  const int64_t row = blockIdx.x;
-  const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
-  float pre[kStreams] = {};
+__device__ __forceinline__ void norm_values(const Packed<T, kVec> (&s)[kCollapse ? kStreams : 1],
+                                            const float* pre, float (&v)[kVec]) {
+  s[0].unpack(v);
   if constexpr (kCollapse) {
+    vmul(v, pre[0], v);
 #pragma unroll
-    for (int i = 0; i < kStreams; ++i) pre[i] = A.pre[row * kStreams + i];
-  }
-  float v[kPer][kVec];
-  float sum[1] = {0.f};
-  NormSource<T, kVec, kCollapse> raw[kPer];
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int64_t c = ((int64_t)k * blockDim.x + threadIdx.x) * kVec;
-    if (c < A.N) raw[k].load(A, x, c);
-  }
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int64_t c = ((int64_t)k * blockDim.x + threadIdx.x) * kVec;
-    if (c < A.N) {
-      raw[k].values(pre, v[k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) v[k][e] = 0.f;
+    for (int i = 1; i < kStreams; ++i) {
+      float t[kVec];
+      s[i].unpack(t);
+      vfma(v, pre[i], t, v);
     }
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) sum[0] += v[k][e];
-  }
-  const float inv = 1.f / (float)A.N;
-  block_sums_all<1>(sum, part[0]);
-  const float mean = sum[0] * inv;
-  float sq[1] = {0.f};
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int64_t c = ((int64_t)k * blockDim.x + threadIdx.x) * kVec;
-    if (c < A.N) {
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) sq[0] = fmaf(v[k][e] - mean, v[k][e] - mean, sq[0]);
-    }
-  }
-  block_sums_all<1>(sq, part[1]);
-  const float rstd = 1.f / sqrtf(sq[0] * inv + A.eps);
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int64_t c = ((int64_t)k * blockDim.x + threadIdx.x) * kVec;
-    if (c < A.N) {
-      if (kCollapse && A.h != nullptr)
-        store_f32<T, kVec>(static_cast<T*>(A.h) + row * A.N + c, v[k]);
-      norm_apply<T, kVec>(A, row, c, mean, rstd, v[k]);
-    }
-  }
-  if (threadIdx.x == 0) {
-    if (A.mean != nullptr) A.mean[row] = mean;
-    if (A.rstd != nullptr) A.rstd[row] = rstd;
   }
 }
 
-// Rows too wide for registers: three passes over the row, the later two mostly
-// from L2.
+// Rows too wide for the ring: three passes over the row, the later two mostly from
+// L2.
 template <typename T, int kVec, bool kCollapse>
 __global__ void __launch_bounds__(512) hcmix_norm_wide_kernel(const NormArgs A) {
   begin_kernel();
   __shared__ float part[2][32];
+  constexpr int kRows = kCollapse ? kStreams : 1;
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
   const int64_t step = (int64_t)blockDim.x * kVec, c0 = (int64_t)threadIdx.x * kVec;
@@ -154,26 +60,43 @@ __global__ void __launch_bounds__(512) hcmix_norm_wide_kernel(const NormArgs A) 
 #pragma unroll
     for (int i = 0; i < kStreams; ++i) pre[i] = A.pre[row * kStreams + i];
   }
-  float v[kVec], sum[1] = {0.f}, sq[1] = {0.f};
-  for (int64_t c = c0; c < A.N; c += step) {
-    norm_source<T, kVec, kCollapse>(A, x, pre, c, v);
+  float v[kVec];
+  const auto load = [&](int64_t c) {
+    Packed<T, kVec> s[kRows];
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) sum[0] += v[e];
+    for (int i = 0; i < kRows; ++i) s[i] = load_vec<T, kVec>(x + i * A.N + c);
+    norm_values<T, kVec, kCollapse>(s, pre, v);
+  };
+  Acc sum, square;
+#pragma unroll 4
+  for (int64_t c = c0; c < A.N; c += step) {
+    load(c);
+    sum.add(v);
   }
   const float inv = 1.f / (float)A.N;
-  block_sums_all<1>(sum, part[0]);
-  const float mean = sum[0] * inv;
+  float total[1] = {sum.sum()};
+  team_sums<1>(total, part[0]);
+  const float mean = total[0] * inv;
+#pragma unroll 4
   for (int64_t c = c0; c < A.N; c += step) {
-    norm_source<T, kVec, kCollapse>(A, x, pre, c, v);
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) sq[0] = fmaf(v[e] - mean, v[e] - mean, sq[0]);
+    load(c);
+    vadd(v, -mean, v);
+    square.add(v, v);
   }
-  block_sums_all<1>(sq, part[1]);
+  float sq[1] = {square.sum()};
+  team_sums<1>(sq, part[1]);
   const float rstd = 1.f / sqrtf(sq[0] * inv + A.eps);
+#pragma unroll 2
   for (int64_t c = c0; c < A.N; c += step) {
-    norm_source<T, kVec, kCollapse>(A, x, pre, c, v);
+    load(c);
     if (kCollapse && A.h != nullptr) store_f32<T, kVec>(static_cast<T*>(A.h) + row * A.N + c, v);
-    norm_apply<T, kVec>(A, row, c, mean, rstd, v);
+    float w[kVec], b[kVec];
+    load_param<T, kVec>(A.weight, A.p32, c, 1.f, w);
+    load_param<T, kVec>(A.bias, A.p32, c, 0.f, b);
+    vadd(v, -mean, v);
+    vmul(v, rstd, v);
+    vfma(v, v, w, b);
+    store_f32<T, kVec>(static_cast<T*>(A.y) + row * A.N + c, v);
   }
   if (threadIdx.x == 0) {
     if (A.mean != nullptr) A.mean[row] = mean;
@@ -181,41 +104,76 @@ __global__ void __launch_bounds__(512) hcmix_norm_wide_kernel(const NormArgs A) 
   }
 }
 
-// Resident blocks take groups of rows b, b + blocks, ... through a ring of
-// kStages groups in shared memory.  Each thread copies the vectors that it will
-// read itself (cp.async), so no barrier stands between the copies and their use,
-// and what belongs to its columns (weight, bias, sums over rows) stays in
-// registers.  A group is kRows source rows (streams; x and dy of several rows).
-template <typename T, int kVec, int kPer, int kRows, int kStages>
+// ---------------------------------------------------------------- the ring
+
+// A ring of kStages groups of rows in shared memory, for one team of blockDim.x
+// threads.  A group is kRows source rows (streams; x and dy of several rows); a thread
+// has kPer vectors of each, its columns the same in every group.  Each thread copies
+// the vectors that it will read itself, so that no barrier stands between the copies
+// and their use.
+//
+// Vectors of 4 bytes and more are copied by cp.async.  Single 16-bit elements
+// (rows that do not even start on 4 bytes) cannot be: they are loaded into registers
+// when their copy is started and stored to the other of two stages by land(), at the
+// end of the work on the group before.
+template <typename T, int kVec, int kPer, int kRows, int kMostStages>
 struct Ring {
   using V = Packed<T, kVec>;
+  static constexpr bool kAsync = sizeof(V) >= 4;
+  static constexpr int kStages = kAsync ? kMostStages : 2;
   unsigned char* mine;
   int pitch;  // bytes from one of the thread's vectors to its next
   int at;     // byte offset of the stage that is read
   int columns, first, step;  // the thread's columns: first + k * step, below columns
+  V pending[kAsync ? 1 : kRows * kPer];
   __device__ __forceinline__ Ring(unsigned char* smem, int64_t width)
-      : mine(smem + threadIdx.x * sizeof(V)),
-        pitch(blockDim.x * sizeof(V)),
+      : pitch(blockDim.x * sizeof(V)),
         at(0),
         columns((int)width),
         first(threadIdx.x * kVec),
-        step(blockDim.x * kVec) {}
-  __device__ __forceinline__ bool has(int k) const { return first + k * step < columns; }
-  __device__ __forceinline__ int column(int k) const { return first + k * step; }
+        step(blockDim.x * kVec) {
+    mine = smem + threadIdx.y * (kStages * group()) + threadIdx.x * sizeof(V);
+  }
+  // Bytes of a team's ring.
+  static size_t bytes(int threads) {
+    return (size_t)kStages * kRows * kPer * threads * sizeof(V);
+  }
   __device__ __forceinline__ int group() const { return kRows * kPer * pitch; }
+  __device__ __forceinline__ int column(int k) const { return first + k * step; }
+  __device__ __forceinline__ bool has(int k) const { return column(k) < columns; }
   // Starts the copy of source row i, given its first element, into the stage at
   // byte offset `to`.
-  __device__ __forceinline__ void copy(int to, int i, const T* row) const {
+  __device__ __forceinline__ void copy(int to, int i, const T* row) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (has(k))
-        async_copy(reinterpret_cast<V*>(mine + to + (i * kPer + k) * pitch), row + column(k));
+    for (int k = 0; k < kPer; ++k) {
+      if constexpr (kAsync) {
+        if (has(k))
+          async_copy(reinterpret_cast<V*>(mine + to + (i * kPer + k) * pitch), row + column(k));
+      } else {
+        // past the end the row's first element again: no branch parts the loads
+        pending[i * kPer + k] = *reinterpret_cast<const V*>(row + (has(k) ? column(k) : 0));
+      }
+    }
+  }
+  __device__ __forceinline__ void land(int to) const {
+    if constexpr (!kAsync) {
+#pragma unroll
+      for (int i = 0; i < kRows * kPer; ++i) *reinterpret_cast<V*>(mine + to + i * pitch) = pending[i];
+    }
+  }
+  // One group of copies ends; an empty one past the last row keeps the count.
+  __device__ __forceinline__ void commit() const {
+    if constexpr (kAsync) async_commit();
+  }
+  __device__ __forceinline__ void wait() const {
+    if constexpr (kAsync) async_wait<kStages - 1>();
   }
   // The stage to refill while this group is worked on: the one read a group ago.
   __device__ __forceinline__ int refill() const {
     return at == 0 ? (kStages - 1) * group() : at - group();
   }
-  __device__ __forceinline__ const V& read(int i, int k) const {
+  // The thread's k-th vector of source row i.
+  __device__ __forceinline__ V read(int i, int k) const {
     return *reinterpret_cast<const V*>(mine + at + (i * kPer + k) * pitch);
   }
   __device__ __forceinline__ void advance() {
@@ -226,99 +184,131 @@ struct Ring {
 
 constexpr int kSms = 152;
 
-// Stages that fit a multiprocessor with kBlocks blocks of kThreads threads: 200 KB,
-// from two to eight.
-template <int kRows, int kPer, int kThreads, int kBlocks>
-constexpr int kRingFit = 200 * 1024 / (kBlocks * kRows * kPer * kThreads * 16);
-template <int kRows, int kPer, int kThreads, int kBlocks>
-constexpr int kRingStages = kRingFit<kRows, kPer, kThreads, kBlocks> > 8   ? 8
-                            : kRingFit<kRows, kPer, kThreads, kBlocks> < 2 ? 2
-                                : kRingFit<kRows, kPer, kThreads, kBlocks>;
+// A shape of ring kernel: blocks of kThreads threads that hold kUnits times 16
+// bytes of each of a group's kRows rows, kBlocks of them a multiprocessor; as many stages as fit
+// 200 KB, up to eight.  Narrow rows take a team of fewer threads each, several teams
+// a block.
+template <int kUnits_, int kThreads_, int kBlocks_>
+struct Shape {
+  static constexpr int kUnits = kUnits_, kThreads = kThreads_, kBlocks = kBlocks_;
+  static constexpr int64_t kRowBytes = (int64_t)kUnits * kThreads * 16;
+};
+template <typename S, int kRows>
+constexpr int kFit = 200 * 1024 / (S::kBlocks * kRows * (int)S::kRowBytes);
+template <typename S, int kRows>
+constexpr int kStagesOf = kFit<S, kRows> > 8 ? 8 : kFit<S, kRows> < 2 ? 2 : kFit<S, kRows>;
 
 struct RingPlan {
-  int threads, each;  // each: blocks a multiprocessor
-  size_t stage;       // bytes
+  int threads, teams, blocks;  // of a team; of a block
 };
-
-// `each` blocks of `most` threads fit a multiprocessor; smaller ones in proportion.
-inline RingPlan ring_plan(int64_t vecs, int per, int most, int each, int rows, int vec_bytes) {
+// `groups` groups of rows of `row_bytes`; as many teams a block as it takes threads,
+// but blocks on every multiprocessor first.
+template <typename S>
+inline RingPlan ring_plan(int64_t row_bytes, int64_t groups) {
+  const int64_t units = (row_bytes + 15) / 16;
   RingPlan p;
-  p.threads = (int)((vecs + per - 1) / per + 31) / 32 * 32;
-  p.each = each * most / p.threads;
-  p.each = p.each > 16 ? 16 : p.each;
-  p.stage = (size_t)rows * per * p.threads * vec_bytes;
+  p.threads = (int)((units + S::kUnits - 1) / S::kUnits + 31) / 32 * 32;
+  const int64_t wanted = (groups + kSms * S::kBlocks - 1) / (kSms * S::kBlocks);
+  p.teams = S::kThreads / p.threads;
+  p.teams = p.teams < wanted ? p.teams : (int)wanted;
+  const int64_t blocks = (groups + p.teams - 1) / p.teams;
+  p.blocks = (int)(blocks < kSms * S::kBlocks ? blocks : kSms * S::kBlocks);
   return p;
 }
 
-// The norm of 16-byte vectors through the ring.
-template <typename T, int kVec, int kPer, int kThreads, int kBlocks, bool kCollapse>
-__global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_ring_kernel(const NormArgs A) {
+// The norm, one row at a time.  The mean is taken first and the variance from the
+// differences, so that a large mean costs no digits.  Weight and bias are kept in
+// registers where they fit beside the row (16 values a thread or fewer).
+template <typename T, int kVec, typename S, bool kCollapse>
+__global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(const NormArgs A) {
   begin_kernel();
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float part[2][32];
+  __shared__ float parts[8][2][32];  // of each team
+  float(&part)[2][32] = parts[threadIdx.y];
   constexpr int kRows = kCollapse ? kStreams : 1;
-  constexpr int kStages = kRingStages<kRows, kPer, kThreads, kBlocks>;
-  Ring<T, kVec, kPer, kRows, kStages> ring(smem, A.N);
-  const T* from = static_cast<const T*>(A.x) + blockIdx.x * A.x_stride;
-  const int64_t jump = gridDim.x * A.x_stride;
-  int64_t next = blockIdx.x;
+  constexpr int kPer = S::kUnits * 16 / (kVec * (int)sizeof(T));
+  using R = Ring<T, kVec, kPer, kRows, kStagesOf<S, kRows>>;
+  constexpr bool kKeep = kPer * kVec <= 16 && R::kAsync;
+  constexpr int kKept = kKeep ? kPer : 1;
+  R ring(smem, A.N);
+  const uint32_t M = (uint32_t)A.M, jump = gridDim.x * blockDim.y;
+  const uint32_t first = blockIdx.x * blockDim.y + threadIdx.y;
+  const T* from = static_cast<const T*>(A.x) + first * A.x_stride;
+  const int64_t x_jump = jump * A.x_stride;
+  uint32_t next = first;
   const auto fetch = [&](int to) {
-    if (next < A.M) {
+    if (next < M) {
 #pragma unroll
       for (int i = 0; i < kRows; ++i) ring.copy(to, i, from + i * A.N);
     }
-    async_commit();  // an empty group past the last row keeps the count
-    next += gridDim.x;
-    from += jump;
+    ring.commit();
+    next += jump;
+    from += x_jump;
   };
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) fetch(s * ring.group());
-  float w[kPer][kVec], b[kPer][kVec];
+  for (int s = 0; s < R::kStages - 1; ++s) {
+    fetch(s * ring.group());
+    ring.land(s * ring.group());
+  }
+  float w[kKept][kVec], b[kKept][kVec];
+  const auto load_params = [&](int k) {
+    load_param<T, kVec>(A.weight, A.p32, ring.column(k), 1.f, w[kKeep ? k : 0]);
+    load_param<T, kVec>(A.bias, A.p32, ring.column(k), 0.f, b[kKeep ? k : 0]);
+  };
+  if constexpr (kKeep) {
 #pragma unroll
-  for (int k = 0; k < kPer; ++k)
-    if (ring.has(k)) norm_params<T, kVec>(A, ring.column(k), w[k], b[k]);
+    for (int k = 0; k < kPer; ++k)
+      if (ring.has(k)) load_params(k);
+  }
   const float inv = 1.f / (float)A.N;
-  for (int64_t row = blockIdx.x; row < A.M; row += gridDim.x) {
+  for (uint32_t row = first; row < M; row += jump) {
     float pre[kStreams] = {};
     if constexpr (kCollapse) {
 #pragma unroll
-      for (int i = 0; i < kStreams; ++i) pre[i] = A.pre[row * kStreams + i];
+      for (int i = 0; i < kStreams; ++i) pre[i] = A.pre[(int64_t)row * kStreams + i];
     }
-    fetch(ring.refill());
-    async_wait<kStages - 1>();
+    const int to = ring.refill();
+    fetch(to);
+    ring.wait();
     float v[kPer][kVec];
     Acc acc;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       if (ring.has(k)) {
-        NormSource<T, kVec, kCollapse> raw;
+        Packed<T, kVec> s[kRows];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) raw.s[i] = ring.read(i, k);
-        raw.values(pre, v[k]);
+        for (int i = 0; i < kRows; ++i)
+          s[i] = ring.read(i, k);
+        norm_values<T, kVec, kCollapse>(s, pre, v[k]);
         acc.add(v[k]);
       }
     }
     float sum[1] = {acc.sum()};
-    block_sums_all<1>(sum, part[0]);
+    team_sums<1>(sum, part[0]);
     const float mean = sum[0] * inv;
+    if (kCollapse && A.h != nullptr) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (ring.has(k))
+          store_f32<T, kVec>(static_cast<T*>(A.h) + row * A.N + ring.column(k), v[k]);
+    }
     Acc square;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       if (ring.has(k)) {
-        if (kCollapse && A.h != nullptr)
-          store_f32<T, kVec>(static_cast<T*>(A.h) + row * A.N + ring.column(k), v[k]);
         vadd(v[k], -mean, v[k]);
         square.add(v[k], v[k]);
       }
     }
     float sq[1] = {square.sum()};
-    block_sums_all<1>(sq, part[1]);
+    team_sums<1>(sq, part[1]);
     const float rstd = 1.f / sqrtf(sq[0] * inv + A.eps);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       if (ring.has(k)) {
+        if (!kKeep) load_params(k);
         vmul(v[k], rstd, v[k]);
-        vfma(v[k], v[k], w[k], b[k]);
+        vfma(v[k], v[k], w[kKeep ? k : 0], b[kKeep ? k : 0]);
         store_f32<T, kVec>(static_cast<T*>(A.y) + row * A.N + ring.column(k), v[k]);
       }
     }
@@ -326,62 +316,65 @@ __global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_ring_kernel(cons
       if (A.mean != nullptr) A.mean[row] = mean;
       if (A.rstd != nullptr) A.rstd[row] = rstd;
     }
+    ring.land(to);
     ring.advance();
   }
 }
 
-template <typename T, int kVec, int kPer, int kThreads, int kBlocks, bool kCollapse>
-hcmix_status launch_norm_ring(const NormArgs& A, int64_t vecs, cudaStream_t stream) {
+template <typename T, int kVec, typename S, bool kCollapse>
+hcmix_status launch_norm_ring(const NormArgs& A, cudaStream_t stream) {
   constexpr int kRows = kCollapse ? kStreams : 1;
-  const RingPlan p = ring_plan(vecs, kPer, kThreads, kBlocks, kRows, kVec * (int)sizeof(T));
-  const size_t smem = kRingStages<kRows, kPer, kThreads, kBlocks> * p.stage;
-  const int64_t blocks = A.M < kSms * p.each ? A.M : kSms * p.each;
-  return launch(hcmix_norm_ring_kernel<T, kVec, kPer, kThreads, kBlocks, kCollapse>,
-                dim3((unsigned)blocks), p.threads, smem, stream, A);
+  const RingPlan p = ring_plan<S>(A.N * (int64_t)sizeof(T), A.M);
+  const size_t smem =
+      p.teams * Ring<T, kVec, S::kUnits * 16 / (kVec * (int)sizeof(T)), kRows,
+                     kStagesOf<S, kRows>>::bytes(p.threads);
+  return launch(hcmix_norm_kernel<T, kVec, S, kCollapse>, dim3(p.blocks),
+                dim3(p.threads, p.teams), smem, stream, A);
 }
 
-// The variant goes by type, alignment and width, never by the number of rows: a
-// row's result is the same bits in a call of one row and of many.
+// The shape goes by type, alignment and width, never by the number of rows: a row's
+// result is the same bits in a call of one row and of many.  The smallest that holds
+// the row is taken; 640 threads with four units of each of four streams would leave
+// room for one stage only.
 template <typename T, int kVec, bool kCollapse>
 hcmix_status launch_norm(const NormArgs& A, cudaStream_t stream) {
-  // vectors a thread and threads of the usual block: what a thread loads before it
-  // adds anything up (four streams' worth when collapsing) has to fit its registers
-  constexpr int kMost = (kVec == 1 ? 16 : 4) / (kCollapse ? 2 : 1);
-  constexpr int kThreads = kCollapse ? 512 : 256;
-  const int64_t vecs = (A.N + kVec - 1) / kVec;
-  const dim3 grid((unsigned)A.M);
-  const auto threads = [&](int per) { return (unsigned)((vecs + per - 1) / per + 31) / 32 * 32; };
-  if constexpr (kVec > 1) {
-    if (vecs <= 256) return launch_norm_ring<T, kVec, 1, 256, 4, kCollapse>(A, vecs, stream);
-    if (vecs <= 640) return launch_norm_ring<T, kVec, 2, 320, 2, kCollapse>(A, vecs, stream);
-    if (vecs <= 1024) return launch_norm_ring<T, kVec, 2, 512, 1, kCollapse>(A, vecs, stream);
+  using S1 = Shape<1, 256, 4>;
+  using S2 = Shape<2, 320, 2>;
+  using S3 = Shape<2, 640, 1>;
+  using S4 = Shape<4, 640, 1>;
+  using S5 = Shape<8, 640, 1>;   // of fp32, as many values a thread as S4's of 16 bits
+  using S6 = Shape<1, 1024, 1>;  // of single 16-bit elements, which wait in registers
+  const int64_t bytes = A.N * (int64_t)sizeof(T);
+  if (bytes <= S1::kRowBytes) return launch_norm_ring<T, kVec, S1, kCollapse>(A, stream);
+  if constexpr (kVec * sizeof(T) >= 4) {
+    if (bytes <= S2::kRowBytes) return launch_norm_ring<T, kVec, S2, kCollapse>(A, stream);
+    if (bytes <= S3::kRowBytes) return launch_norm_ring<T, kVec, S3, kCollapse>(A, stream);
+    if constexpr (!kCollapse) {
+      if (bytes <= S4::kRowBytes) return launch_norm_ring<T, kVec, S4, false>(A, stream);
+      if constexpr (sizeof(T) == 4)
+        if (bytes <= S5::kRowBytes) return launch_norm_ring<T, kVec, S5, false>(A, stream);
+    }
   } else {
-    if (vecs <= kThreads * kMost)
-      return launch(hcmix_norm_kernel<T, kVec, kMost, kThreads, kCollapse>, grid, threads(kMost), 0,
-                    stream, A);
+    if (bytes <= S6::kRowBytes) return launch_norm_ring<T, kVec, S6, kCollapse>(A, stream);
   }
-  if (vecs <= 1024 * kMost)
-    return launch(hcmix_norm_kernel<T, kVec, kMost, 1024, kCollapse>, grid, threads(kMost), 0,
-                  stream, A);
-  return launch(hcmix_norm_wide_kernel<T, kVec, kCollapse>, grid, 512, 0, stream, A);
+  return launch(hcmix_norm_wide_kernel<T, kVec, kCollapse>, dim3((unsigned)A.M), dim3(512), 0,
+                stream, A);
 }
 
 inline hcmix_status run_norm(const NormArgs& A, hcmix_type type, bool collapse,
                              cudaStream_t stream) {
-  const int n = size_of(type);
-  const bool wide = aligned_rows(A.x, A.x_stride, n) && aligned_rows(A.y, A.N, n) &&
-                    aligned_rows(A.h, A.N, n) && A.N * n % 16 == 0;
-  return with_type(type, [&](auto t) {
+  // a row's streams start N apart, whatever its stride
+  const int bytes = vector_bytes(size_of(type), {{A.x, A.x_stride}, {A.y, A.N}, {A.h, A.N}});
+  return with_vector(type, bytes, [&](auto t, auto vec, auto) {
     using T = decltype(t);
-    if (collapse)
-      return wide ? launch_norm<T, kWide<T>, true>(A, stream) : launch_norm<T, 1, true>(A, stream);
-    return wide ? launch_norm<T, kWide<T>, false>(A, stream) : launch_norm<T, 1, false>(A, stream);
+    constexpr int kVec = decltype(vec)::value;
+    return collapse ? launch_norm<T, kVec, true>(A, stream) : launch_norm<T, kVec, false>(A, stream);
   });
 }
 
 // ---------------------------------------------------------------- backward
 
-// dx, one block a row.
+// dx on its own, one block a row, the row passed over twice.
 template <typename T, int kVec>
 __global__ void __launch_bounds__(512) hcmix_norm_dx_kernel(const NormArgs A) {
   begin_kernel();
@@ -391,84 +384,100 @@ __global__ void __launch_bounds__(512) hcmix_norm_dx_kernel(const NormArgs A) {
   const T* dy = static_cast<const T*>(A.dy) + row * A.dy_stride;
   const float mean = A.mean[row], rstd = A.rstd[row];
   const int64_t step = (int64_t)blockDim.x * kVec, c0 = (int64_t)threadIdx.x * kVec;
-  float sum[2] = {0.f, 0.f}, v[kVec], g[kVec], w[kVec];
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) w[e] = 1.f;
+  float xh[kVec], t[kVec], w[kVec];
+  const auto load = [&](int64_t c) {
+    load_vec<T, kVec>(x + c).unpack(xh);
+    load_vec<T, kVec>(dy + c).unpack(t);
+    load_param<T, kVec>(A.weight, A.p32, c, 1.f, w);
+    vadd(xh, -mean, xh);
+    vmul(xh, rstd, xh);
+    vmul(t, t, w);
+  };
+  Acc acc[2];
+#pragma unroll 4
   for (int64_t c = c0; c < A.N; c += step) {
-    load_f32<T, kVec>(x + c, v);
-    load_f32<T, kVec>(dy + c, g);
-    if (A.weight != nullptr) load_param<T, kVec>(A.weight, A.p32, c, w);
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      const float t = g[e] * w[e];
-      sum[0] += t;
-      sum[1] = fmaf(t, (v[e] - mean) * rstd, sum[1]);
-    }
+    load(c);
+    acc[0].add(t);
+    acc[1].add(t, xh);
   }
-  block_sums_all<2>(sum, part);
+  float sum[2] = {acc[0].sum(), acc[1].sum()};
+  team_sums<2>(sum, part);
   const float inv = 1.f / (float)A.N;
   const float c1 = sum[0] * inv, c2 = sum[1] * inv;
+#pragma unroll 4
   for (int64_t c = c0; c < A.N; c += step) {
-    load_f32<T, kVec>(x + c, v);
-    load_f32<T, kVec>(dy + c, g);
-    if (A.weight != nullptr) load_param<T, kVec>(A.weight, A.p32, c, w);
+    load(c);
+    vadd(t, -c1, t);
+    vfma(t, -c2, xh, t);
+    vmul(t, rstd, t);
+    store_f32<T, kVec>(static_cast<T*>(A.dx) + row * A.N + c, t);
+  }
+}
+
+// A thread's vector of the partial sums of the weight's and bias's gradient: on 16
+// bytes in the workspace too where the vectors are 16 bytes.
+template <typename T, int kVec>
+__device__ __forceinline__ void store_partial(float* out, const float (&v)[kVec]) {
+  constexpr int kQuad = kVec % 4 == 0 ? 4 : 1;
 #pragma unroll
-    for (int e = 0; e < kVec; ++e)
-      v[e] = rstd * (fmaf(g[e], w[e], -c1) - (v[e] - mean) * rstd * c2);
-    store_f32<T, kVec>(static_cast<T*>(A.dx) + row * A.N + c, v);
+  for (int e = 0; e < kVec; e += kQuad) {
+    float q[kQuad];
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i) q[i] = v[e + i];
+    store_f32<float, kQuad>(out + e, q);
   }
 }
 
 constexpr int kColumnThreads = 128;
 
-// Partial sums of the weight's and bias's gradient: block (b, s) takes columns
-// from b * kColumnThreads * kVec and rows s, s + slabs, ...
+// Partial sums of the weight's and bias's gradient on their own: block (b, s) takes
+// columns from b * kColumnThreads * kVec and rows s, s + slabs, ...
 template <typename T, int kVec>
 __global__ void __launch_bounds__(kColumnThreads) hcmix_norm_columns_kernel(const NormArgs A) {
   begin_kernel();
   const int64_t c = ((int64_t)blockIdx.x * kColumnThreads + threadIdx.x) * kVec;
   if (c >= A.N) return;
   float dw[kVec] = {}, db[kVec] = {};
+#pragma unroll 4
   for (int64_t row = blockIdx.y; row < A.M; row += gridDim.y) {
     float v[kVec], g[kVec];
-    load_f32<T, kVec>(static_cast<const T*>(A.x) + row * A.x_stride + c, v);
-    load_f32<T, kVec>(static_cast<const T*>(A.dy) + row * A.dy_stride + c, g);
-    const float mean = A.mean[row], rstd = A.rstd[row];
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      dw[e] = fmaf(g[e], (v[e] - mean) * rstd, dw[e]);
-      db[e] += g[e];
-    }
+    load_vec<T, kVec>(static_cast<const T*>(A.x) + row * A.x_stride + c).unpack(v);
+    load_vec<T, kVec>(static_cast<const T*>(A.dy) + row * A.dy_stride + c).unpack(g);
+    vadd(v, -A.mean[row], v);
+    vmul(v, A.rstd[row], v);
+    vfma(dw, g, v, dw);
+    vadd(db, g, db);
   }
-  float* part = A.part + (int64_t)blockIdx.y * 2 * A.N + c;
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) {
-    part[e] = dw[e];
-    part[A.N + e] = db[e];
-  }
+  float* out = A.part + (int64_t)blockIdx.y * 2 * A.N + c;
+  store_partial<T, kVec>(out, dw);
+  store_partial<T, kVec>(out + A.N, db);
 }
 
 // dx and the partial sums of the weight's and bias's gradient in one pass over x
-// and dy, through the ring; a block works on kGroup rows at a time, with one
-// barrier for all their sums.  A thread keeps dweight and dbias of its columns in
-// registers.  With one vector a thread (kPer 1) weight, (x - mean) rstd and
-// dy weight stay there too; with more they are read and worked out again, from
-// L1 and the stage.
-template <typename T, int kVec, int kPer, int kGroup, int kThreads, int kBlocks>
-__global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_backward_kernel(const NormArgs A) {
+// and dy, through the ring; a team works on kGroup rows at a time, with one barrier
+// for all their sums.  A thread keeps dweight and dbias of its columns in registers;
+// with one unit a thread (x - mean) rstd and dy weight stay there too, with more
+// they are read and worked out again from the stage, and the weight fits with two.
+template <typename T, int kVec, typename S, int kGroup>
+__global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_kernel(
+    const NormArgs A) {
   begin_kernel();
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float part[2][2 * kGroup * 32];
-  constexpr bool kKeep = kPer == 1;
-  constexpr int kKept = kKeep ? kGroup : 1;
-  constexpr int kStages = kRingStages<2 * kGroup, kPer, kThreads, kBlocks>;
-  Ring<T, kVec, kPer, 2 * kGroup, kStages> ring(smem, A.N);
-  const T* x = static_cast<const T*>(A.x) + blockIdx.x * kGroup * A.x_stride;
-  const T* dy = static_cast<const T*>(A.dy) + blockIdx.x * kGroup * A.dy_stride;
-  const int64_t x_jump = gridDim.x * kGroup * A.x_stride;
-  const int64_t dy_jump = gridDim.x * kGroup * A.dy_stride;
-  const int M = (int)A.M, jump = gridDim.x * kGroup;
-  int64_t next = blockIdx.x * kGroup;
+  __shared__ float parts[8][2][2 * kGroup * 32];  // of each team
+  float(&part)[2][2 * kGroup * 32] = parts[threadIdx.y];
+  constexpr int kPer = S::kUnits * 16 / (kVec * (int)sizeof(T));
+  using R = Ring<T, kVec, kPer, 2 * kGroup, kStagesOf<S, 2 * kGroup>>;
+  constexpr bool kKeepRow = S::kUnits == 1 && R::kAsync;
+  constexpr bool kKeepWeight = S::kUnits <= (R::kAsync ? 2 : 1);
+  constexpr int kRowsKept = kKeepRow ? kGroup : 1, kKept = kKeepRow ? kPer : 1;
+  constexpr int kWeightsKept = kKeepWeight ? kPer : 1;
+  R ring(smem, A.N);
+  const uint32_t M = (uint32_t)A.M, jump = gridDim.x * blockDim.y * kGroup;
+  const uint32_t first = (blockIdx.x * blockDim.y + threadIdx.y) * kGroup;
+  const T* x = static_cast<const T*>(A.x) + first * A.x_stride;
+  const T* dy = static_cast<const T*>(A.dy) + first * A.dy_stride;
+  const int64_t x_jump = jump * A.x_stride, dy_jump = jump * A.dy_stride;
+  uint32_t next = first;
   const auto fetch = [&](int to) {
 #pragma unroll
     for (int r = 0; r < kGroup; ++r) {
@@ -477,25 +486,29 @@ __global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_backward_kernel(
         ring.copy(to, 2 * r + 1, dy + r * A.dy_stride);
       }
     }
-    async_commit();  // an empty group past the last row keeps the count
+    ring.commit();
     next += jump;
     x += x_jump;
     dy += dy_jump;
   };
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) fetch(s * ring.group());
-  float dw[kPer][kVec] = {}, db[kPer][kVec] = {}, w[kVec];
+  for (int s = 0; s < R::kStages - 1; ++s) {
+    fetch(s * ring.group());
+    ring.land(s * ring.group());
+  }
+  float dw[kPer][kVec] = {}, db[kPer][kVec] = {}, w[kWeightsKept][kVec];
   const auto load_weight = [&](int k) {
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) w[e] = 1.f;
-    if (A.weight != nullptr && ring.has(k))
-      load_param<T, kVec>(A.weight, A.p32, ring.column(k), w);
+    if (ring.has(k))
+      load_param<T, kVec>(A.weight, A.p32, ring.column(k), 1.f, w[kKeepWeight ? k : 0]);
   };
-  if (kKeep) load_weight(0);
+  if constexpr (kKeepWeight) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) load_weight(k);
+  }
   const float inv = 1.f / (float)A.N;
   int odd = 0;
   float next_mean[kGroup], next_rstd[kGroup];
-  const auto fetch_stats = [&](int64_t row) {
+  const auto fetch_stats = [&](uint32_t row) {
 #pragma unroll
     for (int r = 0; r < kGroup; ++r) {
       if (row + r < M) {
@@ -504,23 +517,24 @@ __global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_backward_kernel(
       }
     }
   };
-  fetch_stats(next - (int64_t)(kStages - 1) * jump);
-  for (int64_t row = blockIdx.x * kGroup; row < M; row += jump, odd ^= 1) {
+  fetch_stats(first);
+  for (uint32_t row = first; row < M; row += jump, odd ^= 1) {
     float mean[kGroup], rstd[kGroup];
 #pragma unroll
     for (int r = 0; r < kGroup; ++r) mean[r] = next_mean[r], rstd[r] = next_rstd[r];
     fetch_stats(row + jump);
-    fetch(ring.refill());
-    async_wait<kStages - 1>();
-    float xh[kKept][kVec], t[kKept][kVec], g[kVec];
+    const int to = ring.refill();
+    fetch(to);
+    ring.wait();
+    float xh[kRowsKept][kKept][kVec], t[kRowsKept][kKept][kVec], g[kVec];
     const auto load_row = [&](int r, int k) {
-      const int q = kKeep ? r : 0;
-      ring.read(2 * r, k).unpack(xh[q]);
+      float(&h)[kVec] = xh[kKeepRow ? r : 0][kKeepRow ? k : 0];
+      ring.read(2 * r, k).unpack(h);
       ring.read(2 * r + 1, k).unpack(g);
-      if (!kKeep) load_weight(k);
-      vadd(xh[q], -mean[r], xh[q]);
-      vmul(xh[q], rstd[r], xh[q]);
-      vmul(t[q], g, w);
+      if (!kKeepWeight) load_weight(k);
+      vadd(h, -mean[r], h);
+      vmul(h, rstd[r], h);
+      vmul(t[kKeepRow ? r : 0][kKeepRow ? k : 0], g, w[kKeepWeight ? k : 0]);
     };
     float sums[2 * kGroup];
 #pragma unroll
@@ -529,51 +543,70 @@ __global__ void __launch_bounds__(kThreads, kBlocks) hcmix_norm_backward_kernel(
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         if (ring.has(k) && row + r < M) {
-          const int q = kKeep ? r : 0;
           load_row(r, k);
-          vfma(dw[k], g, xh[q], dw[k]);
+          const float(&h)[kVec] = xh[kKeepRow ? r : 0][kKeepRow ? k : 0];
+          const float(&d)[kVec] = t[kKeepRow ? r : 0][kKeepRow ? k : 0];
+          vfma(dw[k], g, h, dw[k]);
           vadd(db[k], g, db[k]);
-          acc[0].add(t[q]);
-          acc[1].add(t[q], xh[q]);
+          acc[0].add(d);
+          acc[1].add(d, h);
         }
       }
       sums[2 * r] = acc[0].sum();
       sums[2 * r + 1] = acc[1].sum();
     }
     // two groups apart, a barrier lies between the uses of `part`
-    block_sums_all<2 * kGroup>(sums, part[odd]);
+    team_sums<2 * kGroup>(sums, part[odd]);
 #pragma unroll
     for (int r = 0; r < kGroup; ++r) {
       const float c1 = sums[2 * r] * inv, c2 = sums[2 * r + 1] * inv;
+      T* dx = static_cast<T*>(A.dx) + (int64_t)(row + r) * A.N;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         if (ring.has(k) && row + r < M) {
-          const int q = kKeep ? r : 0;
-          if (!kKeep) load_row(r, k);
-          vadd(t[q], -c1, t[q]);
-          vfma(t[q], -c2, xh[q], t[q]);
-          vmul(t[q], rstd[r], t[q]);
-          store_f32<T, kVec>(static_cast<T*>(A.dx) + (row + r) * A.N + ring.column(k), t[q]);
+          if (!kKeepRow) load_row(r, k);
+          float(&d)[kVec] = t[kKeepRow ? r : 0][kKeepRow ? k : 0];
+          vadd(d, -c1, d);
+          vfma(d, -c2, xh[kKeepRow ? r : 0][kKeepRow ? k : 0], d);
+          vmul(d, rstd[r], d);
+          store_f32<T, kVec>(dx + ring.column(k), d);
         }
       }
     }
+    ring.land(to);
     ring.advance();
   }
   float* out = A.part + (int64_t)blockIdx.x * 2 * A.N;
+  if (blockDim.y == 1) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (ring.has(k)) {
+        store_partial<T, kVec>(out + ring.column(k), dw[k]);
+        store_partial<T, kVec>(out + A.N + ring.column(k), db[k]);
+      }
+    }
+    return;
+  }
+  // the teams' sums added up in order, through the rings' memory
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(smem);
+  float* own = sums + threadIdx.y * 2 * ring.columns;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     if (ring.has(k)) {
-      // the workspace is aligned, and so are whole vectors' columns
-      constexpr int kQuad = kVec % 4 == 0 ? 4 : 1;
 #pragma unroll
-      for (int e = 0; e < kVec; e += kQuad) {
-        float q[kQuad], p[kQuad];
-#pragma unroll
-        for (int i = 0; i < kQuad; ++i) q[i] = dw[k][e + i], p[i] = db[k][e + i];
-        store_f32<float, kQuad>(out + ring.column(k) + e, q);
-        store_f32<float, kQuad>(out + A.N + ring.column(k) + e, p);
+      for (int e = 0; e < kVec; ++e) {
+        own[ring.column(k) + e] = dw[k][e];
+        own[ring.columns + ring.column(k) + e] = db[k][e];
       }
     }
+  }
+  __syncthreads();
+  for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 2 * ring.columns;
+       i += blockDim.x * blockDim.y) {
+    float s = 0.f;
+    for (int team = 0; team < (int)blockDim.y; ++team) s += sums[team * 2 * ring.columns + i];
+    out[i] = s;
   }
 }
 
@@ -598,85 +631,87 @@ __global__ void __launch_bounds__(32 * kJoinGroups) hcmix_norm_join_kernel(const
   (c < A.N ? A.dweight[c] : A.dbias[c - A.N]) = s;
 }
 
-// How a backward call runs.
+using Back1 = Shape<1, 256, 3>;
+using Back2 = Shape<1, 640, 1>;
+using Back3 = Shape<2, 640, 1>;
+using Back4 = Shape<4, 640, 1>;
+
+// How a backward call runs: its shape (1 to 4; 0: dx and the column sums by separate
+// kernels) and its blocks, two rows at a time in the first two shapes.
 struct NormPlan {
-  int variant;  // of launch_norm_backward; 0: dx and the column sums by separate kernels
-  int blocks;   // partial rows of the column sums
+  int shape;
   RingPlan ring;
 };
 
-// The same for every call of a size and type, so that the workspace can be sized
-// before the operands are known; rows of 16-byte vectors (`wide`) go through the
-// ring, and so do unaligned fp32 ones, element by element.
-inline NormPlan norm_plan(int size, bool wide, int64_t M, int64_t N) {
+// `bytes`: of a vector.
+inline NormPlan norm_plan(int size, int bytes, int64_t M, int64_t N) {
   NormPlan p = {};
-  const int vec = wide ? 16 / size : 1;
-  const int64_t vecs = (N + vec - 1) / vec;
-  const int per[5] = {0, 1, 1, 2, 4}, most[5] = {0, 256, 640, 640, 640}, each[5] = {0, 3, 1, 1, 1};
-  const int group[5] = {0, 2, 2, 1, 1};  // rows at a time
-  if (vec * size >= 4 && M > 0)
-    for (int v = 1; v < 5 && p.variant == 0; ++v)
-      if (vecs <= per[v] * most[v]) p.variant = v;
-  if (p.variant == 0) {
-    p.blocks = (int)(M < 64 ? M : 64);
-    return p;
-  }
-  const int v = p.variant;
-  p.ring = ring_plan(vecs, per[v], most[v], each[v], 2 * group[v], vec * size);
-  const int64_t groups = (M + group[v] - 1) / group[v];
-  p.blocks = (int)(groups < kSms * p.ring.each ? groups : kSms * p.ring.each);
+  const int64_t row = N * size, pairs = (M + 1) / 2;
+  const bool async = bytes >= 4;  // else rows in flight take registers
+  if (M == 0) return p;
+  if (row <= Back1::kRowBytes) p.shape = 1, p.ring = ring_plan<Back1>(row, async ? pairs : M);
+  else if (row <= Back2::kRowBytes) p.shape = 2, p.ring = ring_plan<Back2>(row, async ? pairs : M);
+  else if (row <= Back3::kRowBytes) p.shape = 3, p.ring = ring_plan<Back3>(row, M);
+  else if (row <= Back4::kRowBytes && async) p.shape = 4, p.ring = ring_plan<Back4>(row, M);
+  else p.ring.blocks = (int)(M < 64 ? M : 64);
   return p;
 }
 
-// The larger of the two alignments' needs.
+// The workspace is sized before the operands' alignment is known: the largest need.
 inline size_t norm_workspace(int size, int64_t M, int64_t N) {
-  const int a = norm_plan(size, true, M, N).blocks, b = norm_plan(size, false, M, N).blocks;
-  return ((size_t)(a > b ? a : b) * 2 * (size_t)N * 4 + 255) / 256 * 256;
+  int most = 0;
+  for (int bytes : {16, 4, size}) {
+    const int b = norm_plan(size, bytes, M, N).ring.blocks;
+    most = b > most ? b : most;
+  }
+  return ((size_t)most * 2 * (size_t)N * 4 + 255) / 256 * 256;
 }
 
-template <typename T, int kVec, int kPer, int kGroup, int kThreads, int kBlocks>
+template <typename T, int kVec, typename S, int kMostGroup>
 hcmix_status launch_norm_backward_ring(const NormArgs& A, const RingPlan& p, cudaStream_t stream) {
-  const size_t smem = kRingStages<2 * kGroup, kPer, kThreads, kBlocks> * p.stage;
-  return launch(hcmix_norm_backward_kernel<T, kVec, kPer, kGroup, kThreads, kBlocks>,
-                dim3(A.blocks), p.threads, smem, stream, A);
+  constexpr int kGroup = kVec * sizeof(T) >= 4 ? kMostGroup : 1;
+  using R = Ring<T, kVec, S::kUnits * 16 / (kVec * (int)sizeof(T)), 2 * kGroup,
+                 kStagesOf<S, 2 * kGroup>>;
+  return launch(hcmix_norm_backward_kernel<T, kVec, S, kGroup>, dim3(p.blocks),
+                dim3(p.threads, p.teams), p.teams * R::bytes(p.threads), stream, A);
 }
 
 template <typename T, int kVec>
 hcmix_status launch_norm_backward(NormArgs A, cudaStream_t stream) {
-  const NormPlan p = norm_plan(sizeof(T), kVec > 1, A.M, A.N);
-  A.blocks = p.blocks;
+  const NormPlan p = norm_plan(sizeof(T), kVec * sizeof(T), A.M, A.N);
+  A.blocks = p.ring.blocks;
   hcmix_status st = HCMIX_OK;
-  if (A.dweight == nullptr || p.variant == 0) {
+  if (A.dweight == nullptr || p.shape == 0) {
     const int64_t vecs = (A.N + kVec - 1) / kVec;
     const unsigned threads = vecs >= 256 ? 256 : (unsigned)(vecs + 31) / 32 * 32;
     if (A.M > 0)
-      st = launch(hcmix_norm_dx_kernel<T, kVec>, dim3((unsigned)A.M), threads, 0, stream, A);
+      st = launch(hcmix_norm_dx_kernel<T, kVec>, dim3((unsigned)A.M), dim3(threads), 0, stream, A);
     if (st != HCMIX_OK || A.dweight == nullptr) return st;
     const int64_t per = (int64_t)kColumnThreads * kVec;
-    if (p.blocks > 0)
+    if (A.blocks > 0)
       st = launch(hcmix_norm_columns_kernel<T, kVec>,
-                  dim3((unsigned)((A.N + per - 1) / per), p.blocks), kColumnThreads, 0, stream, A);
-  } else if constexpr (kVec * sizeof(T) >= 4) {
-    switch (p.variant) {
-      case 1: st = launch_norm_backward_ring<T, kVec, 1, 2, 256, 3>(A, p.ring, stream); break;
-      case 2: st = launch_norm_backward_ring<T, kVec, 1, 2, 640, 1>(A, p.ring, stream); break;
-      case 3: st = launch_norm_backward_ring<T, kVec, 2, 1, 640, 1>(A, p.ring, stream); break;
-      default: st = launch_norm_backward_ring<T, kVec, 4, 1, 640, 1>(A, p.ring, stream); break;
+                  dim3((unsigned)((A.N + per - 1) / per), A.blocks), dim3(kColumnThreads), 0,
+                  stream, A);
+  } else {
+    switch (p.shape) {
+      case 1: st = launch_norm_backward_ring<T, kVec, Back1, 2>(A, p.ring, stream); break;
+      case 2: st = launch_norm_backward_ring<T, kVec, Back2, 2>(A, p.ring, stream); break;
+      case 3: st = launch_norm_backward_ring<T, kVec, Back3, 1>(A, p.ring, stream); break;
+      default:
+        if constexpr (kVec * sizeof(T) >= 4)
+          st = launch_norm_backward_ring<T, kVec, Back4, 1>(A, p.ring, stream);
     }
   }
   if (st != HCMIX_OK) return st;
-  return launch(hcmix_norm_join_kernel, dim3((unsigned)((2 * A.N + 31) / 32)), 32 * kJoinGroups, 0,
-                stream, A);
+  return launch(hcmix_norm_join_kernel, dim3((unsigned)((2 * A.N + 31) / 32)),
+                dim3(32 * kJoinGroups), 0, stream, A);
 }
 
 inline hcmix_status run_norm_backward(const NormArgs& A, hcmix_type type, cudaStream_t stream) {
-  const int n = size_of(type);
-  const bool wide = aligned_rows(A.x, A.x_stride, n) && aligned_rows(A.dy, A.dy_stride, n) &&
-                    aligned_rows(A.dx, A.N, n) && A.N * n % 16 == 0;
-  return with_type(type, [&](auto t) {
-    using T = decltype(t);
-    return wide ? launch_norm_backward<T, kWide<T>>(A, stream)
-                : launch_norm_backward<T, 1>(A, stream);
+  const int bytes =
+      vector_bytes(size_of(type), {{A.x, A.x_stride}, {A.dy, A.dy_stride}, {A.dx, A.N}});
+  return with_vector(type, bytes, [&](auto t, auto vec, auto) {
+    return launch_norm_backward<decltype(t), decltype(vec)::value>(A, stream);
   });
 }
 

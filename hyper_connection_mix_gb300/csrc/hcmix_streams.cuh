@@ -20,53 +20,68 @@ struct StreamsArgs {
   int chunks;  // thread blocks across a row (forward kernels)
 };
 
-template <typename T, int kVec>
+// A thread's first column in the chunk-th block across a row.
+template <int kVec, int kU>
+__device__ __forceinline__ int64_t first_column(int chunk) {
+  return ((int64_t)chunk * kU * blockDim.x + threadIdx.x) * kVec;
+}
+
+template <typename T, int kVec, int kU>
 __global__ void __launch_bounds__(256) hcmix_collapse_kernel(const StreamsArgs A) {
   begin_kernel();
   const int64_t row = blockIdx.x / A.chunks;
-  const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * blockDim.x + threadIdx.x) * kVec;
+  const int64_t c = first_column<kVec, kU>(blockIdx.x % A.chunks);
+  const int step = blockDim.x * kVec;
   if (c >= A.D) return;
-  const T* x = static_cast<const T*>(A.x) + row * A.x_stride + c;
-  float h[kVec] = {};
+  const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
+  Cols<T, kVec, kU> px[kStreams];
+#pragma unroll
+  for (int i = 0; i < kStreams; ++i) px[i].load(x + i * A.D, c, step, A.D);
+  float h[kU * kVec] = {};
 #pragma unroll
   for (int i = 0; i < kStreams; ++i) {
-    float v[kVec];
-    load_f32<T, kVec>(x + i * A.D, v);
-    const float w = A.pre[row * kStreams + i];
-    vfma(h, w, v, h);
+    float v[kU * kVec];
+    px[i].unpack(v);
+    vfma(h, A.pre[row * kStreams + i], v, h);
   }
-  store_f32<T, kVec>(static_cast<T*>(A.out) + row * A.D + c, h);
+  store_cols<T, kVec, kU>(static_cast<T*>(A.out) + row * A.D, c, step, A.D, h);
 }
 
-template <typename T, int kVec>
+template <typename T, int kVec, int kU>
 __global__ void __launch_bounds__(256) hcmix_expand_kernel(const StreamsArgs A) {
   begin_kernel();
   const int64_t row = blockIdx.x / A.chunks;
-  const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * blockDim.x + threadIdx.x) * kVec;
+  const int64_t c = first_column<kVec, kU>(blockIdx.x % A.chunks);
+  const int step = blockDim.x * kVec;
   if (c >= A.D) return;
-  const T* x = static_cast<const T*>(A.x) + row * A.x_stride + c;
+  const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
   const float* comb = A.comb + row * kStreams * kStreams;
-  float v[kStreams][kVec], y[kVec];
+  Cols<T, kVec, kU> px[kStreams], py;
 #pragma unroll
-  for (int j = 0; j < kStreams; ++j) load_f32<T, kVec>(x + j * A.D, v[j]);
-  load_f32<T, kVec>(static_cast<const T*>(A.y) + row * A.y_stride + c, y);
+  for (int j = 0; j < kStreams; ++j) px[j].load(x + j * A.D, c, step, A.D);
+  py.load(static_cast<const T*>(A.y) + row * A.y_stride, c, step, A.D);
+  float v[kStreams][kU * kVec], y[kU * kVec];
+#pragma unroll
+  for (int j = 0; j < kStreams; ++j) px[j].unpack(v[j]);
+  py.unpack(y);
+  T* out = static_cast<T*>(A.out) + row * kStreams * A.D;
 #pragma unroll
   for (int i = 0; i < kStreams; ++i) {
-    const float p = A.post[row * kStreams + i];
-    float o[kVec];
-    vmul(o, p, y);
+    float o[kU * kVec];
+    vmul(o, A.post[row * kStreams + i], y);
 #pragma unroll
     for (int j = 0; j < kStreams; ++j) vfma(o, comb[i * kStreams + j], v[j], o);
-    store_f32<T, kVec>(static_cast<T*>(A.out) + row * kStreams * A.D + i * A.D + c, o);
+    store_cols<T, kVec, kU>(out + i * A.D, c, step, A.D, o);
   }
 }
 
 // One block a row: the row's four dot products need all of its columns.
-template <typename T, int kVec>
+template <typename T, int kVec, int kU>
 __global__ void __launch_bounds__(256) hcmix_collapse_backward_kernel(const StreamsArgs A) {
   begin_kernel();
   __shared__ float part[kStreams * 32];
   const int64_t row = blockIdx.x;
+  const int step = blockDim.x * kVec;
   const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
   const T* g = static_cast<const T*>(A.g) + row * A.g_stride;
   const T* add = static_cast<const T*>(A.add) + row * A.add_stride;
@@ -75,20 +90,20 @@ __global__ void __launch_bounds__(256) hcmix_collapse_backward_kernel(const Stre
   Acc dot[kStreams];
 #pragma unroll
   for (int i = 0; i < kStreams; ++i) pre[i] = A.pre[row * kStreams + i];
-  for (int64_t c = (int64_t)threadIdx.x * kVec; c < A.D; c += blockDim.x * kVec) {
-    Packed<T, kVec> px[kStreams], pa[kStreams];
-    const Packed<T, kVec> pg = load_vec<T, kVec>(g + c);
+  for (int64_t c = first_column<kVec, kU>(0); c < A.D; c += kU * step) {
+    Cols<T, kVec, kU> px[kStreams], pa[kStreams], pg;
+    pg.load(g, c, step, A.D);
 #pragma unroll
-    for (int i = 0; i < kStreams; ++i) px[i] = load_vec<T, kVec>(x + i * A.D + c);
+    for (int i = 0; i < kStreams; ++i) px[i].load(x + i * A.D, c, step, A.D);
     if (A.add != nullptr) {
 #pragma unroll
-      for (int i = 0; i < kStreams; ++i) pa[i] = load_vec<T, kVec>(add + i * A.D + c);
+      for (int i = 0; i < kStreams; ++i) pa[i].load(add + i * A.D, c, step, A.D);
     }
-    float dh[kVec];
+    float dh[kU * kVec];
     pg.unpack(dh);
 #pragma unroll
     for (int i = 0; i < kStreams; ++i) {
-      float v[kVec], d[kVec];
+      float v[kU * kVec], d[kU * kVec];
       px[i].unpack(v);
       dot[i].add(dh, v);
       if (A.add != nullptr) {
@@ -97,7 +112,7 @@ __global__ void __launch_bounds__(256) hcmix_collapse_backward_kernel(const Stre
       } else {
         vmul(d, pre[i], dh);
       }
-      store_f32<T, kVec>(dx + i * A.D + c, d);
+      store_cols<T, kVec, kU>(dx + i * A.D, c, step, A.D, d);
     }
   }
   float sums[kStreams];
@@ -108,12 +123,13 @@ __global__ void __launch_bounds__(256) hcmix_collapse_backward_kernel(const Stre
 }
 
 // One block a row, as above; 4 + 16 dot products.
-template <typename T, int kVec>
+template <typename T, int kVec, int kU>
 __global__ void __launch_bounds__(256, 2) hcmix_expand_backward_kernel(const StreamsArgs A) {
   begin_kernel();
   constexpr int kDots = kStreams + kStreams * kStreams;
   __shared__ float part[kDots * 32];
   const int64_t row = blockIdx.x;
+  const int step = blockDim.x * kVec;
   const T* x = static_cast<const T*>(A.x) + row * A.x_stride;
   const T* y = static_cast<const T*>(A.y) + row * A.y_stride;
   const T* g = static_cast<const T*>(A.g) + row * A.g_stride;
@@ -128,14 +144,14 @@ __global__ void __launch_bounds__(256, 2) hcmix_expand_backward_kernel(const Str
     for (int j = 0; j < kStreams; ++j)
       comb[i][j] = A.comb[(row * kStreams + i) * kStreams + j];
   }
-  for (int64_t c = (int64_t)threadIdx.x * kVec; c < A.D; c += blockDim.x * kVec) {
-    Packed<T, kVec> pg[kStreams], px[kStreams];
+  for (int64_t c = first_column<kVec, kU>(0); c < A.D; c += kU * step) {
+    Cols<T, kVec, kU> pg[kStreams], px[kStreams], py;
 #pragma unroll
-    for (int i = 0; i < kStreams; ++i) pg[i] = load_vec<T, kVec>(g + i * A.D + c);
-    const Packed<T, kVec> py = load_vec<T, kVec>(y + c);
+    for (int i = 0; i < kStreams; ++i) pg[i].load(g + i * A.D, c, step, A.D);
+    py.load(y, c, step, A.D);
 #pragma unroll
-    for (int i = 0; i < kStreams; ++i) px[i] = load_vec<T, kVec>(x + i * A.D + c);
-    float d[kStreams][kVec], v[kVec], o[kVec] = {};
+    for (int i = 0; i < kStreams; ++i) px[i].load(x + i * A.D, c, step, A.D);
+    float d[kStreams][kU * kVec], v[kU * kVec], o[kU * kVec] = {};
     py.unpack(v);
 #pragma unroll
     for (int i = 0; i < kStreams; ++i) {
@@ -143,7 +159,7 @@ __global__ void __launch_bounds__(256, 2) hcmix_expand_backward_kernel(const Str
       vfma(o, post[i], d[i], o);
       dot[i].add(d[i], v);
     }
-    store_f32<T, kVec>(dy + c, o);
+    store_cols<T, kVec, kU>(dy, c, step, A.D, o);
 #pragma unroll
     for (int j = 0; j < kStreams; ++j) {
       px[j].unpack(v);
@@ -152,7 +168,7 @@ __global__ void __launch_bounds__(256, 2) hcmix_expand_backward_kernel(const Str
       for (int i = 1; i < kStreams; ++i) vfma(o, comb[i][j], d[i], o);
 #pragma unroll
       for (int i = 0; i < kStreams; ++i) dot[kStreams + i * kStreams + j].add(d[i], v);
-      store_f32<T, kVec>(dx + j * A.D + c, o);
+      store_cols<T, kVec, kU>(dx + j * A.D, c, step, A.D, o);
     }
   }
   float sums[kDots];
@@ -166,35 +182,34 @@ __global__ void __launch_bounds__(256, 2) hcmix_expand_backward_kernel(const Str
 
 enum class StreamsOp { kCollapse, kExpand, kCollapseBackward, kExpandBackward };
 
-template <typename T, int kVec>
+template <typename T, int kVec, int kU>
 hcmix_status launch_streams(StreamsOp op, StreamsArgs A, cudaStream_t stream) {
-  const int64_t vecs = (A.D + kVec - 1) / kVec;
+  // a row in as many equal parts as blocks of 256 threads need: blocks, or the steps
+  // of one block
+  const int64_t shares = (A.D + kVec * kU - 1) / (kVec * kU);
+  const int64_t parts = (shares + 255) / 256;
+  const unsigned threads = (unsigned)((shares + parts - 1) / parts + 31) / 32 * 32;
   if (op == StreamsOp::kCollapse || op == StreamsOp::kExpand) {
-    A.chunks = (int)((vecs + 255) / 256);
-    const int threads = (int)((vecs + A.chunks - 1) / A.chunks + 31) / 32 * 32;
+    A.chunks = (int)parts;
     const int64_t blocks = A.M * A.chunks;
     if (blocks >= ((int64_t)1 << 31)) return HCMIX_ERR_UNSUPPORTED;
-    return launch(op == StreamsOp::kCollapse ? hcmix_collapse_kernel<T, kVec>
-                                             : hcmix_expand_kernel<T, kVec>,
-                  dim3((unsigned)blocks), threads, 0, stream, A);
+    return launch(op == StreamsOp::kCollapse ? hcmix_collapse_kernel<T, kVec, kU>
+                                             : hcmix_expand_kernel<T, kVec, kU>,
+                  dim3((unsigned)blocks), dim3(threads), 0, stream, A);
   }
-  // as many equal steps through the row as blocks of 256 threads need
-  const int64_t steps = (vecs + 255) / 256;
-  const int threads = (int)((vecs + steps - 1) / steps + 31) / 32 * 32;
-  return launch(op == StreamsOp::kCollapseBackward ? hcmix_collapse_backward_kernel<T, kVec>
-                                                   : hcmix_expand_backward_kernel<T, kVec>,
-                dim3((unsigned)A.M), threads, 0, stream, A);
+  return launch(op == StreamsOp::kCollapseBackward ? hcmix_collapse_backward_kernel<T, kVec, kU>
+                                                   : hcmix_expand_backward_kernel<T, kVec, kU>,
+                dim3((unsigned)A.M), dim3(threads), 0, stream, A);
 }
 
 inline hcmix_status run_streams(StreamsOp op, const StreamsArgs& A, hcmix_type type,
                                 cudaStream_t stream) {
-  const int n = size_of(type);
-  const bool wide = aligned_rows(A.x, A.x_stride, n) && aligned_rows(A.y, A.y_stride, n) &&
-                    aligned_rows(A.g, A.g_stride, n) && aligned_rows(A.add, A.add_stride, n) &&
-                    aligned_rows(A.out, A.D, n) && aligned_rows(A.dy, A.D, n);
-  return with_type(type, [&](auto t) {
-    using T = decltype(t);
-    return wide ? launch_streams<T, kWide<T>>(op, A, stream) : launch_streams<T, 1>(op, A, stream);
+  // a row's streams start D apart, whatever its stride
+  const int bytes = vector_bytes(size_of(type), {{A.x, A.x_stride}, {A.y, A.y_stride},
+                                                 {A.g, A.g_stride}, {A.add, A.add_stride},
+                                                 {A.out, A.D}, {A.dy, A.D}});
+  return with_vector(type, bytes, [&](auto t, auto vec, auto u) {
+    return launch_streams<decltype(t), decltype(vec)::value, decltype(u)::value>(op, A, stream);
   });
 }
 

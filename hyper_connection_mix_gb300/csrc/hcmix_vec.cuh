@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 
 #include "hcmix_sublayer.h"
 
@@ -227,35 +228,47 @@ struct Acc {
   __device__ __forceinline__ float sum() const { return v[0] + v[1]; }
 };
 
+// ---- rows in global memory, in vectors of 16 bytes where every row of every operand
+// starts on 16 bytes, else of 4 bytes or of one element.
+//
 // Streamed operands are read once and not kept in L1, which is left to what every
 // row uses (weights, coefficients).
 template <typename T, int kVec>
 __device__ __forceinline__ Packed<T, kVec> load_vec(const T* p) {
   Packed<T, kVec> r;
-  if constexpr (sizeof(T) * kVec == 16) {
+  if constexpr (sizeof(r) == 16) {
     uint4 v;
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     *reinterpret_cast<uint4*>(&r) = v;
+  } else if constexpr (sizeof(r) == 4) {
+    uint32_t v;
+    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    *reinterpret_cast<uint32_t*>(&r) = v;
   } else {
     r = *reinterpret_cast<const Packed<T, kVec>*>(p);
   }
   return r;
 }
 
+// The same for what other warps of the block read too: kept in L1.
 template <typename T, int kVec>
-__device__ __forceinline__ void store_vec(T* p, const Packed<T, kVec>& v) {
-  if constexpr (sizeof(T) * kVec == 16) {
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&v);
-  } else {
-    *reinterpret_cast<Packed<T, kVec>*>(p) = v;
-  }
+__device__ __forceinline__ Packed<T, kVec> load_cached_vec(const T* p) {
+  Packed<T, kVec> r;
+  if constexpr (sizeof(r) == 16)
+    *reinterpret_cast<uint4*>(&r) = *reinterpret_cast<const uint4*>(p);
+  else
+    r = *reinterpret_cast<const Packed<T, kVec>*>(p);
+  return r;
 }
 
 template <typename T, int kVec>
-__device__ __forceinline__ void load_f32(const T* p, float (&v)[kVec]) {
-  load_vec<T, kVec>(p).unpack(v);
+__device__ __forceinline__ void store_vec(T* p, const Packed<T, kVec>& v) {
+  if constexpr (sizeof(v) == 16)
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&v);
+  else
+    *reinterpret_cast<Packed<T, kVec>*>(p) = v;
 }
 
 template <typename T, int kVec>
@@ -265,35 +278,114 @@ __device__ __forceinline__ void store_f32(T* p, const float (&v)[kVec]) {
   store_vec<T, kVec>(p, r);
 }
 
-// kVec values of a norm's weight or bias, fp32 (p32) or of type T.
-template <typename T, int kVec>
-__device__ __forceinline__ void load_param(const void* p, bool p32, int64_t at, float (&v)[kVec]) {
-  if (p32) {
-    const float* f = static_cast<const float*>(p) + at;
-    if (kVec % 4 == 0 && reinterpret_cast<uintptr_t>(f) % 16 == 0) {
+// A thread's share of a row: kU vectors of kVec elements, `step` apart, from column
+// c on.  Rows of 16-byte vectors take one each; narrower vectors take several, so
+// that as many bytes are under way.  Past the row's end the first vector is loaded
+// again (column c is in the row) and zeros take its place: no branch parts the loads.
+template <typename T, int kVec, int kU>
+struct Cols {
+  Packed<T, kVec> q[kU];
+  __device__ __forceinline__ void load(const T* row, int64_t c, int step, int64_t width) {
 #pragma unroll
-      for (int i = 0; i < kVec; i += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(f + i);
-        v[i] = q.x;
-        if constexpr (kVec % 4 == 0) {
-          v[i + 1] = q.y;
-          v[i + 2] = q.z;
-          v[i + 3] = q.w;
+    for (int u = 0; u < kU; ++u) q[u] = load_vec<T, kVec>(row + place(c, u, step, width));
+    zero_past(c, step, width);
+  }
+  __device__ __forceinline__ void load_cached(const T* row, int64_t c, int step, int64_t width) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) q[u] = load_cached_vec<T, kVec>(row + place(c, u, step, width));
+    zero_past(c, step, width);
+  }
+  __device__ __forceinline__ void store(T* row, int64_t c, int step, int64_t width) const {
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (u == 0 || c + u * step < width) store_vec<T, kVec>(row + c + u * step, q[u]);
+  }
+  __device__ __forceinline__ void unpack(float (&v)[kU * kVec]) const {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      float t[kVec];
+      q[u].unpack(t);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) v[u * kVec + e] = t[e];
+    }
+  }
+  __device__ __forceinline__ void pack(const float (&v)[kU * kVec]) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      float t[kVec];
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) t[e] = v[u * kVec + e];
+      q[u].pack(t);
+    }
+  }
+
+ private:
+  static __device__ __forceinline__ int64_t place(int64_t c, int u, int step, int64_t width) {
+    return u == 0 || c + u * step >= width ? c : c + u * step;
+  }
+  __device__ __forceinline__ void zero_past(int64_t c, int step, int64_t width) {
+#pragma unroll
+    for (int u = 1; u < kU; ++u) {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e)
+        if (c + u * step >= width) q[u].e[e] = from_f32<T>(0.f);
+    }
+  }
+};
+
+template <typename T, int kVec, int kU>
+__device__ __forceinline__ void load_cols(const T* row, int64_t c, int step, int64_t width,
+                                          float (&v)[kU * kVec]) {
+  Cols<T, kVec, kU> q;
+  q.load(row, c, step, width);
+  q.unpack(v);
+}
+
+template <typename T, int kVec, int kU>
+__device__ __forceinline__ void load_cached_cols(const T* row, int64_t c, int step, int64_t width,
+                                                 float (&v)[kU * kVec]) {
+  Cols<T, kVec, kU> q;
+  q.load_cached(row, c, step, width);
+  q.unpack(v);
+}
+
+template <typename T, int kVec, int kU>
+__device__ __forceinline__ void store_cols(T* row, int64_t c, int step, int64_t width,
+                                           const float (&v)[kU * kVec]) {
+  Cols<T, kVec, kU> q;
+  q.pack(v);
+  q.store(row, c, step, width);
+}
+
+// kVec values from column c on of a norm's weight or bias, fp32 (p32) or of type T;
+// `other` where there is none.
+template <typename T, int kVec>
+__device__ __forceinline__ void load_param(const void* p, bool p32, int64_t c, float other,
+                                           float (&v)[kVec]) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) v[e] = other;
+  } else if (p32) {
+    const float* f = static_cast<const float*>(p) + c;
+    if (kVec % 4 == 0 && reinterpret_cast<uintptr_t>(f) % 16 == 0) {
+      if constexpr (kVec % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < kVec; i += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(f + i);
+          v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
         }
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = f[i];
+      for (int e = 0; e < kVec; ++e) v[e] = f[e];
     }
   } else {
-    const T* t = static_cast<const T*>(p) + at;
-    if (kVec > 1 && reinterpret_cast<uintptr_t>(t) % 16 == 0) {
-      Packed<T, kVec> r;
-      r = *reinterpret_cast<const Packed<T, kVec>*>(t);
-      r.unpack(v);
+    const T* t = static_cast<const T*>(p) + c;
+    if (reinterpret_cast<uintptr_t>(t) % sizeof(Packed<T, kVec>) == 0) {
+      load_cached_vec<T, kVec>(t).unpack(v);
     } else {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = to_f32(t[i]);
+      for (int e = 0; e < kVec; ++e) v[e] = to_f32(t[e]);
     }
   }
 }
@@ -359,17 +451,29 @@ __device__ __forceinline__ float block_sums(const float (&v)[kN], float* part) {
   return t;
 }
 
-// Sums of kN values over the block, in every thread, by warp_sums twice: `part`
-// holds 32 * kN floats and is free again at the next barrier.
+// Barrier of the `warps` warps of one of a block's teams (threads of one
+// threadIdx.y); a block of one team is a team of its own.
+__device__ __forceinline__ void team_sync(int warps) {
+  if (blockDim.y == 1)
+    __syncthreads();
+  else if (warps > 1)
+    asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(warps * 32) : "memory");
+  else
+    __syncwarp();
+}
+
+// Sums of kN values over a team (blockDim.x threads), in every thread, by
+// warp_sums twice: `part`, the team's own, holds 32 * kN floats and is free again at
+// the next barrier.
 template <int kN>
-__device__ __forceinline__ void block_sums_all(float (&v)[kN], float* part) {
+__device__ __forceinline__ void team_sums(float (&v)[kN], float* part) {
   static_assert(kPadded<kN> == kN && kN <= 32, "");
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   constexpr int kEach = 32 / kN;  // lanes that hold the same sum
   float s = warp_sums<kN>(v);
   if (warps > 1) {
     if (lane % kEach == 0) part[warp * kN + lane / kEach] = s;
-    __syncthreads();
+    team_sync(warps);
     // kEach lanes share a value's partials, value i's lanes from i * kEach on
     const int i = lane / kEach;
     s = 0.f;
@@ -382,7 +486,7 @@ __device__ __forceinline__ void block_sums_all(float (&v)[kN], float* part) {
 }
 
 // ---- asynchronous copies into shared memory, completed for the copying thread
-// by async_wait; one vector each
+// by async_wait; 16 or 4 bytes each
 
 template <typename V, typename T>
 __device__ __forceinline__ void async_copy(V* dst, const T* src) {
@@ -390,8 +494,7 @@ __device__ __forceinline__ void async_copy(V* dst, const T* src) {
   if constexpr (sizeof(V) == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(src), "n"(sizeof(V))
-                 : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void async_commit() {
@@ -415,8 +518,21 @@ __device__ __forceinline__ void begin_kernel() {
 
 // ---- host side
 
-inline bool aligned_rows(const void* p, int64_t stride, int size) {
-  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * size % 16 == 0);
+// The widest vector that every row of the operands allows: 16 bytes, 4 or one
+// element of `size` bytes.  A null operand allows all.
+struct Operand {
+  const void* p;
+  int64_t stride;  // elements
+};
+inline int vector_bytes(int size, std::initializer_list<Operand> operands) {
+  for (int to : {16, 4}) {
+    bool all = to >= size;
+    for (const Operand& o : operands)
+      all = all && (o.p == nullptr || (reinterpret_cast<uintptr_t>(o.p) % to == 0 &&
+                                       o.stride * size % to == 0));
+    if (all) return to;
+  }
+  return size;
 }
 
 inline int size_of(hcmix_type t) { return t == HCMIX_F32 ? 4 : 2; }
@@ -432,16 +548,33 @@ inline hcmix_status with_type(hcmix_type t, F&& f) {
   return HCMIX_ERR_INVALID_ARG;
 }
 
+// Calls f(T{}, vec, u) with the type, the elements of a vector and the vectors of a
+// thread's share of a row, as constants.
+template <int kN>
+struct Int {
+  static constexpr int value = kN;
+};
+template <typename F>
+inline hcmix_status with_vector(hcmix_type t, int bytes, F&& f) {
+  return with_type(t, [&](auto z) {
+    using T = decltype(z);
+    if (bytes == 16) return f(z, Int<kWide<T>>{}, Int<1>{});
+    if (bytes == (int)sizeof(T)) return f(z, Int<1>{}, Int<4>{});
+    return f(z, Int<4 / (int)sizeof(T)>{}, Int<4>{});
+  });
+}
+
 // Launches a kernel that starts with begin_kernel(); `cluster` blocks a cluster.
 template <typename Args>
-inline hcmix_status launch(void (*kernel)(const Args), dim3 grid, unsigned threads, size_t smem,
+inline hcmix_status launch(void (*kernel)(const Args), dim3 grid, dim3 threads, size_t smem,
                            cudaStream_t stream, const Args& args, unsigned cluster = 1) {
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  // with its static shared memory a kernel may pass the default 48 KB sooner
+  if (smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem) != cudaSuccess)
     return HCMIX_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
+  cfg.blockDim = threads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
