@@ -63,79 +63,101 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def _stream(stream, device: int):
+# A small call's time is this module's, so the checks read each attribute once and
+# every output is an allocation of its own (views of a shared one cost more).
+
+_empty = torch.empty
+_F32, _I32 = torch.float32, torch.int32
+
+
+def _stream(stream, t: torch.Tensor):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
     return binding._stream(stream)
 
 
-def _matrix(t: torch.Tensor, name: str, like: torch.Tensor | None = None, shape=None):
-    """(pointer, row stride) of a matrix; its type, device and shape checked."""
-    if not (t.is_cuda and t.dim() == 2 and t.dtype in TYPES):
+def _matrix(t: torch.Tensor, name: str):
+    """(pointer, row stride, type code, rows, width, dtype, device) of a call's first matrix."""
+    dtype = t.dtype
+    code = TYPES.get(dtype)
+    shape = t.shape
+    if code is None or len(shape) != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D CUDA tensor of bf16, fp16 or fp32")
-    rows, width = t.shape
+    rows, width = shape
     stride, inner = t.stride()
     if inner != 1 and width > 1:
         raise ValueError(f"{name} must have unit inner stride")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if rows <= 1 and stride < width:
+        stride = width
+    return t.data_ptr(), stride, code, rows, width, dtype, t.device
+
+
+def _like(t: torch.Tensor, name: str, shape, dtype, device):
+    """(pointer, row stride) of a further matrix."""
+    if t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name} must have the type and device of the other matrices")
-    if shape is not None and (rows, width) != shape:
-        raise ValueError(f"{name} must be of shape {shape}, not {(rows, width)}")
-    return t.data_ptr(), stride if rows > 1 else max(stride, width)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be of shape {shape}, not {tuple(t.shape)}")
+    rows, width = shape
+    stride, inner = t.stride()
+    if inner != 1 and width > 1:
+        raise ValueError(f"{name} must have unit inner stride")
+    return t.data_ptr(), width if rows <= 1 and stride < width else stride
 
 
-def _floats(t: torch.Tensor, name: str, like: torch.Tensor, shape) -> int:
-    if not (t.dtype == torch.float32 and t.device == like.device and t.shape == shape
-            and t.is_contiguous()):
-        raise ValueError(f"{name} must be contiguous fp32 of shape {tuple(shape)} on the device "
-                         "of the matrices")
+def _floats(t: torch.Tensor, name: str, shape, device) -> int:
+    if t.dtype is not _F32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous fp32 of shape {shape} on the device of the "
+                         "matrices")
     return t.data_ptr()
 
 
-def _ints(t: torch.Tensor, name: str, like: torch.Tensor, dim: int) -> int:
-    if not (t.dtype == torch.int32 and t.device == like.device and t.dim() == dim
-            and t.is_contiguous()):
+def _ints(t: torch.Tensor, name: str, dim: int, device) -> int:
+    if t.dtype is not _I32 or t.dim() != dim or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 with {dim} dimension(s) on the device "
                          "of the matrices")
     return t.data_ptr()
 
 
-def _params(weight, bias, like: torch.Tensor, width: int):
+def _params(weight, bias, dtype, width: int, device):
     """(weight, bias, type code) of a norm's parameters, either of which may be None."""
-    dtype, at = None, []
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is None:
-            at.append(None)
-            continue
-        if not (t.dtype in (torch.float32, like.dtype) and t.device == like.device
-                and t.shape == (width,) and t.is_contiguous() and dtype in (None, t.dtype)):
-            raise ValueError(f"{name} must be contiguous of shape ({width},), fp32 or of the "
-                             "matrices' type, on their device, weight and bias alike")
-        dtype = t.dtype
-        at.append(t.data_ptr())
-    return at[0], at[1], TYPES[dtype or torch.float32]
+    kind, at = None, [None, None]
+    for i, t in enumerate((weight, bias)):
+        if t is not None:
+            d = t.dtype
+            if ((d is not _F32 and d is not dtype) or (kind is not None and d is not kind)
+                    or t.shape != (width,) or t.device != device or not t.is_contiguous()):
+                raise ValueError(f"{'bias' if i else 'weight'} must be contiguous of shape "
+                                 f"({width},), fp32 or of the matrices' type, on their device, "
+                                 "weight and bias alike")
+            kind = d
+            at[i] = t.data_ptr()
+    return at[0], at[1], TYPES[kind or _F32]
 
 
-def _output(out, like: torch.Tensor, *shape) -> torch.Tensor:
-    """A contiguous matrix of `like`'s type and device: `out`, or a new one."""
+def _output(out, shape, dtype, device) -> torch.Tensor:
+    """A contiguous matrix: `out`, or a new one."""
     if out is None:
-        return like.new_empty(shape)
-    if not (out.shape == shape and out.dtype == like.dtype and out.device == like.device
-            and out.is_contiguous()):
+        return _empty(shape, dtype=dtype, device=device)
+    if out.shape != shape or out.dtype is not dtype or out.device != device or not out.is_contiguous():
         raise ValueError(f"out must be contiguous of shape {shape} and the inputs' type, on their "
                          "device")
     return out
 
 
-def _f32(like: torch.Tensor, *shape) -> torch.Tensor:
-    return torch.empty(shape, dtype=torch.float32, device=like.device)
+def _f32(shape, device) -> torch.Tensor:
+    return _empty(shape, dtype=_F32, device=device)
 
 
-def _width(x: torch.Tensor) -> int:
-    """The width of one stream of x[M, HC * D]."""
-    if x.dim() != 2 or x.shape[1] % HC or x.shape[1] == 0:
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _width(K: int) -> int:
+    """The width of one stream of x[M, K]."""
+    if K % HC or K == 0:
         raise ValueError(f"x must be of shape (M, {HC} * D)")
-    return x.shape[1] // HC
+    return K // HC
 
 
 # ---------------------------------------------------------------- layer norm
@@ -146,17 +168,15 @@ def hc_mix_layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5
     """y[M, N], each row of x normalised, scaled by weight[N] and shifted by
     bias[N] (fp32 or x's type; None: ones, zeros); with want_stats (y, mean[M],
     rstd[M]), which hc_mix_layer_norm_backward takes."""
-    px, sx = _matrix(x, "x")
-    M, N = x.shape
-    pw, pb, ptype = _params(weight, bias, x, N)
-    y = _output(out, x, M, N)
-    stats = _f32(x, 2, M).unbind() if want_stats else None
-    st = lib().hc_mix_layer_norm(px, sx, TYPES[x.dtype], M, N, pw, pb, ptype, eps, y.data_ptr(),
-                                 stats[0].data_ptr() if want_stats else None,
-                                 stats[1].data_ptr() if want_stats else None,
-                                 _stream(stream, x.get_device()))
-    _check(st, "hc_mix_layer_norm")
-    return (y, *stats) if want_stats else y
+    px, sx, code, M, N, dtype, device = _matrix(x, "x")
+    pw, pb, ptype = _params(weight, bias, dtype, N, device)
+    y = _output(out, (M, N), dtype, device)
+    mean, rstd = (_f32((M,), device), _f32((M,), device)) if want_stats else (None, None)
+    st = lib().hc_mix_layer_norm(px, sx, code, M, N, pw, pb, ptype, eps, y.data_ptr(), _ptr(mean),
+                                 _ptr(rstd), _stream(stream, x))
+    if st:
+        _check(st, "hc_mix_layer_norm")
+    return (y, mean, rstd) if want_stats else y
 
 
 def layer_norm_workspace_bytes(M: int, N: int, dtype: torch.dtype) -> int:
@@ -169,25 +189,28 @@ def hc_mix_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Te
     """(dx[M, N], dweight[N], dbias[N]) of hc_mix_layer_norm, the latter two in
     fp32 (with want_params=False only dx).  `workspace`: a uint8 tensor of
     layer_norm_workspace_bytes() bytes, allocated here if not given."""
-    px, sx = _matrix(x, "x")
-    M, N = x.shape
-    pd, sd = _matrix(dy, "dy", x, (M, N))
-    pm, pr = _floats(mean, "mean", x, (M,)), _floats(rstd, "rstd", x, (M,))
-    pw, _, ptype = _params(weight, None, x, N)
-    dx = _output(out, x, M, N)
-    grads, nbytes = (None, None), 0
+    px, sx, code, M, N, dtype, device = _matrix(x, "x")
+    pd, sd = _like(dy, "dy", (M, N), dtype, device)
+    pm, pr = _floats(mean, "mean", (M,), device), _floats(rstd, "rstd", (M,), device)
+    pw, _, ptype = _params(weight, None, dtype, N, device)
+    dx = _output(out, (M, N), dtype, device)
+    L = lib()
+    dweight = dbias = None
+    nbytes = 0
     if want_params:
-        grads = _f32(x, 2, N).unbind()
-        nbytes = layer_norm_workspace_bytes(M, N, x.dtype)
+        dweight, dbias = _f32((N,), device), _f32((N,), device)
         if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-        nbytes = workspace.numel()
-    st = lib().hc_mix_layer_norm_backward(
-        pd, sd, px, sx, TYPES[x.dtype], M, N, pm, pr, pw, ptype, dx.data_ptr(),
-        grads[0].data_ptr() if want_params else None, grads[1].data_ptr() if want_params else None,
-        workspace.data_ptr() if want_params else None, nbytes, _stream(stream, x.get_device()))
-    _check(st, "hc_mix_layer_norm_backward")
-    return (dx, *grads) if want_params else dx
+            nbytes = L.hc_mix_layer_norm_workspace_bytes(code, M, N)
+            workspace = _empty(nbytes, dtype=torch.uint8, device=device)
+        else:
+            nbytes = workspace.numel()
+    st = L.hc_mix_layer_norm_backward(pd, sd, px, sx, code, M, N, pm, pr, pw, ptype, dx.data_ptr(),
+                                      _ptr(dweight), _ptr(dbias),
+                                      _ptr(workspace) if want_params else None, nbytes,
+                                      _stream(stream, x))
+    if st:
+        _check(st, "hc_mix_layer_norm_backward")
+    return (dx, dweight, dbias) if want_params else dx
 
 
 # ---------------------------------------------------------------- streams
@@ -195,13 +218,13 @@ def hc_mix_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Te
 
 def hc_mix_collapse(x: torch.Tensor, pre: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     """h[M, D] = sum_i pre[:, i] x_i of the streams x[M, 4 * D]."""
-    px, sx = _matrix(x, "x")
-    M, D = x.shape[0], _width(x)
-    pp = _floats(pre, "pre", x, (M, HC))
-    h = _output(out, x, M, D)
-    st = lib().hc_mix_collapse(px, sx, TYPES[x.dtype], M, D, HC, pp, h.data_ptr(),
-                               _stream(stream, x.get_device()))
-    _check(st, "hc_mix_collapse")
+    px, sx, code, M, K, dtype, device = _matrix(x, "x")
+    D = _width(K)
+    pp = _floats(pre, "pre", (M, HC), device)
+    h = _output(out, (M, D), dtype, device)
+    st = lib().hc_mix_collapse(px, sx, code, M, D, HC, pp, h.data_ptr(), _stream(stream, x))
+    if st:
+        _check(st, "hc_mix_collapse")
     return h
 
 
@@ -209,34 +232,37 @@ def hc_mix_collapse_norm(x: torch.Tensor, pre: torch.Tensor, weight=None, bias=N
                          eps: float = 1e-5, want_saved: bool = False, out=None, stream=None):
     """y[M, D], the layer norm of hc_mix_collapse's h in one pass over x; with
     want_saved (y, h, mean, rstd), for hc_mix_layer_norm_backward on h."""
-    px, sx = _matrix(x, "x")
-    M, D = x.shape[0], _width(x)
-    pp = _floats(pre, "pre", x, (M, HC))
-    pw, pb, ptype = _params(weight, bias, x, D)
-    y = _output(out, x, M, D)
-    saved = (x.new_empty((M, D)), *_f32(x, 2, M).unbind()) if want_saved else (None,) * 3
-    st = lib().hc_mix_collapse_norm(px, sx, TYPES[x.dtype], M, D, HC, pp, pw, pb, ptype, eps,
-                                    y.data_ptr(), *(s if s is None else s.data_ptr() for s in saved),
-                                    _stream(stream, x.get_device()))
-    _check(st, "hc_mix_collapse_norm")
-    return (y, *saved) if want_saved else y
+    px, sx, code, M, K, dtype, device = _matrix(x, "x")
+    D = _width(K)
+    pp = _floats(pre, "pre", (M, HC), device)
+    pw, pb, ptype = _params(weight, bias, dtype, D, device)
+    y = _output(out, (M, D), dtype, device)
+    h = mean = rstd = None
+    if want_saved:
+        h = _empty((M, D), dtype=dtype, device=device)
+        mean, rstd = _f32((M,), device), _f32((M,), device)
+    st = lib().hc_mix_collapse_norm(px, sx, code, M, D, HC, pp, pw, pb, ptype, eps, y.data_ptr(),
+                                    _ptr(h), _ptr(mean), _ptr(rstd), _stream(stream, x))
+    if st:
+        _check(st, "hc_mix_collapse_norm")
+    return (y, h, mean, rstd) if want_saved else y
 
 
 def hc_mix_collapse_backward(dh: torch.Tensor, x: torch.Tensor, pre: torch.Tensor, dx_add=None,
                              out=None, stream=None):
     """(dx[M, 4 * D], dpre[M, 4]) of hc_mix_collapse, dx with dx_add[M, 4 * D]
     added (the gradient of x through hc_mix_expand); out may be dx_add."""
-    px, sx = _matrix(x, "x")
-    M, D = x.shape[0], _width(x)
-    pd, sd = _matrix(dh, "dh", x, (M, D))
-    pa, sa = (None, 0) if dx_add is None else _matrix(dx_add, "dx_add", x, (M, HC * D))
-    pp = _floats(pre, "pre", x, (M, HC))
-    dx = _output(out, x, M, HC * D)
-    dpre = _f32(x, M, HC)
-    st = lib().hc_mix_collapse_backward(pd, sd, px, sx, pa, sa, TYPES[x.dtype], M, D, HC, pp,
-                                        dx.data_ptr(), dpre.data_ptr(),
-                                        _stream(stream, x.get_device()))
-    _check(st, "hc_mix_collapse_backward")
+    px, sx, code, M, K, dtype, device = _matrix(x, "x")
+    D = _width(K)
+    pd, sd = _like(dh, "dh", (M, D), dtype, device)
+    pa, sa = (None, 0) if dx_add is None else _like(dx_add, "dx_add", (M, K), dtype, device)
+    pp = _floats(pre, "pre", (M, HC), device)
+    dx = _output(out, (M, K), dtype, device)
+    dpre = _f32((M, HC), device)
+    st = lib().hc_mix_collapse_backward(pd, sd, px, sx, pa, sa, code, M, D, HC, pp, dx.data_ptr(),
+                                        dpre.data_ptr(), _stream(stream, x))
+    if st:
+        _check(st, "hc_mix_collapse_backward")
     return dx, dpre
 
 
@@ -244,14 +270,15 @@ def hc_mix_expand(x: torch.Tensor, y: torch.Tensor, post: torch.Tensor, comb: to
                   out=None, stream=None) -> torch.Tensor:
     """The next streams [M, 4 * D]: stream i is post[:, i] y + sum_j
     comb[:, i, j] x_j.  out may be x."""
-    px, sx = _matrix(x, "x")
-    M, D = x.shape[0], _width(x)
-    py, sy = _matrix(y, "y", x, (M, D))
-    pp, pc = _floats(post, "post", x, (M, HC)), _floats(comb, "comb", x, (M, HC, HC))
-    out = _output(out, x, M, HC * D)
-    st = lib().hc_mix_expand(px, sx, py, sy, TYPES[x.dtype], M, D, HC, pp, pc, out.data_ptr(),
-                             _stream(stream, x.get_device()))
-    _check(st, "hc_mix_expand")
+    px, sx, code, M, K, dtype, device = _matrix(x, "x")
+    D = _width(K)
+    py, sy = _like(y, "y", (M, D), dtype, device)
+    pp, pc = _floats(post, "post", (M, HC), device), _floats(comb, "comb", (M, HC, HC), device)
+    out = _output(out, (M, K), dtype, device)
+    st = lib().hc_mix_expand(px, sx, py, sy, code, M, D, HC, pp, pc, out.data_ptr(),
+                             _stream(stream, x))
+    if st:
+        _check(st, "hc_mix_expand")
     return out
 
 
@@ -259,17 +286,19 @@ def hc_mix_expand_backward(dout: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
                            post: torch.Tensor, comb: torch.Tensor, out=None, stream=None):
     """(dx[M, 4 * D], dy[M, D], dpost[M, 4], dcomb[M, 4, 4]) of hc_mix_expand;
     out (for dx) may be dout."""
-    px, sx = _matrix(x, "x")
-    M, D = x.shape[0], _width(x)
-    pd, sd = _matrix(dout, "dout", x, (M, HC * D))
-    py, sy = _matrix(y, "y", x, (M, D))
-    pp, pc = _floats(post, "post", x, (M, HC)), _floats(comb, "comb", x, (M, HC, HC))
-    dx, dy = _output(out, x, M, HC * D), x.new_empty((M, D))
-    dpost, dcomb = _f32(x, M, HC), _f32(x, M, HC, HC)
-    st = lib().hc_mix_expand_backward(pd, sd, px, sx, py, sy, TYPES[x.dtype], M, D, HC, pp, pc,
-                                      dx.data_ptr(), dy.data_ptr(), dpost.data_ptr(),
-                                      dcomb.data_ptr(), _stream(stream, x.get_device()))
-    _check(st, "hc_mix_expand_backward")
+    px, sx, code, M, K, dtype, device = _matrix(x, "x")
+    D = _width(K)
+    pd, sd = _like(dout, "dout", (M, K), dtype, device)
+    py, sy = _like(y, "y", (M, D), dtype, device)
+    pp, pc = _floats(post, "post", (M, HC), device), _floats(comb, "comb", (M, HC, HC), device)
+    dx = _output(out, (M, K), dtype, device)
+    dy = _empty((M, D), dtype=dtype, device=device)
+    dpost, dcomb = _f32((M, HC), device), _f32((M, HC, HC), device)
+    st = lib().hc_mix_expand_backward(pd, sd, px, sx, py, sy, code, M, D, HC, pp, pc, dx.data_ptr(),
+                                      dy.data_ptr(), dpost.data_ptr(), dcomb.data_ptr(),
+                                      _stream(stream, x))
+    if st:
+        _check(st, "hc_mix_expand_backward")
     return dx, dy, dpost, dcomb
 
 
@@ -281,29 +310,33 @@ def hc_mix_expert_sort(ids: torch.Tensor, n_experts: int, stream=None):
     or int64): expert e's rows are offsets[e] .. offsets[e + 1] - 1, slots gives
     each pair's row and source each row's pair, in the order of ids within an
     expert.  An id outside 0 .. E - 1 has slot -1; rows without a pair source -1."""
-    if not (ids.is_cuda and ids.dim() == 2 and ids.dtype in (torch.int32, torch.int64)
-            and ids.is_contiguous()):
+    dtype, shape = ids.dtype, ids.shape
+    wide = dtype is torch.int64
+    if not (wide or dtype is _I32) or len(shape) != 2 or not ids.is_cuda or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous 2-D CUDA tensor of int32 or int64")
-    T, k = ids.shape
-    offsets = torch.empty(max(n_experts, 0) + 1, dtype=torch.int32, device=ids.device)
-    slots = torch.empty((T, k), dtype=torch.int32, device=ids.device)
-    source = torch.empty(T * k, dtype=torch.int32, device=ids.device)
-    st = lib().hc_mix_expert_sort(ids.data_ptr(), ids.element_size(), T, k, n_experts,
+    T, k = shape
+    device = ids.device
+    offsets = _empty(n_experts + 1 if n_experts > 0 else 1, dtype=_I32, device=device)
+    slots = _empty(shape, dtype=_I32, device=device)
+    source = _empty(T * k, dtype=_I32, device=device)
+    st = lib().hc_mix_expert_sort(ids.data_ptr(), 8 if wide else 4, T, k, n_experts,
                                   offsets.data_ptr(), slots.data_ptr(), source.data_ptr(),
-                                  _stream(stream, ids.get_device()))
-    _check(st, "hc_mix_expert_sort")
+                                  _stream(stream, ids))
+    if st:
+        _check(st, "hc_mix_expert_sort")
     return offsets, slots, source
 
 
-def _slots(slots, like, T):
-    p = _ints(slots, "slots", like, 2)
-    if slots.shape[0] != T:
+def _slots(slots, T: int, device):
+    p = _ints(slots, "slots", 2, device)
+    rows, k = slots.shape
+    if rows != T:
         raise ValueError(f"slots must have {T} rows")
-    return p, slots.shape[1]
+    return p, k
 
 
-def _offsets(offsets, like):
-    return (None, 0) if offsets is None else (_ints(offsets, "offsets", like, 1),
+def _offsets(offsets, device):
+    return (None, 0) if offsets is None else (_ints(offsets, "offsets", 1, device),
                                               offsets.shape[0] - 1)
 
 
@@ -311,14 +344,14 @@ def hc_mix_expert_dispatch(x: torch.Tensor, slots: torch.Tensor, offsets=None, o
                            stream=None) -> torch.Tensor:
     """xs[T * k, D] with xs[slots[t, j]] = x[t] and zeros from row offsets[E] on
     (without offsets those rows are left as they are)."""
-    px, sx = _matrix(x, "x")
-    T, D = x.shape
-    ps, k = _slots(slots, x, T)
-    po, E = _offsets(offsets, x)
-    xs = _output(out, x, T * k, D)
-    st = lib().hc_mix_expert_dispatch(px, sx, TYPES[x.dtype], T, k, D, ps, po, E, xs.data_ptr(),
-                                      _stream(stream, x.get_device()))
-    _check(st, "hc_mix_expert_dispatch")
+    px, sx, code, T, D, dtype, device = _matrix(x, "x")
+    ps, k = _slots(slots, T, device)
+    po, E = _offsets(offsets, device)
+    xs = _output(out, (T * k, D), dtype, device)
+    st = lib().hc_mix_expert_dispatch(px, sx, code, T, k, D, ps, po, E, xs.data_ptr(),
+                                      _stream(stream, x))
+    if st:
+        _check(st, "hc_mix_expert_dispatch")
     return xs
 
 
@@ -326,15 +359,15 @@ def hc_mix_expert_combine(ys: torch.Tensor, slots: torch.Tensor, weights=None, o
                           stream=None) -> torch.Tensor:
     """y[T, D] with y[t] = sum_j weights[t, j] ys[slots[t, j]]; without weights,
     of ones: the gradient of hc_mix_expert_dispatch."""
-    py, sy = _matrix(ys, "ys")
-    rows, D = ys.shape
-    ps, k = _slots(slots, ys, slots.shape[0])
+    py, sy, code, rows, D, dtype, device = _matrix(ys, "ys")
     T = slots.shape[0]
-    pw = None if weights is None else _floats(weights, "weights", ys, (T, k))
-    y = _output(out, ys, T, D)
-    st = lib().hc_mix_expert_combine(py, sy, TYPES[ys.dtype], rows, T, k, D, ps, pw, y.data_ptr(),
-                                     _stream(stream, ys.get_device()))
-    _check(st, "hc_mix_expert_combine")
+    ps, k = _slots(slots, T, device)
+    pw = None if weights is None else _floats(weights, "weights", (T, k), device)
+    y = _output(out, (T, D), dtype, device)
+    st = lib().hc_mix_expert_combine(py, sy, code, rows, T, k, D, ps, pw, y.data_ptr(),
+                                     _stream(stream, ys))
+    if st:
+        _check(st, "hc_mix_expert_combine")
     return y
 
 
@@ -343,17 +376,17 @@ def hc_mix_expert_combine_backward(dy: torch.Tensor, ys: torch.Tensor, slots: to
     """(dys, dweights[T, k]) of hc_mix_expert_combine: dys[slots[t, j]] =
     weights[t, j] dy[t], zeros from row offsets[E] on (offsets None: left as
     they are), dweights[t, j] = dy[t] . ys[slots[t, j]]."""
-    py, sy = _matrix(ys, "ys")
-    rows, D = ys.shape
+    py, sy, code, rows, D, dtype, device = _matrix(ys, "ys")
     T = dy.shape[0]
-    pd, sd = _matrix(dy, "dy", ys, (T, D))
-    ps, k = _slots(slots, ys, T)
-    po, E = _offsets(offsets, ys)
-    pw = _floats(weights, "weights", ys, (T, k))
-    dys = _output(out, ys, rows, D)
-    dweights = _f32(ys, T, k)
-    st = lib().hc_mix_expert_combine_backward(pd, sd, py, sy, TYPES[ys.dtype], rows, T, k, D, ps,
-                                              po, E, pw, dys.data_ptr(), dweights.data_ptr(),
-                                              _stream(stream, ys.get_device()))
-    _check(st, "hc_mix_expert_combine_backward")
+    pd, sd = _like(dy, "dy", (T, D), dtype, device)
+    ps, k = _slots(slots, T, device)
+    po, E = _offsets(offsets, device)
+    pw = _floats(weights, "weights", (T, k), device)
+    dys = _output(out, (rows, D), dtype, device)
+    dweights = _f32((T, k), device)
+    st = lib().hc_mix_expert_combine_backward(pd, sd, py, sy, code, rows, T, k, D, ps, po, E, pw,
+                                              dys.data_ptr(), dweights.data_ptr(),
+                                              _stream(stream, ys))
+    if st:
+        _check(st, "hc_mix_expert_combine_backward")
     return dys, dweights
