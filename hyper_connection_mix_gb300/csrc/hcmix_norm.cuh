@@ -116,7 +116,9 @@ __global__ void __launch_bounds__(512) hcmix_norm_wide_kernel(const NormArgs A) 
 // (rows that do not even start on 4 bytes) cannot be: they are loaded into registers
 // when their copy is started and stored to the other of two stages by land(), at the
 // end of the work on the group before.
-template <typename T, int kVec, int kPer, int kRows, int kMostStages>
+//
+// The first kFull vectors of every thread lie within the row.
+template <typename T, int kVec, int kPer, int kRows, int kMostStages, int kFull>
 struct Ring {
   using V = Packed<T, kVec>;
   static constexpr bool kAsync = sizeof(V) >= 4;
@@ -140,7 +142,7 @@ struct Ring {
   }
   __device__ __forceinline__ int group() const { return kRows * kPer * pitch; }
   __device__ __forceinline__ int column(int k) const { return first + k * step; }
-  __device__ __forceinline__ bool has(int k) const { return column(k) < columns; }
+  __device__ __forceinline__ bool has(int k) const { return k < kFull || column(k) < columns; }
   // Starts the copy of source row i, given its first element, into the stage at
   // byte offset `to`.
   __device__ __forceinline__ void copy(int to, int i, const T* row) {
@@ -188,13 +190,20 @@ constexpr int kSms = 152;
 // bytes of each of a group's kRows rows, kBlocks of them a multiprocessor; as many stages as fit
 // 200 KB, up to eight.  Narrow rows take a team of fewer threads each, several teams
 // a block.
-template <int kUnits_, int kThreads_, int kBlocks_>
+//
+// A shape is taken for rows of more than kOver bytes, so its teams have at least
+// kLeast threads.  They have less than 32 threads' worth of vectors to spare: of kPer
+// vectors a thread only the last ceil(32 kPer / kLeast) can lie past the row's end.
+template <int kUnits_, int kThreads_, int kBlocks_, int kOver_>
 struct Shape {
   static constexpr int kUnits = kUnits_, kThreads = kThreads_, kBlocks = kBlocks_;
-  static constexpr int64_t kRowBytes = (int64_t)kUnits * kThreads * 16;
+  static constexpr int kRowBytes = kUnits * kThreads * 16;
+  static constexpr int kLeast = (kOver_ / 16 / kUnits + 1 + 31) / 32 * 32;
+  template <int kPer>
+  static constexpr int kFull = kPer - (32 * kPer + kLeast - 1) / kLeast;
 };
 template <typename S, int kRows>
-constexpr int kFit = 200 * 1024 / (S::kBlocks * kRows * (int)S::kRowBytes);
+constexpr int kFit = 200 * 1024 / (S::kBlocks * kRows * S::kRowBytes);
 template <typename S, int kRows>
 constexpr int kStagesOf = kFit<S, kRows> > 8 ? 8 : kFit<S, kRows> < 2 ? 2 : kFit<S, kRows>;
 
@@ -227,7 +236,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(con
   float(&part)[2][32] = parts[threadIdx.y];
   constexpr int kRows = kCollapse ? kStreams : 1;
   constexpr int kPer = S::kUnits * 16 / (kVec * (int)sizeof(T));
-  using R = Ring<T, kVec, kPer, kRows, kStagesOf<S, kRows>>;
+  using R = Ring<T, kVec, kPer, kRows, kStagesOf<S, kRows>, S::template kFull<kPer>>;
   constexpr bool kKeep = kPer * kVec <= 16 && R::kAsync;
   constexpr int kKept = kKeep ? kPer : 1;
   R ring(smem, A.N);
@@ -327,7 +336,7 @@ hcmix_status launch_norm_ring(const NormArgs& A, cudaStream_t stream) {
   const RingPlan p = ring_plan<S>(A.N * (int64_t)sizeof(T), A.M);
   const size_t smem =
       p.teams * Ring<T, kVec, S::kUnits * 16 / (kVec * (int)sizeof(T)), kRows,
-                     kStagesOf<S, kRows>>::bytes(p.threads);
+                     kStagesOf<S, kRows>, 0>::bytes(p.threads);
   return launch(hcmix_norm_kernel<T, kVec, S, kCollapse>, dim3(p.blocks),
                 dim3(p.threads, p.teams), smem, stream, A);
 }
@@ -338,12 +347,12 @@ hcmix_status launch_norm_ring(const NormArgs& A, cudaStream_t stream) {
 // room for one stage only.
 template <typename T, int kVec, bool kCollapse>
 hcmix_status launch_norm(const NormArgs& A, cudaStream_t stream) {
-  using S1 = Shape<1, 256, 4>;
-  using S2 = Shape<2, 320, 2>;
-  using S3 = Shape<2, 640, 1>;
-  using S4 = Shape<4, 640, 1>;
-  using S5 = Shape<8, 640, 1>;   // of fp32, as many values a thread as S4's of 16 bits
-  using S6 = Shape<1, 1024, 1>;  // of single 16-bit elements, which wait in registers
+  using S1 = Shape<1, 256, 4, 0>;
+  using S2 = Shape<2, 320, 2, S1::kRowBytes>;
+  using S3 = Shape<2, 640, 1, S2::kRowBytes>;
+  using S4 = Shape<4, 640, 1, S3::kRowBytes>;
+  using S5 = Shape<8, 640, 1, S4::kRowBytes>;   // of fp32, as many values a thread as S4's of 16 bits
+  using S6 = Shape<1, 1024, 1, S1::kRowBytes>;  // of single 16-bit elements, which wait in registers
   const int64_t bytes = A.N * (int64_t)sizeof(T);
   if (bytes <= S1::kRowBytes) return launch_norm_ring<T, kVec, S1, kCollapse>(A, stream);
   if constexpr (kVec * sizeof(T) >= 4) {
@@ -466,7 +475,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
   __shared__ float parts[8][2][2 * kGroup * 32];  // of each team
   float(&part)[2][2 * kGroup * 32] = parts[threadIdx.y];
   constexpr int kPer = S::kUnits * 16 / (kVec * (int)sizeof(T));
-  using R = Ring<T, kVec, kPer, 2 * kGroup, kStagesOf<S, 2 * kGroup>>;
+  using R = Ring<T, kVec, kPer, 2 * kGroup, kStagesOf<S, 2 * kGroup>, S::template kFull<kPer>>;
   constexpr bool kKeepRow = S::kUnits == 1 && R::kAsync;
   constexpr bool kKeepWeight = S::kUnits <= (R::kAsync ? 2 : 1);
   constexpr int kRowsKept = kKeepRow ? kGroup : 1, kKept = kKeepRow ? kPer : 1;
@@ -559,16 +568,16 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
     team_sums<2 * kGroup>(sums, part[odd]);
 #pragma unroll
     for (int r = 0; r < kGroup; ++r) {
-      const float c1 = sums[2 * r] * inv, c2 = sums[2 * r + 1] * inv;
+      // dx = rstd t - rstd c1 - rstd c2 xh, c1 and c2 the means of t and t xh
+      const float s1 = -rstd[r] * (sums[2 * r] * inv), s2 = -rstd[r] * (sums[2 * r + 1] * inv);
       T* dx = static_cast<T*>(A.dx) + (int64_t)(row + r) * A.N;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         if (ring.has(k) && row + r < M) {
           if (!kKeepRow) load_row(r, k);
-          float(&d)[kVec] = t[kKeepRow ? r : 0][kKeepRow ? k : 0];
-          vadd(d, -c1, d);
-          vfma(d, -c2, xh[kKeepRow ? r : 0][kKeepRow ? k : 0], d);
-          vmul(d, rstd[r], d);
+          float(&d)[kVec] = xh[kKeepRow ? r : 0][kKeepRow ? k : 0];
+          vfma(d, s2, d, s1);
+          vfma(d, rstd[r], t[kKeepRow ? r : 0][kKeepRow ? k : 0], d);
           store_f32<T, kVec>(dx + ring.column(k), d);
         }
       }
@@ -611,8 +620,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
 }
 
 // The partial rows added up: 32 columns a block, 16 groups of rows, each group's
-// rows and then the groups in order.
-constexpr int kJoinGroups = 16;
+// rows and then the groups in order.  Up to 320 partial rows (two blocks a
+// multiprocessor leave 304) are one round of loads.
+constexpr int kJoinGroups = 16, kJoinRound = 20;
 
 __global__ void __launch_bounds__(32 * kJoinGroups) hcmix_norm_join_kernel(const NormArgs A) {
   begin_kernel();
@@ -621,8 +631,16 @@ __global__ void __launch_bounds__(32 * kJoinGroups) hcmix_norm_join_kernel(const
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < 2 * A.N) {
-#pragma unroll 8
-    for (int b = group; b < A.blocks; b += kJoinGroups) s += A.part[(int64_t)b * 2 * A.N + c];
+    for (int b = group; b < A.blocks; b += kJoinGroups * kJoinRound) {
+      float v[kJoinRound];
+#pragma unroll
+      for (int q = 0; q < kJoinRound; ++q) {
+        const int r = b + q * kJoinGroups;
+        v[q] = r < A.blocks ? A.part[(int64_t)r * 2 * A.N + c] : 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < kJoinRound; ++q) s += v[q];
+    }
   }
   part[group][lane] = s;
   __syncthreads();
@@ -631,10 +649,10 @@ __global__ void __launch_bounds__(32 * kJoinGroups) hcmix_norm_join_kernel(const
   (c < A.N ? A.dweight[c] : A.dbias[c - A.N]) = s;
 }
 
-using Back1 = Shape<1, 256, 3>;
-using Back2 = Shape<1, 640, 1>;
-using Back3 = Shape<2, 640, 1>;
-using Back4 = Shape<4, 640, 1>;
+using Back1 = Shape<1, 256, 3, 0>;
+using Back2 = Shape<2, 320, 2, Back1::kRowBytes>;
+using Back3 = Shape<2, 640, 1, Back2::kRowBytes>;
+using Back4 = Shape<4, 640, 1, Back3::kRowBytes>;
 
 // How a backward call runs: its shape (1 to 4; 0: dx and the column sums by separate
 // kernels) and its blocks, two rows at a time in the first two shapes.
@@ -671,7 +689,7 @@ template <typename T, int kVec, typename S, int kMostGroup>
 hcmix_status launch_norm_backward_ring(const NormArgs& A, const RingPlan& p, cudaStream_t stream) {
   constexpr int kGroup = kVec * sizeof(T) >= 4 ? kMostGroup : 1;
   using R = Ring<T, kVec, S::kUnits * 16 / (kVec * (int)sizeof(T)), 2 * kGroup,
-                 kStagesOf<S, 2 * kGroup>>;
+                 kStagesOf<S, 2 * kGroup>, 0>;
   return launch(hcmix_norm_backward_kernel<T, kVec, S, kGroup>, dim3(p.blocks),
                 dim3(p.threads, p.teams), p.teams * R::bytes(p.threads), stream, A);
 }

@@ -134,6 +134,22 @@ __device__ __forceinline__ void vfma(float (&d)[N], float a, const float (&b)[N]
 }
 
 template <int N>
+__device__ __forceinline__ void vfma(float (&d)[N], float a, const float (&b)[N], float c) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 r =
+          __ffma2_rn(make_float2(a, a), make_float2(b[i], b[i + 1]), make_float2(c, c));
+      d[i] = r.x;
+      d[i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = fmaf(a, b[i], c);
+  }
+}
+
+template <int N>
 __device__ __forceinline__ void vmul(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
   if constexpr (N % 2 == 0) {
 #pragma unroll
