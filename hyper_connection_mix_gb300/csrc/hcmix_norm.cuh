@@ -106,77 +106,105 @@ __global__ void __launch_bounds__(512) hcmix_norm_wide_kernel(const NormArgs A) 
 
 // ---------------------------------------------------------------- the ring
 
+// A matrix in memory, whose rows a ring copies.
+struct Matrix {
+  const unsigned char *begin, *end;
+  uint32_t row_bytes;  // from a row to the next, as far as its low bits go
+  template <typename T>
+  static __device__ __forceinline__ Matrix of(const void* p, int64_t rows, int64_t stride,
+                                              int64_t width) {
+    const unsigned char* b = static_cast<const unsigned char*>(p);
+    return {b, b + ((rows - 1) * stride + width) * (int64_t)sizeof(T),
+            (uint32_t)stride * (uint32_t)sizeof(T)};
+  }
+  // How far past 16 bytes row r starts.
+  __device__ __forceinline__ int misalignment(uint32_t r) const {
+    return ((uint32_t)reinterpret_cast<uintptr_t>(begin) + r * row_bytes) & 15;
+  }
+};
+
 // A ring of kStages groups of rows in shared memory, for one team of blockDim.x
 // threads.  A group is kRows source rows (streams; x and dy of several rows); a thread
-// has kPer vectors of each, its columns the same in every group.  Each thread copies
-// the vectors that it will read itself, so that no barrier stands between the copies
-// and their use.
+// works on kPer vectors of each, its columns the same in every group.  Rows come by
+// asynchronous 16-byte copies.
 //
-// Vectors of 4 bytes and more are copied by cp.async.  Single 16-bit elements
-// (rows that do not even start on 4 bytes) cannot be: they are loaded into registers
-// when their copy is started and stored to the other of two stages by land(), at the
-// end of the work on the group before.
+// Rows of 16-byte vectors (kOwn): each thread copies the vectors that it will read
+// itself, so that no barrier stands between the copies and their use.  Other rows are
+// copied as the aligned 16-byte blocks that hold them, and read by 4-byte vectors or
+// by elements as they lie there, after a barrier.  The bytes of a block beside its row
+// belong to the rows next to it, except at the matrix's two ends, where the elements
+// are copied one by one.
 //
 // The first kFull vectors of every thread lie within the row.
-template <typename T, int kVec, int kPer, int kRows, int kMostStages, int kFull>
+template <typename T, int kVec, int kPer, int kRows, int kStages, int kFull>
 struct Ring {
   using V = Packed<T, kVec>;
-  static constexpr bool kAsync = sizeof(V) >= 4;
-  static constexpr int kStages = kAsync ? kMostStages : 2;
-  unsigned char* mine;
-  int pitch;  // bytes from one of the thread's vectors to its next
-  int at;     // byte offset of the stage that is read
+  static constexpr bool kOwn = sizeof(V) == 16;
+  unsigned char* base;  // of the team
+  int pitch;   // bytes from one of the thread's vectors to its next
+  int at;      // byte offset of the stage that is read
   int columns, first, step;  // the thread's columns: first + k * step, below columns
-  V pending[kAsync ? 1 : kRows * kPer];
   __device__ __forceinline__ Ring(unsigned char* smem, int64_t width)
       : pitch(blockDim.x * sizeof(V)),
         at(0),
         columns((int)width),
         first(threadIdx.x * kVec),
         step(blockDim.x * kVec) {
-    mine = smem + threadIdx.y * (kStages * group()) + threadIdx.x * sizeof(V);
+    base = smem + threadIdx.y * (kStages * group());
   }
   // Bytes of a team's ring.
   static size_t bytes(int threads) {
-    return (size_t)kStages * kRows * kPer * threads * sizeof(V);
+    return (size_t)kStages * kRows * (kPer * threads * sizeof(V) + (kOwn ? 0 : 16));
   }
-  __device__ __forceinline__ int group() const { return kRows * kPer * pitch; }
+  __device__ __forceinline__ int row() const { return kPer * pitch + (kOwn ? 0 : 16); }
+  __device__ __forceinline__ int group() const { return kRows * row(); }
   __device__ __forceinline__ int column(int k) const { return first + k * step; }
   __device__ __forceinline__ bool has(int k) const { return k < kFull || column(k) < columns; }
   // Starts the copy of source row i, given its first element, into the stage at
   // byte offset `to`.
-  __device__ __forceinline__ void copy(int to, int i, const T* row) {
+  __device__ __forceinline__ void copy(int to, int i, const T* from, const Matrix& all) const {
+    unsigned char* dst = base + to + i * row();
+    if constexpr (kOwn) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if constexpr (kAsync) {
-        if (has(k))
-          async_copy(reinterpret_cast<V*>(mine + to + (i * kPer + k) * pitch), row + column(k));
-      } else {
-        // past the end the row's first element again: no branch parts the loads
-        pending[i * kPer + k] = *reinterpret_cast<const V*>(row + (has(k) ? column(k) : 0));
+      for (int k = 0; k < kPer; ++k)
+        if (has(k)) async_copy16(dst + threadIdx.x * 16 + k * pitch, from + column(k));
+    } else {
+      const int m = (int)(reinterpret_cast<uintptr_t>(from) & 15);
+      const int blocks = (m + columns * (int)sizeof(T) + 15) / 16;
+      const unsigned char* src = reinterpret_cast<const unsigned char*>(from) - m;
+      for (int b = threadIdx.x; b < blocks; b += blockDim.x) {
+        const unsigned char* p = src + b * 16;
+        if (p >= all.begin && p + 16 <= all.end) {
+          async_copy16(dst + b * 16, p);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; e += (int)sizeof(T))
+            if (p + e >= all.begin && p + e < all.end)
+              *reinterpret_cast<T*>(dst + b * 16 + e) = *reinterpret_cast<const T*>(p + e);
+        }
       }
     }
-  }
-  __device__ __forceinline__ void land(int to) const {
-    if constexpr (!kAsync) {
-#pragma unroll
-      for (int i = 0; i < kRows * kPer; ++i) *reinterpret_cast<V*>(mine + to + i * pitch) = pending[i];
-    }
-  }
-  // One group of copies ends; an empty one past the last row keeps the count.
-  __device__ __forceinline__ void commit() const {
-    if constexpr (kAsync) async_commit();
-  }
-  __device__ __forceinline__ void wait() const {
-    if constexpr (kAsync) async_wait<kStages - 1>();
   }
   // The stage to refill while this group is worked on: the one read a group ago.
   __device__ __forceinline__ int refill() const {
     return at == 0 ? (kStages - 1) * group() : at - group();
   }
-  // The thread's k-th vector of source row i.
-  __device__ __forceinline__ V read(int i, int k) const {
-    return *reinterpret_cast<const V*>(mine + at + (i * kPer + k) * pitch);
+  // Starts the next group's copies by fetch(stage) and waits for this group's.
+  template <typename Fetch>
+  __device__ __forceinline__ void turn(Fetch&& fetch) const {
+    if constexpr (kOwn) {
+      fetch(refill());
+      async_wait<kStages - 1>();
+    } else {
+      async_wait<kStages - 2>();
+      team_sync(blockDim.x / 32);  // and the stage to refill has been read by all
+      fetch(refill());
+    }
+  }
+  // The thread's k-th vector of source row i, which starts m bytes past 16.
+  __device__ __forceinline__ V read(int i, int k, int m) const {
+    const unsigned char* p = base + at + i * row() + threadIdx.x * (int)sizeof(V) + k * pitch;
+    return *reinterpret_cast<const V*>(kOwn ? p : p + m);
   }
   __device__ __forceinline__ void advance() {
     at += group();
@@ -236,10 +264,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(con
   float(&part)[2][32] = parts[threadIdx.y];
   constexpr int kRows = kCollapse ? kStreams : 1;
   constexpr int kPer = S::kUnits * 16 / (kVec * (int)sizeof(T));
-  using R = Ring<T, kVec, kPer, kRows, kStagesOf<S, kRows>, S::template kFull<kPer>>;
-  constexpr bool kKeep = kPer * kVec <= 16 && R::kAsync;
+  constexpr int kStages = kStagesOf<S, kRows>;
+  using R = Ring<T, kVec, kPer, kRows, kStages, S::template kFull<kPer>>;
+  constexpr bool kKeep = kPer * kVec <= 16;
   constexpr int kKept = kKeep ? kPer : 1;
   R ring(smem, A.N);
+  const Matrix all = Matrix::of<T>(A.x, A.M, A.x_stride, kRows * A.N);
   const uint32_t M = (uint32_t)A.M, jump = gridDim.x * blockDim.y;
   const uint32_t first = blockIdx.x * blockDim.y + threadIdx.y;
   const T* from = static_cast<const T*>(A.x) + first * A.x_stride;
@@ -248,17 +278,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(con
   const auto fetch = [&](int to) {
     if (next < M) {
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) ring.copy(to, i, from + i * A.N);
+      for (int i = 0; i < kRows; ++i) ring.copy(to, i, from + i * A.N, all);
     }
-    ring.commit();
+    async_commit();  // an empty group past the last row keeps the count
     next += jump;
     from += x_jump;
   };
 #pragma unroll
-  for (int s = 0; s < R::kStages - 1; ++s) {
-    fetch(s * ring.group());
-    ring.land(s * ring.group());
-  }
+  for (int s = 0; s < kStages - 1; ++s) fetch(s * ring.group());
   float w[kKept][kVec], b[kKept][kVec];
   const auto load_params = [&](int k) {
     load_param<T, kVec>(A.weight, A.p32, ring.column(k), 1.f, w[kKeep ? k : 0]);
@@ -276,9 +303,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(con
 #pragma unroll
       for (int i = 0; i < kStreams; ++i) pre[i] = A.pre[(int64_t)row * kStreams + i];
     }
-    const int to = ring.refill();
-    fetch(to);
-    ring.wait();
+    ring.turn(fetch);
+    int m[kRows] = {};
+    if constexpr (!R::kOwn) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        m[i] = (all.misalignment(row) + i * (int)A.N * (int)sizeof(T)) & 15;
+    }
     float v[kPer][kVec];
     Acc acc;
 #pragma unroll
@@ -286,8 +317,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(con
       if (ring.has(k)) {
         Packed<T, kVec> s[kRows];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-          s[i] = ring.read(i, k);
+        for (int i = 0; i < kRows; ++i) s[i] = ring.read(i, k, m[i]);
         norm_values<T, kVec, kCollapse>(s, pre, v[k]);
         acc.add(v[k]);
       }
@@ -325,7 +355,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(con
       if (A.mean != nullptr) A.mean[row] = mean;
       if (A.rstd != nullptr) A.rstd[row] = rstd;
     }
-    ring.land(to);
     ring.advance();
   }
 }
@@ -347,24 +376,20 @@ hcmix_status launch_norm_ring(const NormArgs& A, cudaStream_t stream) {
 // room for one stage only.
 template <typename T, int kVec, bool kCollapse>
 hcmix_status launch_norm(const NormArgs& A, cudaStream_t stream) {
-  using S1 = Shape<1, 256, 4, 0>;
-  using S2 = Shape<2, 320, 2, S1::kRowBytes>;
+  constexpr int kNarrow = 4096;  // bytes
+  using S1 = Shape<2, 256, 3, 0>;
+  using S2 = Shape<2, 320, 2, kNarrow>;
   using S3 = Shape<2, 640, 1, S2::kRowBytes>;
   using S4 = Shape<4, 640, 1, S3::kRowBytes>;
-  using S5 = Shape<8, 640, 1, S4::kRowBytes>;   // of fp32, as many values a thread as S4's of 16 bits
-  using S6 = Shape<1, 1024, 1, S1::kRowBytes>;  // of single 16-bit elements, which wait in registers
+  using S5 = Shape<8, 640, 1, S4::kRowBytes>;  // of fp32, as many values a thread as S4's of 16 bits
   const int64_t bytes = A.N * (int64_t)sizeof(T);
-  if (bytes <= S1::kRowBytes) return launch_norm_ring<T, kVec, S1, kCollapse>(A, stream);
-  if constexpr (kVec * sizeof(T) >= 4) {
-    if (bytes <= S2::kRowBytes) return launch_norm_ring<T, kVec, S2, kCollapse>(A, stream);
-    if (bytes <= S3::kRowBytes) return launch_norm_ring<T, kVec, S3, kCollapse>(A, stream);
-    if constexpr (!kCollapse) {
-      if (bytes <= S4::kRowBytes) return launch_norm_ring<T, kVec, S4, false>(A, stream);
-      if constexpr (sizeof(T) == 4)
-        if (bytes <= S5::kRowBytes) return launch_norm_ring<T, kVec, S5, false>(A, stream);
-    }
-  } else {
-    if (bytes <= S6::kRowBytes) return launch_norm_ring<T, kVec, S6, kCollapse>(A, stream);
+  if (bytes <= kNarrow) return launch_norm_ring<T, kVec, S1, kCollapse>(A, stream);
+  if (bytes <= S2::kRowBytes) return launch_norm_ring<T, kVec, S2, kCollapse>(A, stream);
+  if (bytes <= S3::kRowBytes) return launch_norm_ring<T, kVec, S3, kCollapse>(A, stream);
+  if constexpr (!kCollapse) {
+    if (bytes <= S4::kRowBytes) return launch_norm_ring<T, kVec, S4, false>(A, stream);
+    if constexpr (sizeof(T) == 4)
+      if (bytes <= S5::kRowBytes) return launch_norm_ring<T, kVec, S5, false>(A, stream);
   }
   return launch(hcmix_norm_wide_kernel<T, kVec, kCollapse>, dim3((unsigned)A.M), dim3(512), 0,
                 stream, A);
@@ -464,9 +489,9 @@ __global__ void __launch_bounds__(kColumnThreads) hcmix_norm_columns_kernel(cons
 
 // dx and the partial sums of the weight's and bias's gradient in one pass over x
 // and dy, through the ring; a team works on kGroup rows at a time, with one barrier
-// for all their sums.  A thread keeps dweight and dbias of its columns in registers;
-// with one unit a thread (x - mean) rstd and dy weight stay there too, with more
-// they are read and worked out again from the stage, and the weight fits with two.
+// for all their sums.  A thread keeps dweight and dbias of its columns in registers,
+// and the weight where they leave room (two units a thread); after the barrier x and
+// dy are read from the stage again.
 template <typename T, int kVec, typename S, int kGroup>
 __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_kernel(
     const NormArgs A) {
@@ -475,12 +500,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
   __shared__ float parts[8][2][2 * kGroup * 32];  // of each team
   float(&part)[2][2 * kGroup * 32] = parts[threadIdx.y];
   constexpr int kPer = S::kUnits * 16 / (kVec * (int)sizeof(T));
-  using R = Ring<T, kVec, kPer, 2 * kGroup, kStagesOf<S, 2 * kGroup>, S::template kFull<kPer>>;
-  constexpr bool kKeepRow = S::kUnits == 1 && R::kAsync;
-  constexpr bool kKeepWeight = S::kUnits <= (R::kAsync ? 2 : 1);
-  constexpr int kRowsKept = kKeepRow ? kGroup : 1, kKept = kKeepRow ? kPer : 1;
+  constexpr int kStages = kStagesOf<S, 2 * kGroup>;
+  using R = Ring<T, kVec, kPer, 2 * kGroup, kStages, S::template kFull<kPer>>;
+  constexpr bool kKeepWeight = S::kUnits <= 2;
   constexpr int kWeightsKept = kKeepWeight ? kPer : 1;
   R ring(smem, A.N);
+  const Matrix all_x = Matrix::of<T>(A.x, A.M, A.x_stride, A.N);
+  const Matrix all_dy = Matrix::of<T>(A.dy, A.M, A.dy_stride, A.N);
   const uint32_t M = (uint32_t)A.M, jump = gridDim.x * blockDim.y * kGroup;
   const uint32_t first = (blockIdx.x * blockDim.y + threadIdx.y) * kGroup;
   const T* x = static_cast<const T*>(A.x) + first * A.x_stride;
@@ -491,20 +517,17 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
 #pragma unroll
     for (int r = 0; r < kGroup; ++r) {
       if (next + r < M) {
-        ring.copy(to, 2 * r, x + r * A.x_stride);
-        ring.copy(to, 2 * r + 1, dy + r * A.dy_stride);
+        ring.copy(to, 2 * r, x + r * A.x_stride, all_x);
+        ring.copy(to, 2 * r + 1, dy + r * A.dy_stride, all_dy);
       }
     }
-    ring.commit();
+    async_commit();  // an empty group past the last row keeps the count
     next += jump;
     x += x_jump;
     dy += dy_jump;
   };
 #pragma unroll
-  for (int s = 0; s < R::kStages - 1; ++s) {
-    fetch(s * ring.group());
-    ring.land(s * ring.group());
-  }
+  for (int s = 0; s < kStages - 1; ++s) fetch(s * ring.group());
   float dw[kPer][kVec] = {}, db[kPer][kVec] = {}, w[kWeightsKept][kVec];
   const auto load_weight = [&](int k) {
     if (ring.has(k))
@@ -532,18 +555,17 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
 #pragma unroll
     for (int r = 0; r < kGroup; ++r) mean[r] = next_mean[r], rstd[r] = next_rstd[r];
     fetch_stats(row + jump);
-    const int to = ring.refill();
-    fetch(to);
-    ring.wait();
-    float xh[kRowsKept][kKept][kVec], t[kRowsKept][kKept][kVec], g[kVec];
+    ring.turn(fetch);
+    float xh[kVec], t[kVec], g[kVec];
     const auto load_row = [&](int r, int k) {
-      float(&h)[kVec] = xh[kKeepRow ? r : 0][kKeepRow ? k : 0];
-      ring.read(2 * r, k).unpack(h);
-      ring.read(2 * r + 1, k).unpack(g);
+      int mx = 0, my = 0;
+      if constexpr (!R::kOwn) mx = all_x.misalignment(row + r), my = all_dy.misalignment(row + r);
+      ring.read(2 * r, k, mx).unpack(xh);
+      ring.read(2 * r + 1, k, my).unpack(g);
       if (!kKeepWeight) load_weight(k);
-      vadd(h, -mean[r], h);
-      vmul(h, rstd[r], h);
-      vmul(t[kKeepRow ? r : 0][kKeepRow ? k : 0], g, w[kKeepWeight ? k : 0]);
+      vadd(xh, -mean[r], xh);
+      vmul(xh, rstd[r], xh);
+      vmul(t, g, w[kKeepWeight ? k : 0]);
     };
     float sums[2 * kGroup];
 #pragma unroll
@@ -553,12 +575,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
       for (int k = 0; k < kPer; ++k) {
         if (ring.has(k) && row + r < M) {
           load_row(r, k);
-          const float(&h)[kVec] = xh[kKeepRow ? r : 0][kKeepRow ? k : 0];
-          const float(&d)[kVec] = t[kKeepRow ? r : 0][kKeepRow ? k : 0];
-          vfma(dw[k], g, h, dw[k]);
+          vfma(dw[k], g, xh, dw[k]);
           vadd(db[k], g, db[k]);
-          acc[0].add(d);
-          acc[1].add(d, h);
+          acc[0].add(t);
+          acc[1].add(t, xh);
         }
       }
       sums[2 * r] = acc[0].sum();
@@ -574,15 +594,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         if (ring.has(k) && row + r < M) {
-          if (!kKeepRow) load_row(r, k);
-          float(&d)[kVec] = xh[kKeepRow ? r : 0][kKeepRow ? k : 0];
-          vfma(d, s2, d, s1);
-          vfma(d, rstd[r], t[kKeepRow ? r : 0][kKeepRow ? k : 0], d);
-          store_f32<T, kVec>(dx + ring.column(k), d);
+          load_row(r, k);
+          vfma(xh, s2, xh, s1);
+          vfma(xh, rstd[r], t, xh);
+          store_f32<T, kVec>(dx + ring.column(k), xh);
         }
       }
     }
-    ring.land(to);
     ring.advance();
   }
   float* out = A.part + (int64_t)blockIdx.x * 2 * A.N;
@@ -649,8 +667,10 @@ __global__ void __launch_bounds__(32 * kJoinGroups) hcmix_norm_join_kernel(const
   (c < A.N ? A.dweight[c] : A.dbias[c - A.N]) = s;
 }
 
-using Back1 = Shape<1, 256, 3, 0>;
-using Back2 = Shape<2, 320, 2, Back1::kRowBytes>;
+// Rows of up to kBackNarrow bytes, then of what a shape holds.
+constexpr int kBackNarrow = 4096;
+using Back1 = Shape<2, 256, 2, 0>;
+using Back2 = Shape<2, 320, 2, kBackNarrow>;
 using Back3 = Shape<2, 640, 1, Back2::kRowBytes>;
 using Back4 = Shape<4, 640, 1, Back3::kRowBytes>;
 
@@ -661,33 +681,24 @@ struct NormPlan {
   RingPlan ring;
 };
 
-// `bytes`: of a vector.
-inline NormPlan norm_plan(int size, int bytes, int64_t M, int64_t N) {
+inline NormPlan norm_plan(int size, int64_t M, int64_t N) {
   NormPlan p = {};
   const int64_t row = N * size, pairs = (M + 1) / 2;
-  const bool async = bytes >= 4;  // else rows in flight take registers
   if (M == 0) return p;
-  if (row <= Back1::kRowBytes) p.shape = 1, p.ring = ring_plan<Back1>(row, async ? pairs : M);
-  else if (row <= Back2::kRowBytes) p.shape = 2, p.ring = ring_plan<Back2>(row, async ? pairs : M);
+  if (row <= kBackNarrow) p.shape = 1, p.ring = ring_plan<Back1>(row, pairs);
+  else if (row <= Back2::kRowBytes) p.shape = 2, p.ring = ring_plan<Back2>(row, pairs);
   else if (row <= Back3::kRowBytes) p.shape = 3, p.ring = ring_plan<Back3>(row, M);
-  else if (row <= Back4::kRowBytes && async) p.shape = 4, p.ring = ring_plan<Back4>(row, M);
+  else if (row <= Back4::kRowBytes) p.shape = 4, p.ring = ring_plan<Back4>(row, M);
   else p.ring.blocks = (int)(M < 64 ? M : 64);
   return p;
 }
 
-// The workspace is sized before the operands' alignment is known: the largest need.
 inline size_t norm_workspace(int size, int64_t M, int64_t N) {
-  int most = 0;
-  for (int bytes : {16, 4, size}) {
-    const int b = norm_plan(size, bytes, M, N).ring.blocks;
-    most = b > most ? b : most;
-  }
-  return ((size_t)most * 2 * (size_t)N * 4 + 255) / 256 * 256;
+  return ((size_t)norm_plan(size, M, N).ring.blocks * 2 * (size_t)N * 4 + 255) / 256 * 256;
 }
 
-template <typename T, int kVec, typename S, int kMostGroup>
+template <typename T, int kVec, typename S, int kGroup>
 hcmix_status launch_norm_backward_ring(const NormArgs& A, const RingPlan& p, cudaStream_t stream) {
-  constexpr int kGroup = kVec * sizeof(T) >= 4 ? kMostGroup : 1;
   using R = Ring<T, kVec, S::kUnits * 16 / (kVec * (int)sizeof(T)), 2 * kGroup,
                  kStagesOf<S, 2 * kGroup>, 0>;
   return launch(hcmix_norm_backward_kernel<T, kVec, S, kGroup>, dim3(p.blocks),
@@ -696,7 +707,7 @@ hcmix_status launch_norm_backward_ring(const NormArgs& A, const RingPlan& p, cud
 
 template <typename T, int kVec>
 hcmix_status launch_norm_backward(NormArgs A, cudaStream_t stream) {
-  const NormPlan p = norm_plan(sizeof(T), kVec * sizeof(T), A.M, A.N);
+  const NormPlan p = norm_plan(sizeof(T), A.M, A.N);
   A.blocks = p.ring.blocks;
   hcmix_status st = HCMIX_OK;
   if (A.dweight == nullptr || p.shape == 0) {
@@ -715,9 +726,7 @@ hcmix_status launch_norm_backward(NormArgs A, cudaStream_t stream) {
       case 1: st = launch_norm_backward_ring<T, kVec, Back1, 2>(A, p.ring, stream); break;
       case 2: st = launch_norm_backward_ring<T, kVec, Back2, 2>(A, p.ring, stream); break;
       case 3: st = launch_norm_backward_ring<T, kVec, Back3, 1>(A, p.ring, stream); break;
-      default:
-        if constexpr (kVec * sizeof(T) >= 4)
-          st = launch_norm_backward_ring<T, kVec, Back4, 1>(A, p.ring, stream);
+      default: st = launch_norm_backward_ring<T, kVec, Back4, 1>(A, p.ring, stream);
     }
   }
   if (st != HCMIX_OK) return st;

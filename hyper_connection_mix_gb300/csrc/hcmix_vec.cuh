@@ -502,15 +502,11 @@ __device__ __forceinline__ void team_sums(float (&v)[kN], float* part) {
 }
 
 // ---- asynchronous copies into shared memory, completed for the copying thread
-// by async_wait; 16 or 4 bytes each
+// by async_wait; 16 bytes each
 
-template <typename V, typename T>
-__device__ __forceinline__ void async_copy(V* dst, const T* src) {
+__device__ __forceinline__ void async_copy16(void* dst, const void* src) {
   const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  if constexpr (sizeof(V) == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void async_commit() {
