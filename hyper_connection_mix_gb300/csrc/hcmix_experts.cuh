@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(256) hcmix_expert_combine_kernel(const RowsArg
 // A warp takes a pair: its one dot product needs no other warp.  The block's warps
 // take the pairs of neighbouring tokens, so dy[t] comes from L1 for all but the
 // first of a token's pairs.
-constexpr int kPairWarps = 8;
+constexpr int kPairWarps = 4;
 
 template <typename T, int kVec, int kU>
 __global__ void __launch_bounds__(32 * kPairWarps) hcmix_expert_combine_backward_kernel(
@@ -299,12 +299,15 @@ hcmix_status launch_rows(RowsOp op, RowsArgs A, cudaStream_t stream) {
                   dim3(32 * kPairWarps), 0, stream, A);
   }
   const int64_t shares = (A.D + kVec * kU - 1) / (kVec * kU);
-  A.chunks = (int)((shares + 255) / 256);
+  // combine's blocks of 128 threads keep more of them apart: 53.4 us for 54.9 us at 4096
+  // tokens of 8 rows of 5120 bf16; of one row each (13074 of 6976) 94 us, of 256 threads 73 us
+  const int most = op == RowsOp::kCombine && A.k > 1 ? 128 : 256;
+  A.chunks = (int)((shares + most - 1) / most);
   const unsigned threads = (unsigned)((shares + A.chunks - 1) / A.chunks + 31) / 32 * 32;
   const int64_t blocks = A.T * A.chunks;
   if (blocks >= ((int64_t)1 << 31)) return HCMIX_ERR_UNSUPPORTED;
-  // Rows of 16-byte vectors four at a time: 4096 tokens of 8 rows of 5120 bf16 take 55.0 us,
-  // two at a time 59.8 us, eight 56.3 us; of one row each a batch of four takes 115 us for
+  // Rows of 16-byte vectors four at a time: 4096 tokens of 8 rows of 5120 bf16 took 55.0 us
+  // (in blocks of 256 threads), two at a time 59.8 us, eight 56.3 us; of one row each a batch of four takes 115 us for
   // 13074 tokens of 6976 bf16, its own kernel 72 us.  Narrow vectors have four loads a row
   // already: 3000 tokens of 7 rows of 3001 bf16 take 59 us two at a time, 68 us four.
   constexpr int kBatch = kU > 1 ? 2 : 4;

@@ -378,7 +378,9 @@ template <typename T, int kVec, bool kCollapse>
 hcmix_status launch_norm(const NormArgs& A, cudaStream_t stream) {
   constexpr int kNarrow = 4096;  // bytes
   using S1 = Shape<2, 256, 3, 0>;
-  using S2 = Shape<2, 320, 2, kNarrow>;
+  // 16384 rows of 5120 bf16: two blocks 64.5 us, three 80 us (too few registers); 3001 of
+  // 2051 fp32: 15.3 us and 14.2 us
+  using S2 = Shape<2, 320, sizeof(T) == 4 && !kCollapse ? 3 : 2, kNarrow>;
   using S3 = Shape<2, 640, 1, S2::kRowBytes>;
   using S4 = Shape<4, 640, 1, S3::kRowBytes>;
   using S5 = Shape<8, 640, 1, S4::kRowBytes>;  // of fp32, as many values a thread as S4's of 16 bits
