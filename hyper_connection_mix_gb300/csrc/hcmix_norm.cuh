@@ -253,15 +253,18 @@ inline RingPlan ring_plan(int64_t row_bytes, int64_t groups) {
   return p;
 }
 
-// The norm, one row at a time.  The mean is taken first and the variance from the
-// differences, so that a large mean costs no digits.  Weight and bias are kept in
-// registers where they fit beside the row (16 values a thread or fewer).
+// The norm, one row at a time.  A warp takes the mean of its columns and the squared
+// differences from that, and one barrier later the warps' are joined:
+//   mean = sum_w s_w / N,  N var = sum_w (q_w + n_w (s_w / n_w - mean)^2),
+// so that a large mean costs no digits.  Weight and bias are kept in registers where they
+// fit beside the row (16 values a thread or fewer).
 template <typename T, int kVec, typename S, bool kCollapse>
 __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(const NormArgs A) {
   begin_kernel();
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float parts[8][2][32];  // of each team
-  float(&part)[2][32] = parts[threadIdx.y];
+  __shared__ float2 parts[8][2][32];  // of each team: s_w and q_w
+  __shared__ float counts[8][32];     // n_w
+  float2(&part)[2][32] = parts[threadIdx.y];
   constexpr int kRows = kCollapse ? kStreams : 1;
   constexpr int kPer = S::kUnits * 16 / (kVec * (int)sizeof(T));
   constexpr int kStages = kStagesOf<S, kRows>;
@@ -296,8 +299,15 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(con
     for (int k = 0; k < kPer; ++k)
       if (ring.has(k)) load_params(k);
   }
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int count = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) count += ring.has(k) ? kVec : 0;
+  const float n = (float)__reduce_add_sync(0xffffffffu, count), inv_n = n > 0.f ? 1.f / n : 0.f;
+  if (lane == 0) counts[threadIdx.y][warp] = n;
+  int odd = 0;
   const float inv = 1.f / (float)A.N;
-  for (uint32_t row = first; row < M; row += jump) {
+  for (uint32_t row = first; row < M; row += jump, odd ^= 1) {
     float pre[kStreams] = {};
     if constexpr (kCollapse) {
 #pragma unroll
@@ -322,30 +332,36 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(con
         acc.add(v[k]);
       }
     }
-    float sum[1] = {acc.sum()};
-    team_sums<1>(sum, part[0]);
-    const float mean = sum[0] * inv;
-    if (kCollapse && A.h != nullptr) {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        if (ring.has(k))
-          store_f32<T, kVec>(static_cast<T*>(A.h) + row * A.N + ring.column(k), v[k]);
-    }
+    const float sum = warp_sum(acc.sum()), own_mean = sum * inv_n;
     Acc square;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       if (ring.has(k)) {
-        vadd(v[k], -mean, v[k]);
-        square.add(v[k], v[k]);
+        float d[kVec];
+        vadd(d, -own_mean, v[k]);
+        square.add(d, d);
       }
     }
-    float sq[1] = {square.sum()};
-    team_sums<1>(sq, part[1]);
-    const float rstd = 1.f / sqrtf(sq[0] * inv + A.eps);
+    const float own_square = warp_sum(square.sum());
+    float mean = own_mean, all_square = own_square;
+    if (warps > 1) {
+      // two rows apart, a barrier lies between the uses of `part`
+      if (lane == 0) part[odd][warp] = make_float2(sum, own_square);
+      team_sync(warps);
+      const float2 p = lane < warps ? part[odd][lane] : make_float2(0.f, 0.f);
+      const float c = lane < warps ? counts[threadIdx.y][lane] : 0.f;
+      mean = warp_sum(p.x) * inv;
+      const float d = c > 0.f ? p.x / c - mean : 0.f;
+      all_square = warp_sum(fmaf(c * d, d, p.y));
+    }
+    const float rstd = 1.f / sqrtf(all_square * inv + A.eps);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       if (ring.has(k)) {
+        if (kCollapse && A.h != nullptr)
+          store_f32<T, kVec>(static_cast<T*>(A.h) + row * A.N + ring.column(k), v[k]);
         if (!kKeep) load_params(k);
+        vadd(v[k], -mean, v[k]);
         vmul(v[k], rstd, v[k]);
         vfma(v[k], v[k], w[kKeep ? k : 0], b[kKeep ? k : 0]);
         store_f32<T, kVec>(static_cast<T*>(A.y) + row * A.N + ring.column(k), v[k]);
