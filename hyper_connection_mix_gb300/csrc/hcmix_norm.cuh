@@ -4,6 +4,10 @@
 // ahead of their use; what belongs to a thread's columns (weight, bias, sums over
 // rows) stays in its registers.  Rows too wide for that are passed over several
 // times.
+//
+// Bound by HBM (copy rate 6787 GB/s) less what a row's reduction stalls: measured, collapse
+// + norm of 16384 x 4 x 5120 bf16 137 us (839 MB, 6.1 TB/s), norm of 16384 x 5120 bf16 64 us
+// (5.2 TB/s), backward of 4096 x 5120 bf16 29.5 us (126 MB, 4.3 TB/s; 4 us of it the join).
 #pragma once
 
 #include "hcmix_vec.cuh"

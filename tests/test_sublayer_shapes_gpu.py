@@ -184,3 +184,33 @@ def test_sort_is_the_same_every_time():
     for _ in range(50):
         for a, b in zip(first, sub.hc_mix_expert_sort(ids, 128)):
             assert torch.equal(a, b)
+
+
+def test_norm_and_experts_past_32_bits():
+    """Matrices of more than 2^31 elements: the last rows are right."""
+    M, D = 430000, 5120
+    x = torch.zeros(M, D, dtype=torch.bfloat16, device="cuda")
+    x[-33:] = randn(33, D, dtype=torch.bfloat16)
+    tail = slice(M - 33, M)
+    y, mean, rstd = sub.hc_mix_layer_norm(x, want_stats=True)
+    few = x[tail].clone()  # x is written over below
+    y1, mean1, rstd1 = sub.hc_mix_layer_norm(few, want_stats=True)
+    assert torch.equal(y[tail], y1) and torch.equal(mean[tail], mean1)
+    dx, _, db = sub.hc_mix_layer_norm_backward(y, x, mean, rstd, out=y)
+    dx1, _, _ = sub.hc_mix_layer_norm_backward(y1, few, mean1, rstd1)
+    assert torch.equal(dx[tail], dx1)
+    del y, dx
+    # the last rows of the experts' matrix belong to the last tokens, twice in a row
+    T = M // 2
+    ids = torch.arange(M, device="cuda").view(2, T).t().contiguous() // T  # both experts of each token
+    offsets, slots, _ = sub.hc_mix_expert_sort(ids, 2)
+    assert offsets.tolist() == [0, T, M] and int(slots[-1, 1]) == M - 1
+    xs = sub.hc_mix_expert_dispatch(x[-T:], slots, offsets)
+    assert torch.equal(xs[tail], x[tail]) and torch.equal(xs[T - 33:T], x[tail])
+    weights = torch.full((T, 2), 0.5, device="cuda")
+    back = sub.hc_mix_expert_combine(xs, slots, weights)
+    assert torch.equal(back[-33:], x[tail])
+    dys, dw = sub.hc_mix_expert_combine_backward(back, xs, slots, offsets, weights, out=x)
+    assert torch.equal(dys[tail], back[-33:] * 0.5)
+    dots = (few.double() * few.double()).sum(1)
+    assert ((dw[-33:, 1].double() - dots).abs() <= chain(D) * U32 * dots).all()
