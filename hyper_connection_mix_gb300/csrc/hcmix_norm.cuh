@@ -697,26 +697,31 @@ using Back3 = Shape<2, 640, 1, Back2::kRowBytes>;
 using Back4 = Shape<4, 640, 1, Back3::kRowBytes>;
 
 // How a backward call runs: its shape (1 to 4; 0: dx and the column sums by separate
-// kernels) and its blocks, two rows at a time in the first two shapes.
+// kernels) and its blocks.  Rows of 16-byte vectors (`own`) go two at a time in the first two
+// shapes; narrower vectors have no registers for that (4096 x 5119 bf16: two at a time 99 us,
+// one 56 us).
 struct NormPlan {
   int shape;
   RingPlan ring;
 };
 
-inline NormPlan norm_plan(int size, int64_t M, int64_t N) {
+inline NormPlan norm_plan(int size, bool own, int64_t M, int64_t N) {
   NormPlan p = {};
-  const int64_t row = N * size, pairs = (M + 1) / 2;
+  const int64_t row = N * size, groups = own ? (M + 1) / 2 : M;
   if (M == 0) return p;
-  if (row <= kBackNarrow) p.shape = 1, p.ring = ring_plan<Back1>(row, pairs);
-  else if (row <= Back2::kRowBytes) p.shape = 2, p.ring = ring_plan<Back2>(row, pairs);
+  if (row <= kBackNarrow) p.shape = 1, p.ring = ring_plan<Back1>(row, groups);
+  else if (row <= Back2::kRowBytes) p.shape = 2, p.ring = ring_plan<Back2>(row, groups);
   else if (row <= Back3::kRowBytes) p.shape = 3, p.ring = ring_plan<Back3>(row, M);
   else if (row <= Back4::kRowBytes) p.shape = 4, p.ring = ring_plan<Back4>(row, M);
   else p.ring.blocks = (int)(M < 64 ? M : 64);
   return p;
 }
 
+// The workspace is sized before the operands' alignment is known: the larger need.
 inline size_t norm_workspace(int size, int64_t M, int64_t N) {
-  return ((size_t)norm_plan(size, M, N).ring.blocks * 2 * (size_t)N * 4 + 255) / 256 * 256;
+  const int a = norm_plan(size, true, M, N).ring.blocks;
+  const int b = norm_plan(size, false, M, N).ring.blocks;
+  return ((size_t)(a > b ? a : b) * 2 * (size_t)N * 4 + 255) / 256 * 256;
 }
 
 template <typename T, int kVec, typename S, int kGroup>
@@ -729,7 +734,9 @@ hcmix_status launch_norm_backward_ring(const NormArgs& A, const RingPlan& p, cud
 
 template <typename T, int kVec>
 hcmix_status launch_norm_backward(NormArgs A, cudaStream_t stream) {
-  const NormPlan p = norm_plan(sizeof(T), A.M, A.N);
+  constexpr bool kOwn = kVec * sizeof(T) == 16;
+  constexpr int kGroup = kOwn ? 2 : 1;
+  const NormPlan p = norm_plan(sizeof(T), kOwn, A.M, A.N);
   A.blocks = p.ring.blocks;
   hcmix_status st = HCMIX_OK;
   if (A.dweight == nullptr || p.shape == 0) {
@@ -745,8 +752,8 @@ hcmix_status launch_norm_backward(NormArgs A, cudaStream_t stream) {
                   stream, A);
   } else {
     switch (p.shape) {
-      case 1: st = launch_norm_backward_ring<T, kVec, Back1, 2>(A, p.ring, stream); break;
-      case 2: st = launch_norm_backward_ring<T, kVec, Back2, 2>(A, p.ring, stream); break;
+      case 1: st = launch_norm_backward_ring<T, kVec, Back1, kGroup>(A, p.ring, stream); break;
+      case 2: st = launch_norm_backward_ring<T, kVec, Back2, kGroup>(A, p.ring, stream); break;
       case 3: st = launch_norm_backward_ring<T, kVec, Back3, 1>(A, p.ring, stream); break;
       default: st = launch_norm_backward_ring<T, kVec, Back4, 1>(A, p.ring, stream);
     }
