@@ -1,9 +1,9 @@
 // Loads, stores, conversions and reductions shared by the sublayer kernels.
 //
-// A kernel handles a row in vectors of kVec consecutive elements per thread:
-// 16 bytes where every row of every operand starts on 16 bytes, else one
-// element.  Values are unpacked to fp32, and a result is rounded once, here,
-// when it is packed for its store.
+// A kernel handles a row in vectors of kVec consecutive elements per thread: 16
+// bytes where every row of every operand starts on 16 bytes, else 4 bytes where all
+// start on 4, else one element.  Values are unpacked to fp32, and a result is rounded
+// once, here, when it is packed for its store.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -348,22 +348,6 @@ struct Cols {
     }
   }
 };
-
-template <typename T, int kVec, int kU>
-__device__ __forceinline__ void load_cols(const T* row, int64_t c, int step, int64_t width,
-                                          float (&v)[kU * kVec]) {
-  Cols<T, kVec, kU> q;
-  q.load(row, c, step, width);
-  q.unpack(v);
-}
-
-template <typename T, int kVec, int kU>
-__device__ __forceinline__ void load_cached_cols(const T* row, int64_t c, int step, int64_t width,
-                                                 float (&v)[kU * kVec]) {
-  Cols<T, kVec, kU> q;
-  q.load_cached(row, c, step, width);
-  q.unpack(v);
-}
 
 template <typename T, int kVec, int kU>
 __device__ __forceinline__ void store_cols(T* row, int64_t c, int step, int64_t width,

@@ -26,7 +26,9 @@
  *     start on 16 bytes are read and written in 16-byte pieces and run fastest.
  *   - Zero rows are a valid call.  Outputs that sum over rows are then zero.
  *   - Results do not depend on the order in which thread blocks run: there
- *     are no atomics on values.  One GPU model gives the same bits every time.
+ *     are no atomics on values, and the same call gives the same bits every
+ *     time.  What belongs to one row is the same bits whatever other rows its
+ *     call has; dweight and dbias, sums over rows, are formed by their number.
  *   - Outputs may not overlap inputs, except where said.
  */
 #ifndef HCMIX_SUBLAYER_H
