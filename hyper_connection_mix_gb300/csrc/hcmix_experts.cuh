@@ -319,22 +319,23 @@ hcmix_status launch_rows(RowsOp op, RowsArgs A, cudaStream_t stream) {
     return launch(hcmix_expert_combine_backward_kernel<T, kVec, kU>, dim3((unsigned)blocks),
                   dim3(32 * kPairWarps), 0, stream, A);
   }
-  const int64_t shares = (A.D + kVec * kU - 1) / (kVec * kU);
-  // combine's blocks of 128 threads keep more of them apart: 53.4 us for 54.9 us at 4096
-  // tokens of 8 rows of 5120 bf16; of one row each (13074 of 6976) 94 us, of 256 threads 73 us
-  const int most = op == RowsOp::kCombine && A.k > 1 ? 128 : 256;
+  // Combine has four of a token's rows under way, in blocks of 128 threads: 4096 tokens of 8
+  // rows of 5120 bf16 take 53.4 us, in blocks of 256 threads 54.9 us, two rows at a time 59.8 us,
+  // eight 56.3 us.  Narrow vectors have four loads a row already: 3000 tokens of 7 rows of
+  // 3001 bf16 take 59 us two at a time, 68 us four.  One row a token is a kernel of its own
+  // with more of the row a thread: 13074 tokens of 6976 bf16 take 65 us, one vector a thread
+  // 73 us, a batch of four 115 us.
+  constexpr int kBatch = kU > 1 ? 2 : 4, kOneU = kU > 1 ? kU : 2;
+  const bool combine = op == RowsOp::kCombine, one = combine && A.k == 1;
+  const int64_t share = kVec * (one ? kOneU : kU), shares = (A.D + share - 1) / share;
+  const int most = combine && !one ? 128 : 256;
   A.chunks = (int)((shares + most - 1) / most);
   const unsigned threads = (unsigned)((shares + A.chunks - 1) / A.chunks + 31) / 32 * 32;
   const int64_t blocks = A.T * A.chunks;
   if (blocks >= ((int64_t)1 << 31)) return HCMIX_ERR_UNSUPPORTED;
-  // Rows of 16-byte vectors four at a time: 4096 tokens of 8 rows of 5120 bf16 took 55.0 us
-  // (in blocks of 256 threads), two at a time 59.8 us, eight 56.3 us; of one row each a batch of four takes 115 us for
-  // 13074 tokens of 6976 bf16, its own kernel 72 us.  Narrow vectors have four loads a row
-  // already: 3000 tokens of 7 rows of 3001 bf16 take 59 us two at a time, 68 us four.
-  constexpr int kBatch = kU > 1 ? 2 : 4;
-  const auto kernel = op == RowsOp::kDispatch ? hcmix_expert_dispatch_kernel<T, kVec, kU>
-                      : A.k == 1              ? hcmix_expert_combine_kernel<T, kVec, kU, 1>
-                                              : hcmix_expert_combine_kernel<T, kVec, kU, kBatch>;
+  const auto kernel = one       ? hcmix_expert_combine_kernel<T, kVec, kOneU, 1>
+                      : combine ? hcmix_expert_combine_kernel<T, kVec, kU, kBatch>
+                                : hcmix_expert_dispatch_kernel<T, kVec, kU>;
   return launch(kernel, dim3((unsigned)blocks), dim3(threads), 0, stream, A);
 }
 
