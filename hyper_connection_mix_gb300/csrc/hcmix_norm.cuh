@@ -261,7 +261,9 @@ inline RingPlan ring_plan(int64_t row_bytes, int64_t groups) {
 // differences from that, and one barrier later the warps' are joined:
 //   mean = sum_w s_w / N,  N var = sum_w (q_w + n_w (s_w / n_w - mean)^2),
 // so that a large mean costs no digits.  Weight and bias are kept in registers where they
-// fit beside the row (16 values a thread or fewer).
+// fit beside the row (16 values a thread or fewer); else they come for every row, 16
+// values of each a thread at a time so that their loads overlap (3588 x 12562 fp32: 137 us,
+// a vector at a time 222 us).
 template <typename T, int kVec, typename S, bool kCollapse>
 __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(const NormArgs A) {
   begin_kernel();
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(con
   constexpr int kStages = kStagesOf<S, kRows>;
   using R = Ring<T, kVec, kPer, kRows, kStages, S::template kFull<kPer>>;
   constexpr bool kKeep = kPer * kVec <= 16;
-  constexpr int kKept = kKeep ? kPer : 1;
+  constexpr int kKept = kKeep ? kPer : 16 / kVec;  // else as many at a time
   R ring(smem, A.N);
   const Matrix all = Matrix::of<T>(A.x, A.M, A.x_stride, kRows * A.N);
   const uint32_t M = (uint32_t)A.M, jump = gridDim.x * blockDim.y;
@@ -294,15 +296,16 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(con
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) fetch(s * ring.group());
   float w[kKept][kVec], b[kKept][kVec];
-  const auto load_params = [&](int k) {
-    load_param<T, kVec>(A.weight, A.p32, ring.column(k), 1.f, w[kKeep ? k : 0]);
-    load_param<T, kVec>(A.bias, A.p32, ring.column(k), 0.f, b[kKeep ? k : 0]);
-  };
-  if constexpr (kKeep) {
+  const auto load_params = [&](int from) {  // of vectors from .. from + kKept - 1
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (ring.has(k)) load_params(k);
-  }
+    for (int i = 0; i < kKept; ++i) {
+      if (ring.has(from + i)) {
+        load_param<T, kVec>(A.weight, A.p32, ring.column(from + i), 1.f, w[i]);
+        load_param<T, kVec>(A.bias, A.p32, ring.column(from + i), 0.f, b[i]);
+      }
+    }
+  };
+  if constexpr (kKeep) load_params(0);
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   int count = 0;
 #pragma unroll
@@ -361,13 +364,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_kernel(con
     const float rstd = 1.f / sqrtf(all_square * inv + A.eps);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
+      if (!kKeep && k % kKept == 0) load_params(k);
       if (ring.has(k)) {
         if (kCollapse && A.h != nullptr)
           store_f32<T, kVec>(static_cast<T*>(A.h) + row * A.N + ring.column(k), v[k]);
-        if (!kKeep) load_params(k);
         vadd(v[k], -mean, v[k]);
         vmul(v[k], rstd, v[k]);
-        vfma(v[k], v[k], w[kKeep ? k : 0], b[kKeep ? k : 0]);
+        vfma(v[k], v[k], w[k % kKept], b[k % kKept]);
         store_f32<T, kVec>(static_cast<T*>(A.y) + row * A.N + ring.column(k), v[k]);
       }
     }
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
   constexpr int kStages = kStagesOf<S, 2 * kGroup>;
   using R = Ring<T, kVec, kPer, 2 * kGroup, kStages, S::template kFull<kPer>>;
   constexpr bool kKeepWeight = S::kUnits <= 2;
-  constexpr int kWeightsKept = kKeepWeight ? kPer : 1;
+  constexpr int kKept = kKeepWeight ? kPer : 16 / kVec < kPer ? 16 / kVec : kPer;  // or at a time
   R ring(smem, A.N);
   const Matrix all_x = Matrix::of<T>(A.x, A.M, A.x_stride, A.N);
   const Matrix all_dy = Matrix::of<T>(A.dy, A.M, A.dy_stride, A.N);
@@ -550,15 +553,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
   };
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) fetch(s * ring.group());
-  float dw[kPer][kVec] = {}, db[kPer][kVec] = {}, w[kWeightsKept][kVec];
-  const auto load_weight = [&](int k) {
-    if (ring.has(k))
-      load_param<T, kVec>(A.weight, A.p32, ring.column(k), 1.f, w[kKeepWeight ? k : 0]);
-  };
-  if constexpr (kKeepWeight) {
+  float dw[kPer][kVec] = {}, db[kPer][kVec] = {}, w[kKept][kVec];
+  const auto load_weights = [&](int from) {  // of vectors from .. from + kKept - 1
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) load_weight(k);
-  }
+    for (int i = 0; i < kKept; ++i)
+      if (ring.has(from + i))
+        load_param<T, kVec>(A.weight, A.p32, ring.column(from + i), 1.f, w[i]);
+  };
+  if constexpr (kKeepWeight) load_weights(0);
   const float inv = 1.f / (float)A.N;
   int odd = 0;
   float next_mean[kGroup], next_rstd[kGroup];
@@ -584,10 +586,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
       if constexpr (!R::kOwn) mx = all_x.misalignment(row + r), my = all_dy.misalignment(row + r);
       ring.read(2 * r, k, mx).unpack(xh);
       ring.read(2 * r + 1, k, my).unpack(g);
-      if (!kKeepWeight) load_weight(k);
       vadd(xh, -mean[r], xh);
       vmul(xh, rstd[r], xh);
-      vmul(t, g, w[kKeepWeight ? k : 0]);
+      vmul(t, g, w[k % kKept]);
     };
     float sums[2 * kGroup];
 #pragma unroll
@@ -595,6 +596,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
       Acc acc[2];
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
+        if (!kKeepWeight && k % kKept == 0) load_weights(k);
         if (ring.has(k) && row + r < M) {
           load_row(r, k);
           vfma(dw[k], g, xh, dw[k]);
@@ -615,6 +617,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) hcmix_norm_backward_k
       T* dx = static_cast<T*>(A.dx) + (int64_t)(row + r) * A.N;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
+        if (!kKeepWeight && k % kKept == 0) load_weights(k);
         if (ring.has(k) && row + r < M) {
           load_row(r, k);
           vfma(xh, s2, xh, s1);
