@@ -3,7 +3,7 @@
 // again, with the gradients.  No atomics: every row has one writer.
 //
 // The rows' copies are bound by HBM (copy rate 6787 GB/s).  Measured for 4096 tokens of 5120
-// bf16 to 8 of 128 experts: sort 7.7 us, dispatch 56 us (378 MB, 6.7 TB/s), combine 53.5 us
+// bf16 to 8 of 128 experts: sort 8.0 us, dispatch 56 us (378 MB, 6.7 TB/s), combine 53.5 us
 // (378 MB, 7.1 TB/s), combine backward 107 us (713 MB, 6.7 TB/s).
 #pragma once
 
@@ -23,10 +23,10 @@ struct SortArgs {
 
 constexpr int kMostExperts = 4096;
 constexpr int kSortCounters = 32 * 1024;  // warps * experts, 128 KB
-// Pairs that one block sorts: 512 take it 3.3 us and 1024 4.7 us, a cluster 3.9 us.
+// Pairs that one block sorts: 512 take it 3.3 us and 1024 4.7 us, a cluster 4.0 us.
 constexpr int64_t kSortAlone = 512;
 // Blocks of the cluster that sorts more.  The scattered stores of source, one sector
-// a pair, are shared out over them: 32768 pairs of 128 experts take 16 blocks 7.7 us
+// a pair, are shared out over them: 32768 pairs of 128 experts take 16 blocks 8.0 us
 // (8 blocks, before the loops were rolled, 10.3 us).  Each holds a row of totals for
 // every block, 64 KB in all.
 inline int sort_blocks(int64_t n, int64_t E) { return n <= kSortAlone ? 1 : E <= 1024 ? 16 : 4; }
@@ -50,6 +50,14 @@ __device__ __forceinline__ unsigned same_key(int key, int bits) {
   return same;
 }
 
+// A barrier of the cluster's threads in two halves: arrive, and wait for all others'.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // One cluster sorts all pairs.  Each of its warps takes a contiguous range of
 // them and walks it in batches of 32, counting its experts in shared memory: a
 // pair's rank in its warp is the count so far and the lower lanes with its expert.
@@ -65,6 +73,7 @@ __global__ void __launch_bounds__(1024) hcmix_expert_sort_kernel(const SortArgs 
   extern __shared__ int sort_shared[];
   const cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), cta = cluster.block_rank();
+  if (ctas > 1) cluster_arrive();
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int E = A.E, bits = 32 - __clz(E);  // of the keys 0 .. E
   int* count = sort_shared;         // [warps][E], then the counts of the warps before
@@ -93,6 +102,9 @@ __global__ void __launch_bounds__(1024) hcmix_expert_sort_kernel(const SortArgs 
     key = next;
   }
   __syncthreads();
+  // A block's memory is there for others from its start to its end: they are touched
+  // between the barrier on which every block arrives when it starts, and the next one.
+  if (ctas > 1) cluster_wait();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int s = 0;
 #pragma unroll 4
@@ -103,7 +115,6 @@ __global__ void __launch_bounds__(1024) hcmix_expert_sort_kernel(const SortArgs 
     }
     for (int b = 0; b < ctas; ++b) cluster.map_shared_rank(totals, b)[cta * E + e] = s;
   }
-  // after this no block touches another's memory
   if (ctas > 1)
     cluster.sync();
   else
