@@ -68,6 +68,13 @@ def lib() -> ctypes.CDLL:
 
 _empty = torch.empty
 _F32, _I32 = torch.float32, torch.int32
+_device = torch._C._cuda_getDevice  # the current device's index
+
+
+def _there(device, call, *args, **kw):
+    """call(*args) with the tensors' device current: the library launches on the current one."""
+    with torch.cuda.device(device):
+        return call(*args, **kw)
 
 
 def _stream(stream, t: torch.Tensor):
@@ -169,6 +176,9 @@ def hc_mix_layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5
     bias[N] (fp32 or x's type; None: ones, zeros); with want_stats (y, mean[M],
     rstd[M]), which hc_mix_layer_norm_backward takes."""
     px, sx, code, M, N, dtype, device = _matrix(x, "x")
+    if device.index != _device():
+        return _there(device, hc_mix_layer_norm, x, weight, bias, eps, want_stats, out,
+                      stream=stream)
     pw, pb, ptype = _params(weight, bias, dtype, N, device)
     y = _output(out, (M, N), dtype, device)
     mean, rstd = (_f32((M,), device), _f32((M,), device)) if want_stats else (None, None)
@@ -190,6 +200,9 @@ def hc_mix_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Te
     fp32 (with want_params=False only dx).  `workspace`: a uint8 tensor of
     layer_norm_workspace_bytes() bytes, allocated here if not given."""
     px, sx, code, M, N, dtype, device = _matrix(x, "x")
+    if device.index != _device():
+        return _there(device, hc_mix_layer_norm_backward, dy, x, mean, rstd, weight, want_params,
+                      out, workspace, stream=stream)
     pd, sd = _like(dy, "dy", (M, N), dtype, device)
     pm, pr = _floats(mean, "mean", (M,), device), _floats(rstd, "rstd", (M,), device)
     pw, _, ptype = _params(weight, None, dtype, N, device)
@@ -219,6 +232,8 @@ def hc_mix_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Te
 def hc_mix_collapse(x: torch.Tensor, pre: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     """h[M, D] = sum_i pre[:, i] x_i of the streams x[M, 4 * D]."""
     px, sx, code, M, K, dtype, device = _matrix(x, "x")
+    if device.index != _device():
+        return _there(device, hc_mix_collapse, x, pre, out, stream=stream)
     D = _width(K)
     pp = _floats(pre, "pre", (M, HC), device)
     h = _output(out, (M, D), dtype, device)
@@ -233,6 +248,9 @@ def hc_mix_collapse_norm(x: torch.Tensor, pre: torch.Tensor, weight=None, bias=N
     """y[M, D], the layer norm of hc_mix_collapse's h in one pass over x; with
     want_saved (y, h, mean, rstd), for hc_mix_layer_norm_backward on h."""
     px, sx, code, M, K, dtype, device = _matrix(x, "x")
+    if device.index != _device():
+        return _there(device, hc_mix_collapse_norm, x, pre, weight, bias, eps, want_saved, out,
+                      stream=stream)
     D = _width(K)
     pp = _floats(pre, "pre", (M, HC), device)
     pw, pb, ptype = _params(weight, bias, dtype, D, device)
@@ -253,6 +271,8 @@ def hc_mix_collapse_backward(dh: torch.Tensor, x: torch.Tensor, pre: torch.Tenso
     """(dx[M, 4 * D], dpre[M, 4]) of hc_mix_collapse, dx with dx_add[M, 4 * D]
     added (the gradient of x through hc_mix_expand); out may be dx_add."""
     px, sx, code, M, K, dtype, device = _matrix(x, "x")
+    if device.index != _device():
+        return _there(device, hc_mix_collapse_backward, dh, x, pre, dx_add, out, stream=stream)
     D = _width(K)
     pd, sd = _like(dh, "dh", (M, D), dtype, device)
     pa, sa = (None, 0) if dx_add is None else _like(dx_add, "dx_add", (M, K), dtype, device)
@@ -271,6 +291,8 @@ def hc_mix_expand(x: torch.Tensor, y: torch.Tensor, post: torch.Tensor, comb: to
     """The next streams [M, 4 * D]: stream i is post[:, i] y + sum_j
     comb[:, i, j] x_j.  out may be x."""
     px, sx, code, M, K, dtype, device = _matrix(x, "x")
+    if device.index != _device():
+        return _there(device, hc_mix_expand, x, y, post, comb, out, stream=stream)
     D = _width(K)
     py, sy = _like(y, "y", (M, D), dtype, device)
     pp, pc = _floats(post, "post", (M, HC), device), _floats(comb, "comb", (M, HC, HC), device)
@@ -287,6 +309,8 @@ def hc_mix_expand_backward(dout: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
     """(dx[M, 4 * D], dy[M, D], dpost[M, 4], dcomb[M, 4, 4]) of hc_mix_expand;
     out (for dx) may be dout."""
     px, sx, code, M, K, dtype, device = _matrix(x, "x")
+    if device.index != _device():
+        return _there(device, hc_mix_expand_backward, dout, x, y, post, comb, out, stream=stream)
     D = _width(K)
     pd, sd = _like(dout, "dout", (M, K), dtype, device)
     py, sy = _like(y, "y", (M, D), dtype, device)
@@ -316,6 +340,8 @@ def hc_mix_expert_sort(ids: torch.Tensor, n_experts: int, stream=None):
         raise ValueError("ids must be a contiguous 2-D CUDA tensor of int32 or int64")
     T, k = shape
     device = ids.device
+    if device.index != _device():
+        return _there(device, hc_mix_expert_sort, ids, n_experts, stream=stream)
     offsets = _empty(n_experts + 1 if n_experts > 0 else 1, dtype=_I32, device=device)
     slots = _empty(shape, dtype=_I32, device=device)
     source = _empty(T * k, dtype=_I32, device=device)
@@ -345,6 +371,8 @@ def hc_mix_expert_dispatch(x: torch.Tensor, slots: torch.Tensor, offsets=None, o
     """xs[T * k, D] with xs[slots[t, j]] = x[t] and zeros from row offsets[E] on
     (without offsets those rows are left as they are)."""
     px, sx, code, T, D, dtype, device = _matrix(x, "x")
+    if device.index != _device():
+        return _there(device, hc_mix_expert_dispatch, x, slots, offsets, out, stream=stream)
     ps, k = _slots(slots, T, device)
     po, E = _offsets(offsets, device)
     xs = _output(out, (T * k, D), dtype, device)
@@ -360,6 +388,8 @@ def hc_mix_expert_combine(ys: torch.Tensor, slots: torch.Tensor, weights=None, o
     """y[T, D] with y[t] = sum_j weights[t, j] ys[slots[t, j]]; without weights,
     of ones: the gradient of hc_mix_expert_dispatch."""
     py, sy, code, rows, D, dtype, device = _matrix(ys, "ys")
+    if device.index != _device():
+        return _there(device, hc_mix_expert_combine, ys, slots, weights, out, stream=stream)
     T = slots.shape[0]
     ps, k = _slots(slots, T, device)
     pw = None if weights is None else _floats(weights, "weights", (T, k), device)
@@ -377,6 +407,9 @@ def hc_mix_expert_combine_backward(dy: torch.Tensor, ys: torch.Tensor, slots: to
     weights[t, j] dy[t], zeros from row offsets[E] on (offsets None: left as
     they are), dweights[t, j] = dy[t] . ys[slots[t, j]]."""
     py, sy, code, rows, D, dtype, device = _matrix(ys, "ys")
+    if device.index != _device():
+        return _there(device, hc_mix_expert_combine_backward, dy, ys, slots, offsets, weights, out,
+                      stream=stream)
     T = dy.shape[0]
     pd, sd = _like(dy, "dy", (T, D), dtype, device)
     ps, k = _slots(slots, T, device)

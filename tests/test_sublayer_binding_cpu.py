@@ -1,0 +1,131 @@
+"""Where the sublayer binding's calls go, checked without a GPU: stand-ins for CUDA tensors,
+streams and the library record the device and the stream under which each thing happens."""
+import contextlib
+
+import pytest
+import torch
+
+from hyper_connection_mix_gb300 import sublayer as sub
+
+BF16, F32, I32, I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+M, D, E, K = 6, 32, 8, 2
+
+
+class Tensor:
+    """As much of a contiguous CUDA tensor as the binding looks at."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device, place=None):
+        shape = (shape,) if isinstance(shape, int) else shape
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device(device)
+        self.place = place  # the (device, stream) that it was allocated under
+        self.on = []        # the streams that it was recorded on
+
+    def stride(self):
+        return (self.shape[1], 1)
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.device.index
+
+    def data_ptr(self):
+        return 0x10000
+
+    def record_stream(self, stream):
+        self.on.append(stream.cuda_stream)
+
+
+class Cuda:
+    """The current device, each device's current stream, and what happened where."""
+
+    def __init__(self):
+        self.device, self.streams = 0, {0: 100, 1: 200}
+        self.allocated, self.called = [], []
+
+    def where(self):
+        return self.device, self.streams[self.device]
+
+    def empty(self, shape, dtype, device):
+        self.allocated.append(Tensor(shape, dtype, device, self.where()))
+        return self.allocated[-1]
+
+    def __getattr__(self, name):  # an entry point of the library
+        def call(*args):
+            if name.endswith("_bytes"):
+                return 1024
+            self.called.append((name, self.where(), args[-1]))
+            return 0
+        return call
+
+    @contextlib.contextmanager
+    def on_device(self, device):
+        before, self.device = self.device, torch.device(device).index
+        yield
+        self.device = before
+
+
+@pytest.fixture
+def cuda(monkeypatch):
+    c = Cuda()
+    monkeypatch.setattr(sub, "lib", lambda: c)
+    monkeypatch.setattr(sub, "_empty", c.empty)
+    monkeypatch.setattr(sub, "_device", lambda: c.device, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: c.streams[i], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", c.on_device)
+    return c
+
+
+def entry_points(device):
+    """Every call of the module on tensors of `device`."""
+    t = lambda dtype, *shape: Tensor(shape, dtype, device)  # noqa: E731
+    x, y, h = t(BF16, M, 4 * D), t(BF16, M, D), t(BF16, M, D)
+    pre, post, comb = t(F32, M, 4), t(F32, M, 4), t(F32, M, 4, 4)
+    mean, rstd, weight = t(F32, M), t(F32, M), t(F32, D)
+    slots, offsets, weights = t(I32, M, K), t(I32, E + 1), t(F32, M, K)
+    ys = t(BF16, M * K, D)
+    return {
+        "hc_mix_layer_norm": ((y, weight, weight), {"want_stats": True}),
+        "hc_mix_layer_norm_backward": ((h, y, mean, rstd, weight), {}),
+        "hc_mix_collapse": ((x, pre), {}),
+        "hc_mix_collapse_norm": ((x, pre, weight, weight), {"want_saved": True}),
+        "hc_mix_collapse_backward": ((h, x, pre), {"dx_add": t(BF16, M, 4 * D)}),
+        "hc_mix_expand": ((x, y, post, comb), {}),
+        "hc_mix_expand_backward": ((t(BF16, M, 4 * D), x, y, post, comb), {}),
+        "hc_mix_expert_sort": ((t(I64, M, K), E), {}),
+        "hc_mix_expert_dispatch": ((y, slots, offsets), {}),
+        "hc_mix_expert_combine": ((ys, slots, weights), {}),
+        "hc_mix_expert_combine_backward": ((y, ys, slots, offsets, weights), {}),
+    }
+
+
+NAMES = list(entry_points("cuda:0"))
+
+
+def test_every_entry_point_is_here():
+    assert sorted(NAMES) == sorted(n for n in sub.EXPORTS if not n.endswith("_bytes"))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_call_goes_to_the_current_stream(cuda, name):
+    args, kw = entry_points("cuda:0")[name]
+    getattr(sub, name)(*args, **kw)
+    assert cuda.called == [(name, (0, 100), 100)]
+    assert {t.place for t in cuda.allocated} == {(0, 100)}
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_call_goes_to_the_device_of_its_tensors(cuda, name):
+    """The library launches on the current device: it is the tensors' during the call."""
+    args, kw = entry_points("cuda:1")[name]
+    getattr(sub, name)(*args, **kw)
+    assert cuda.called == [(name, (1, 200), 200)]
+    assert {t.device.index for t in cuda.allocated} == {1}
+    assert cuda.device == 0
