@@ -8,6 +8,12 @@ here (or given with `out`), a call goes to the current stream of its tensors'
 device unless `stream` says otherwise, and a non-OK status raises HcMixError.
 There is no CPU fallback.
 
+With `stream` (a torch stream or a raw handle) outputs are allocated there, as
+in a `with torch.cuda.stream(...)` block.  The caller orders the streams' work, as
+for any kernel; tensors may be let go at once on either side, since the inputs are
+recorded on `stream` and the outputs on the stream that was current.  That
+takes about 25 us of host time a call (a stream that is current, about 6).
+
 Matrices are 2-D CUDA tensors of one type (bf16, fp16 or fp32) with unit inner
 stride; coefficients, statistics and expert weights are contiguous fp32.
 """
@@ -71,16 +77,37 @@ _F32, _I32 = torch.float32, torch.int32
 _device = torch._C._cuda_getDevice  # the current device's index
 
 
-def _there(device, call, *args, **kw):
-    """call(*args) with the tensors' device current: the library launches on the current one."""
-    with torch.cuda.device(device):
-        return call(*args, **kw)
-
-
-def _stream(stream, t: torch.Tensor):
+def _there(stream, device, call, *args):
+    """call(*args) with the tensors' device current (the library launches on the current one) and,
+    if given, on `stream`: what the call allocates and frees is memory of the stream that uses it.
+    """
+    if device.index != _device():
+        with torch.cuda.device(device):
+            return _there(stream, device, call, *args)
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    return binding._stream(stream)
+        return call(*args)
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError("stream must be of the device of the matrices")
+    handle = binding._stream(stream)
+    if handle == torch._C._cuda_getCurrentRawStream(device.index):
+        return call(*args)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle
+                  else torch.cuda.default_stream(device))
+    before = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        result = call(*args)
+    # either stream may still use a tensor when its last reference goes
+    for t in args:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+    for t in result if isinstance(result, tuple) else (result,):
+        t.record_stream(before)
+    return result
+
+
+def _stream(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _matrix(t: torch.Tensor, name: str):
@@ -176,14 +203,13 @@ def hc_mix_layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5
     bias[N] (fp32 or x's type; None: ones, zeros); with want_stats (y, mean[M],
     rstd[M]), which hc_mix_layer_norm_backward takes."""
     px, sx, code, M, N, dtype, device = _matrix(x, "x")
-    if device.index != _device():
-        return _there(device, hc_mix_layer_norm, x, weight, bias, eps, want_stats, out,
-                      stream=stream)
+    if stream is not None or device.index != _device():
+        return _there(stream, device, hc_mix_layer_norm, x, weight, bias, eps, want_stats, out)
     pw, pb, ptype = _params(weight, bias, dtype, N, device)
     y = _output(out, (M, N), dtype, device)
     mean, rstd = (_f32((M,), device), _f32((M,), device)) if want_stats else (None, None)
     st = lib().hc_mix_layer_norm(px, sx, code, M, N, pw, pb, ptype, eps, y.data_ptr(), _ptr(mean),
-                                 _ptr(rstd), _stream(stream, x))
+                                 _ptr(rstd), _stream(x))
     if st:
         _check(st, "hc_mix_layer_norm")
     return (y, mean, rstd) if want_stats else y
@@ -200,9 +226,9 @@ def hc_mix_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Te
     fp32 (with want_params=False only dx).  `workspace`: a uint8 tensor of
     layer_norm_workspace_bytes() bytes, allocated here if not given."""
     px, sx, code, M, N, dtype, device = _matrix(x, "x")
-    if device.index != _device():
-        return _there(device, hc_mix_layer_norm_backward, dy, x, mean, rstd, weight, want_params,
-                      out, workspace, stream=stream)
+    if stream is not None or device.index != _device():
+        return _there(stream, device, hc_mix_layer_norm_backward, dy, x, mean, rstd, weight,
+                      want_params, out, workspace)
     pd, sd = _like(dy, "dy", (M, N), dtype, device)
     pm, pr = _floats(mean, "mean", (M,), device), _floats(rstd, "rstd", (M,), device)
     pw, _, ptype = _params(weight, None, dtype, N, device)
@@ -220,7 +246,7 @@ def hc_mix_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Te
     st = L.hc_mix_layer_norm_backward(pd, sd, px, sx, code, M, N, pm, pr, pw, ptype, dx.data_ptr(),
                                       _ptr(dweight), _ptr(dbias),
                                       _ptr(workspace) if want_params else None, nbytes,
-                                      _stream(stream, x))
+                                      _stream(x))
     if st:
         _check(st, "hc_mix_layer_norm_backward")
     return (dx, dweight, dbias) if want_params else dx
@@ -232,12 +258,12 @@ def hc_mix_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Te
 def hc_mix_collapse(x: torch.Tensor, pre: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     """h[M, D] = sum_i pre[:, i] x_i of the streams x[M, 4 * D]."""
     px, sx, code, M, K, dtype, device = _matrix(x, "x")
-    if device.index != _device():
-        return _there(device, hc_mix_collapse, x, pre, out, stream=stream)
+    if stream is not None or device.index != _device():
+        return _there(stream, device, hc_mix_collapse, x, pre, out)
     D = _width(K)
     pp = _floats(pre, "pre", (M, HC), device)
     h = _output(out, (M, D), dtype, device)
-    st = lib().hc_mix_collapse(px, sx, code, M, D, HC, pp, h.data_ptr(), _stream(stream, x))
+    st = lib().hc_mix_collapse(px, sx, code, M, D, HC, pp, h.data_ptr(), _stream(x))
     if st:
         _check(st, "hc_mix_collapse")
     return h
@@ -248,9 +274,9 @@ def hc_mix_collapse_norm(x: torch.Tensor, pre: torch.Tensor, weight=None, bias=N
     """y[M, D], the layer norm of hc_mix_collapse's h in one pass over x; with
     want_saved (y, h, mean, rstd), for hc_mix_layer_norm_backward on h."""
     px, sx, code, M, K, dtype, device = _matrix(x, "x")
-    if device.index != _device():
-        return _there(device, hc_mix_collapse_norm, x, pre, weight, bias, eps, want_saved, out,
-                      stream=stream)
+    if stream is not None or device.index != _device():
+        return _there(stream, device, hc_mix_collapse_norm, x, pre, weight, bias, eps,
+                      want_saved, out)
     D = _width(K)
     pp = _floats(pre, "pre", (M, HC), device)
     pw, pb, ptype = _params(weight, bias, dtype, D, device)
@@ -260,7 +286,7 @@ def hc_mix_collapse_norm(x: torch.Tensor, pre: torch.Tensor, weight=None, bias=N
         h = _empty((M, D), dtype=dtype, device=device)
         mean, rstd = _f32((M,), device), _f32((M,), device)
     st = lib().hc_mix_collapse_norm(px, sx, code, M, D, HC, pp, pw, pb, ptype, eps, y.data_ptr(),
-                                    _ptr(h), _ptr(mean), _ptr(rstd), _stream(stream, x))
+                                    _ptr(h), _ptr(mean), _ptr(rstd), _stream(x))
     if st:
         _check(st, "hc_mix_collapse_norm")
     return (y, h, mean, rstd) if want_saved else y
@@ -271,8 +297,8 @@ def hc_mix_collapse_backward(dh: torch.Tensor, x: torch.Tensor, pre: torch.Tenso
     """(dx[M, 4 * D], dpre[M, 4]) of hc_mix_collapse, dx with dx_add[M, 4 * D]
     added (the gradient of x through hc_mix_expand); out may be dx_add."""
     px, sx, code, M, K, dtype, device = _matrix(x, "x")
-    if device.index != _device():
-        return _there(device, hc_mix_collapse_backward, dh, x, pre, dx_add, out, stream=stream)
+    if stream is not None or device.index != _device():
+        return _there(stream, device, hc_mix_collapse_backward, dh, x, pre, dx_add, out)
     D = _width(K)
     pd, sd = _like(dh, "dh", (M, D), dtype, device)
     pa, sa = (None, 0) if dx_add is None else _like(dx_add, "dx_add", (M, K), dtype, device)
@@ -280,7 +306,7 @@ def hc_mix_collapse_backward(dh: torch.Tensor, x: torch.Tensor, pre: torch.Tenso
     dx = _output(out, (M, K), dtype, device)
     dpre = _f32((M, HC), device)
     st = lib().hc_mix_collapse_backward(pd, sd, px, sx, pa, sa, code, M, D, HC, pp, dx.data_ptr(),
-                                        dpre.data_ptr(), _stream(stream, x))
+                                        dpre.data_ptr(), _stream(x))
     if st:
         _check(st, "hc_mix_collapse_backward")
     return dx, dpre
@@ -291,14 +317,14 @@ def hc_mix_expand(x: torch.Tensor, y: torch.Tensor, post: torch.Tensor, comb: to
     """The next streams [M, 4 * D]: stream i is post[:, i] y + sum_j
     comb[:, i, j] x_j.  out may be x."""
     px, sx, code, M, K, dtype, device = _matrix(x, "x")
-    if device.index != _device():
-        return _there(device, hc_mix_expand, x, y, post, comb, out, stream=stream)
+    if stream is not None or device.index != _device():
+        return _there(stream, device, hc_mix_expand, x, y, post, comb, out)
     D = _width(K)
     py, sy = _like(y, "y", (M, D), dtype, device)
     pp, pc = _floats(post, "post", (M, HC), device), _floats(comb, "comb", (M, HC, HC), device)
     out = _output(out, (M, K), dtype, device)
     st = lib().hc_mix_expand(px, sx, py, sy, code, M, D, HC, pp, pc, out.data_ptr(),
-                             _stream(stream, x))
+                             _stream(x))
     if st:
         _check(st, "hc_mix_expand")
     return out
@@ -309,8 +335,8 @@ def hc_mix_expand_backward(dout: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
     """(dx[M, 4 * D], dy[M, D], dpost[M, 4], dcomb[M, 4, 4]) of hc_mix_expand;
     out (for dx) may be dout."""
     px, sx, code, M, K, dtype, device = _matrix(x, "x")
-    if device.index != _device():
-        return _there(device, hc_mix_expand_backward, dout, x, y, post, comb, out, stream=stream)
+    if stream is not None or device.index != _device():
+        return _there(stream, device, hc_mix_expand_backward, dout, x, y, post, comb, out)
     D = _width(K)
     pd, sd = _like(dout, "dout", (M, K), dtype, device)
     py, sy = _like(y, "y", (M, D), dtype, device)
@@ -320,7 +346,7 @@ def hc_mix_expand_backward(dout: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
     dpost, dcomb = _f32((M, HC), device), _f32((M, HC, HC), device)
     st = lib().hc_mix_expand_backward(pd, sd, px, sx, py, sy, code, M, D, HC, pp, pc, dx.data_ptr(),
                                       dy.data_ptr(), dpost.data_ptr(), dcomb.data_ptr(),
-                                      _stream(stream, x))
+                                      _stream(x))
     if st:
         _check(st, "hc_mix_expand_backward")
     return dx, dy, dpost, dcomb
@@ -340,14 +366,14 @@ def hc_mix_expert_sort(ids: torch.Tensor, n_experts: int, stream=None):
         raise ValueError("ids must be a contiguous 2-D CUDA tensor of int32 or int64")
     T, k = shape
     device = ids.device
-    if device.index != _device():
-        return _there(device, hc_mix_expert_sort, ids, n_experts, stream=stream)
+    if stream is not None or device.index != _device():
+        return _there(stream, device, hc_mix_expert_sort, ids, n_experts)
     offsets = _empty(n_experts + 1 if n_experts > 0 else 1, dtype=_I32, device=device)
     slots = _empty(shape, dtype=_I32, device=device)
     source = _empty(T * k, dtype=_I32, device=device)
     st = lib().hc_mix_expert_sort(ids.data_ptr(), 8 if wide else 4, T, k, n_experts,
                                   offsets.data_ptr(), slots.data_ptr(), source.data_ptr(),
-                                  _stream(stream, ids))
+                                  _stream(ids))
     if st:
         _check(st, "hc_mix_expert_sort")
     return offsets, slots, source
@@ -371,13 +397,13 @@ def hc_mix_expert_dispatch(x: torch.Tensor, slots: torch.Tensor, offsets=None, o
     """xs[T * k, D] with xs[slots[t, j]] = x[t] and zeros from row offsets[E] on
     (without offsets those rows are left as they are)."""
     px, sx, code, T, D, dtype, device = _matrix(x, "x")
-    if device.index != _device():
-        return _there(device, hc_mix_expert_dispatch, x, slots, offsets, out, stream=stream)
+    if stream is not None or device.index != _device():
+        return _there(stream, device, hc_mix_expert_dispatch, x, slots, offsets, out)
     ps, k = _slots(slots, T, device)
     po, E = _offsets(offsets, device)
     xs = _output(out, (T * k, D), dtype, device)
     st = lib().hc_mix_expert_dispatch(px, sx, code, T, k, D, ps, po, E, xs.data_ptr(),
-                                      _stream(stream, x))
+                                      _stream(x))
     if st:
         _check(st, "hc_mix_expert_dispatch")
     return xs
@@ -388,14 +414,14 @@ def hc_mix_expert_combine(ys: torch.Tensor, slots: torch.Tensor, weights=None, o
     """y[T, D] with y[t] = sum_j weights[t, j] ys[slots[t, j]]; without weights,
     of ones: the gradient of hc_mix_expert_dispatch."""
     py, sy, code, rows, D, dtype, device = _matrix(ys, "ys")
-    if device.index != _device():
-        return _there(device, hc_mix_expert_combine, ys, slots, weights, out, stream=stream)
+    if stream is not None or device.index != _device():
+        return _there(stream, device, hc_mix_expert_combine, ys, slots, weights, out)
     T = slots.shape[0]
     ps, k = _slots(slots, T, device)
     pw = None if weights is None else _floats(weights, "weights", (T, k), device)
     y = _output(out, (T, D), dtype, device)
     st = lib().hc_mix_expert_combine(py, sy, code, rows, T, k, D, ps, pw, y.data_ptr(),
-                                     _stream(stream, ys))
+                                     _stream(ys))
     if st:
         _check(st, "hc_mix_expert_combine")
     return y
@@ -407,9 +433,9 @@ def hc_mix_expert_combine_backward(dy: torch.Tensor, ys: torch.Tensor, slots: to
     weights[t, j] dy[t], zeros from row offsets[E] on (offsets None: left as
     they are), dweights[t, j] = dy[t] . ys[slots[t, j]]."""
     py, sy, code, rows, D, dtype, device = _matrix(ys, "ys")
-    if device.index != _device():
-        return _there(device, hc_mix_expert_combine_backward, dy, ys, slots, offsets, weights, out,
-                      stream=stream)
+    if stream is not None or device.index != _device():
+        return _there(stream, device, hc_mix_expert_combine_backward, dy, ys, slots, offsets,
+                      weights, out)
     T = dy.shape[0]
     pd, sd = _like(dy, "dy", (T, D), dtype, device)
     ps, k = _slots(slots, T, device)
@@ -419,7 +445,7 @@ def hc_mix_expert_combine_backward(dy: torch.Tensor, ys: torch.Tensor, slots: to
     dweights = _f32((T, k), device)
     st = lib().hc_mix_expert_combine_backward(pd, sd, py, sy, code, rows, T, k, D, ps, po, E, pw,
                                               dys.data_ptr(), dweights.data_ptr(),
-                                              _stream(stream, ys))
+                                              _stream(ys))
     if st:
         _check(st, "hc_mix_expert_combine_backward")
     return dys, dweights

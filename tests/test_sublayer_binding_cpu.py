@@ -43,6 +43,14 @@ class Tensor:
         self.on.append(stream.cuda_stream)
 
 
+class Stream:
+    def __init__(self, handle, device="cuda:0"):
+        self.cuda_stream, self.device = handle, torch.device(device)
+
+    def __eq__(self, other):
+        return self.cuda_stream == other.cuda_stream
+
+
 class Cuda:
     """The current device, each device's current stream, and what happened where."""
 
@@ -71,6 +79,13 @@ class Cuda:
         yield
         self.device = before
 
+    @contextlib.contextmanager
+    def on_stream(self, stream):
+        at = stream.device.index
+        before, self.streams[at] = self.streams[at], stream.cuda_stream
+        yield
+        self.streams[at] = before
+
 
 @pytest.fixture
 def cuda(monkeypatch):
@@ -80,6 +95,12 @@ def cuda(monkeypatch):
     monkeypatch.setattr(sub, "_device", lambda: c.device, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: c.streams[i], raising=False)
     monkeypatch.setattr(torch.cuda, "device", c.on_device)
+    monkeypatch.setattr(torch.cuda, "stream", c.on_stream)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch, "Tensor", Tensor)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device: Stream(h, device))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: Stream(0, device))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream(c.where()[1], f"cuda:{c.device}"))
     return c
 
 
@@ -129,3 +150,34 @@ def test_a_call_goes_to_the_device_of_its_tensors(cuda, name):
     assert cuda.called == [(name, (1, 200), 200)]
     assert {t.device.index for t in cuda.allocated} == {1}
     assert cuda.device == 0
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("stream,handle", [(Stream(300), 300), (301, 301), (0, 0)],
+                         ids=["stream", "handle", "default"])
+def test_memory_belongs_to_the_stream_that_uses_it(cuda, name, stream, handle):
+    """With `stream`, outputs and workspaces are allocated under it; the inputs are recorded on
+    it, and the outputs on the stream that the caller goes on with."""
+    args, kw = entry_points("cuda:0")[name]
+    result = getattr(sub, name)(*args, **kw, stream=stream)
+    assert cuda.called == [(name, (0, handle), handle)]
+    assert {t.place for t in cuda.allocated} == {(0, handle)}
+    inputs = [t for t in (*args, *kw.values()) if isinstance(t, Tensor)]
+    assert {tuple(t.on) for t in inputs} <= {(handle,), (handle, handle)}  # weight given as bias too
+    outputs = result if isinstance(result, tuple) else (result,)
+    assert {tuple(t.on) for t in outputs} == {(100,)}
+    assert cuda.where() == (0, 100)
+
+
+@pytest.mark.parametrize("stream", [Stream(100), 100], ids=["stream", "handle"])
+def test_the_current_stream_given_by_name(cuda, stream):
+    y = Tensor((M, D), BF16, "cuda:0")
+    out = sub.hc_mix_layer_norm(y, stream=stream)
+    assert cuda.called == [("hc_mix_layer_norm", (0, 100), 100)]
+    assert out.place == (0, 100) and not out.on and not y.on
+
+
+def test_a_stream_of_another_device_is_refused(cuda):
+    with pytest.raises(ValueError):
+        sub.hc_mix_layer_norm(Tensor((M, D), BF16, "cuda:0"), stream=Stream(300, "cuda:1"))
+    assert not cuda.called
