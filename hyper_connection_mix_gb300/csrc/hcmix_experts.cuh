@@ -29,7 +29,15 @@ constexpr int64_t kSortAlone = 512;
 // a pair, are shared out over them: 32768 pairs of 128 experts take 16 blocks 8.0 us
 // (8 blocks, before the loops were rolled, 10.3 us).  Each holds a row of totals for
 // every block, 64 KB in all.
-inline int sort_blocks(int64_t n, int64_t E) { return n <= kSortAlone ? 1 : E <= 1024 ? 16 : 4; }
+constexpr int kSortBlocks = 16, kSortBlocksWide = 4, kSortWide = 1024;  // past so many experts
+inline int sort_blocks(int64_t n, int64_t E) { 
+  return n <= kSortAlone ? 1 : E <= kSortWide ? kSortBlocks : kSortBlocksWide;
+}
+// The most shared memory that a sort takes: counters, totals, starts and the scan's sums.
+constexpr int kSortRows = (kSortBlocks + 1) * kSortWide > (kSortBlocksWide + 1) * kMostExperts
+                              ? (kSortBlocks + 1) * kSortWide
+                              : (kSortBlocksWide + 1) * kMostExperts;
+constexpr size_t kSortMost = ((size_t)kSortCounters + kSortRows + 32) * 4;
 
 template <typename Id>
 __device__ __forceinline__ int expert_of(const SortArgs& A, int64_t i) {
@@ -181,8 +189,8 @@ hcmix_status launch_sort(const SortArgs& A, cudaStream_t stream) {
                                        cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
                       cudaSuccess)
     return HCMIX_ERR_CUDA;
-  return launch(hcmix_expert_sort_kernel<Id>, dim3(ctas), dim3((unsigned)warps * 32), smem, stream, A,
-                ctas);
+  return launch(hcmix_expert_sort_kernel<Id>, dim3(ctas), dim3((unsigned)warps * 32), smem,
+                kSortMost, stream, A, ctas);
 }
 
 inline hcmix_status run_sort(const SortArgs& A, bool wide_ids, cudaStream_t stream) {
@@ -328,7 +336,7 @@ hcmix_status launch_rows(RowsOp op, RowsArgs A, cudaStream_t stream) {
     int64_t blocks = (A.T * A.k + kPairWarps - 1) / kPairWarps;
     blocks = blocks > 0 ? blocks : 1;
     return launch(hcmix_expert_combine_backward_kernel<T, kVec, kU>, dim3((unsigned)blocks),
-                  dim3(32 * kPairWarps), 0, stream, A);
+                  dim3(32 * kPairWarps), 0, 0, stream, A);
   }
   // Combine has four of a token's rows under way, in blocks of 128 threads: 4096 tokens of 8
   // rows of 5120 bf16 take 53.4 us, in blocks of 256 threads 54.9 us, two rows at a time 59.8 us,
@@ -347,7 +355,7 @@ hcmix_status launch_rows(RowsOp op, RowsArgs A, cudaStream_t stream) {
   const auto kernel = one       ? hcmix_expert_combine_kernel<T, kVec, kOneU, 1>
                       : combine ? hcmix_expert_combine_kernel<T, kVec, kU, kBatch>
                                 : hcmix_expert_dispatch_kernel<T, kVec, kU>;
-  return launch(kernel, dim3((unsigned)blocks), dim3(threads), 0, stream, A);
+  return launch(kernel, dim3((unsigned)blocks), dim3(threads), 0, 0, stream, A);
 }
 
 inline hcmix_status run_rows(RowsOp op, const RowsArgs& A, hcmix_type type, cudaStream_t stream) {

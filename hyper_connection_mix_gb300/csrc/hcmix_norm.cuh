@@ -156,9 +156,9 @@ struct Ring {
         step(blockDim.x * kVec) {
     base = smem + threadIdx.y * (kStages * group());
   }
-  // Bytes of a team's ring.
-  static size_t bytes(int threads) {
-    return (size_t)kStages * kRows * (kPer * threads * sizeof(V) + (kOwn ? 0 : 16));
+  // Bytes of a block's rings: `teams` of `threads` threads.
+  static constexpr size_t bytes(int threads, int teams) {
+    return (size_t)kStages * kRows * teams * (kPer * threads * sizeof(V) + (kOwn ? 0 : 16));
   }
   __device__ __forceinline__ int row() const { return kPer * pitch + (kOwn ? 0 : 16); }
   __device__ __forceinline__ int group() const { return kRows * row(); }
@@ -231,6 +231,7 @@ struct Shape {
   static constexpr int kUnits = kUnits_, kThreads = kThreads_, kBlocks = kBlocks_;
   static constexpr int kRowBytes = kUnits * kThreads * 16;
   static constexpr int kLeast = (kOver_ / 16 / kUnits + 1 + 31) / 32 * 32;
+  static constexpr int kTeams = kThreads / kLeast;  // at most
   template <int kPer>
   static constexpr int kFull = kPer - (32 * kPer + kLeast - 1) / kLeast;
 };
@@ -238,6 +239,10 @@ template <typename S, int kRows>
 constexpr int kFit = 200 * 1024 / (S::kBlocks * kRows * S::kRowBytes);
 template <typename S, int kRows>
 constexpr int kStagesOf = kFit<S, kRows> > 8 ? 8 : kFit<S, kRows> < 2 ? 2 : kFit<S, kRows>;
+
+// The most shared memory that a kernel of ring R and shape S takes.
+template <typename R, typename S>
+constexpr size_t ring_most = R::bytes(S::kThreads / S::kTeams, S::kTeams);
 
 struct RingPlan {
   int threads, teams, blocks;  // of a team; of a block
@@ -386,11 +391,9 @@ template <typename T, int kVec, typename S, bool kCollapse>
 hcmix_status launch_norm_ring(const NormArgs& A, cudaStream_t stream) {
   constexpr int kRows = kCollapse ? kStreams : 1;
   const RingPlan p = ring_plan<S>(A.N * (int64_t)sizeof(T), A.M);
-  const size_t smem =
-      p.teams * Ring<T, kVec, S::kUnits * 16 / (kVec * (int)sizeof(T)), kRows,
-                     kStagesOf<S, kRows>, 0>::bytes(p.threads);
+  using R = Ring<T, kVec, S::kUnits * 16 / (kVec * (int)sizeof(T)), kRows, kStagesOf<S, kRows>, 0>;
   return launch(hcmix_norm_kernel<T, kVec, S, kCollapse>, dim3(p.blocks),
-                dim3(p.threads, p.teams), smem, stream, A);
+                dim3(p.threads, p.teams), R::bytes(p.threads, p.teams), ring_most<R, S>, stream, A);
 }
 
 // The shape goes by type, alignment and width, never by the number of rows: a row's
@@ -416,7 +419,7 @@ hcmix_status launch_norm(const NormArgs& A, cudaStream_t stream) {
     if constexpr (sizeof(T) == 4)
       if (bytes <= S5::kRowBytes) return launch_norm_ring<T, kVec, S5, false>(A, stream);
   }
-  return launch(hcmix_norm_wide_kernel<T, kVec, kCollapse>, dim3((unsigned)A.M), dim3(512), 0,
+  return launch(hcmix_norm_wide_kernel<T, kVec, kCollapse>, dim3((unsigned)A.M), dim3(512), 0, 0,
                 stream, A);
 }
 
@@ -732,7 +735,7 @@ hcmix_status launch_norm_backward_ring(const NormArgs& A, const RingPlan& p, cud
   using R = Ring<T, kVec, S::kUnits * 16 / (kVec * (int)sizeof(T)), 2 * kGroup,
                  kStagesOf<S, 2 * kGroup>, 0>;
   return launch(hcmix_norm_backward_kernel<T, kVec, S, kGroup>, dim3(p.blocks),
-                dim3(p.threads, p.teams), p.teams * R::bytes(p.threads), stream, A);
+                dim3(p.threads, p.teams), R::bytes(p.threads, p.teams), ring_most<R, S>, stream, A);
 }
 
 template <typename T, int kVec>
@@ -746,12 +749,12 @@ hcmix_status launch_norm_backward(NormArgs A, cudaStream_t stream) {
     const int64_t vecs = (A.N + kVec - 1) / kVec;
     const unsigned threads = vecs >= 256 ? 256 : (unsigned)(vecs + 31) / 32 * 32;
     if (A.M > 0)
-      st = launch(hcmix_norm_dx_kernel<T, kVec>, dim3((unsigned)A.M), dim3(threads), 0, stream, A);
+      st = launch(hcmix_norm_dx_kernel<T, kVec>, dim3((unsigned)A.M), dim3(threads), 0, 0, stream, A);
     if (st != HCMIX_OK || A.dweight == nullptr) return st;
     const int64_t per = (int64_t)kColumnThreads * kVec;
     if (A.blocks > 0)
       st = launch(hcmix_norm_columns_kernel<T, kVec>,
-                  dim3((unsigned)((A.N + per - 1) / per), A.blocks), dim3(kColumnThreads), 0,
+                  dim3((unsigned)((A.N + per - 1) / per), A.blocks), dim3(kColumnThreads), 0, 0,
                   stream, A);
   } else {
     switch (p.shape) {
@@ -763,7 +766,7 @@ hcmix_status launch_norm_backward(NormArgs A, cudaStream_t stream) {
   }
   if (st != HCMIX_OK) return st;
   return launch(hcmix_norm_join_kernel, dim3((unsigned)((2 * A.N + 31) / 32)),
-                dim3(32 * kJoinGroups), 0, stream, A);
+                dim3(32 * kJoinGroups), 0, 0, stream, A);
 }
 
 inline hcmix_status run_norm_backward(const NormArgs& A, hcmix_type type, cudaStream_t stream) {

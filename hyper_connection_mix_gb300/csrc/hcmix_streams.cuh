@@ -205,11 +205,11 @@ hcmix_status launch_streams(StreamsOp op, StreamsArgs A, cudaStream_t stream) {
     if (blocks >= ((int64_t)1 << 31)) return HCMIX_ERR_UNSUPPORTED;
     return launch(op == StreamsOp::kCollapse ? hcmix_collapse_kernel<T, kVec, kU>
                                              : hcmix_expand_kernel<T, kVec, kU>,
-                  dim3((unsigned)blocks), dim3(threads), 0, stream, A);
+                  dim3((unsigned)blocks), dim3(threads), 0, 0, stream, A);
   }
   return launch(op == StreamsOp::kCollapseBackward ? hcmix_collapse_backward_kernel<T, kVec, kU>
                                                    : hcmix_expand_backward_kernel<T, kVec, kU>,
-                dim3((unsigned)A.M), dim3(threads), 0, stream, A);
+                dim3((unsigned)A.M), dim3(threads), 0, 0, stream, A);
 }
 
 inline hcmix_status run_streams(StreamsOp op, const StreamsArgs& A, hcmix_type type,

@@ -560,13 +560,17 @@ inline hcmix_status with_vector(hcmix_type t, int bytes, F&& f) {
   });
 }
 
-// Launches a kernel that starts with begin_kernel(); `cluster` blocks a cluster.
+// Launches a kernel that starts with begin_kernel(); `cluster` blocks a cluster.  The kernel's
+// limit of dynamic shared memory is one for all threads of the process: it is set to `most`, the
+// most that any call of the kernel takes, so that no call lowers it under another's launch.
 template <typename Args>
 inline hcmix_status launch(void (*kernel)(const Args), dim3 grid, dim3 threads, size_t smem,
-                           cudaStream_t stream, const Args& args, unsigned cluster = 1) {
+                           size_t most, cudaStream_t stream, const Args& args,
+                           unsigned cluster = 1) {
+  if (smem > most) return HCMIX_ERR_UNSUPPORTED;
   // with its static shared memory a kernel may pass the default 48 KB sooner
   if (smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem) != cudaSuccess)
+                                               (int)most) != cudaSuccess)
     return HCMIX_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
