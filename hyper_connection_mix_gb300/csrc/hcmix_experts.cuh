@@ -185,10 +185,11 @@ hcmix_status launch_sort(const SortArgs& A, cudaStream_t stream) {
   const int most = kSortCounters / A.E < 32 ? kSortCounters / A.E : 32;
   warps = warps < 4 ? 4 : warps > most ? most : warps;
   const size_t smem = (((size_t)warps + ctas + 1) * A.E + 32) * 4;
-  if (ctas > 8 && cudaFuncSetAttribute(hcmix_expert_sort_kernel<Id>,
-                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-                      cudaSuccess)
-    return HCMIX_ERR_CUDA;
+  if (ctas > 8) {
+    const hcmix_status st = checked(cudaFuncSetAttribute(
+        hcmix_expert_sort_kernel<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    if (st != HCMIX_OK) return st;
+  }
   return launch(hcmix_expert_sort_kernel<Id>, dim3(ctas), dim3((unsigned)warps * 32), smem,
                 kSortMost, stream, A, ctas);
 }

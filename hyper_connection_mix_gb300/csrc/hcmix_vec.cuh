@@ -560,6 +560,14 @@ inline hcmix_status with_vector(hcmix_type t, int bytes, F&& f) {
   });
 }
 
+// HCMIX_OK, or HCMIX_ERR_CUDA with the error taken from the runtime, where a later call of
+// the process that asks for the last error would take it for its own.
+inline hcmix_status checked(cudaError_t e) {
+  if (e == cudaSuccess) return HCMIX_OK;
+  cudaGetLastError();
+  return HCMIX_ERR_CUDA;
+}
+
 // Launches a kernel that starts with begin_kernel(); `cluster` blocks a cluster.  The kernel's
 // limit of dynamic shared memory is one for all threads of the process: it is set to `most`, the
 // most that any call of the kernel takes, so that no call lowers it under another's launch.
@@ -569,9 +577,11 @@ inline hcmix_status launch(void (*kernel)(const Args), dim3 grid, dim3 threads, 
                            unsigned cluster = 1) {
   if (smem > most) return HCMIX_ERR_UNSUPPORTED;
   // with its static shared memory a kernel may pass the default 48 KB sooner
-  if (smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)most) != cudaSuccess)
-    return HCMIX_ERR_CUDA;
+  if (smem > 32 * 1024) {
+    const hcmix_status st = checked(
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
+    if (st != HCMIX_OK) return st;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = threads;
@@ -586,11 +596,7 @@ inline hcmix_status launch(void (*kernel)(const Args), dim3 grid, dim3 threads, 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args) != cudaSuccess) {
-    cudaGetLastError();
-    return HCMIX_ERR_CUDA;
-  }
-  return HCMIX_OK;
+  return checked(cudaLaunchKernelEx(&cfg, kernel, args));
 }
 
 }  // namespace sublayer
