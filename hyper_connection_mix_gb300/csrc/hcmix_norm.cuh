@@ -490,7 +490,7 @@ __device__ __forceinline__ void store_partial(float* out, const float (&v)[kVec]
   }
 }
 
-constexpr int kColumnThreads = 128;
+constexpr int kColumnThreads = 128, kColumnSlabs = 64;
 
 // Partial sums of the weight's and bias's gradient on their own: block (b, s) takes
 // columns from b * kColumnThreads * kVec and rows s, s + slabs, ...
@@ -719,15 +719,19 @@ inline NormPlan norm_plan(int size, bool own, int64_t M, int64_t N) {
   else if (row <= Back2::kRowBytes) p.shape = 2, p.ring = ring_plan<Back2>(row, groups);
   else if (row <= Back3::kRowBytes) p.shape = 3, p.ring = ring_plan<Back3>(row, M);
   else if (row <= Back4::kRowBytes) p.shape = 4, p.ring = ring_plan<Back4>(row, M);
-  else p.ring.blocks = (int)(M < 64 ? M : 64);
+  else p.ring.blocks = (int)(M < kColumnSlabs ? M : kColumnSlabs);
   return p;
 }
 
-// The workspace is sized before the operands' alignment is known: the larger need.
+// The workspace is sized before the operands' alignment is known, and one for many rows does
+// for fewer: a partial row for each block that the shape can have.
 inline size_t norm_workspace(int size, int64_t M, int64_t N) {
-  const int a = norm_plan(size, true, M, N).ring.blocks;
-  const int b = norm_plan(size, false, M, N).ring.blocks;
-  return ((size_t)(a > b ? a : b) * 2 * (size_t)N * 4 + 255) / 256 * 256;
+  const NormPlan p = norm_plan(size, true, M, N);
+  const int64_t most = p.shape == 0   ? kColumnSlabs
+                       : p.shape <= 2 ? kSms * Back1::kBlocks
+                                      : kSms * Back3::kBlocks;
+  static_assert(Back1::kBlocks == Back2::kBlocks && Back3::kBlocks == Back4::kBlocks, "");
+  return ((size_t)(M < most ? M : most) * 2 * (size_t)N * 4 + 255) / 256 * 256;
 }
 
 template <typename T, int kVec, typename S, int kGroup>

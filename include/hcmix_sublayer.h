@@ -57,7 +57,8 @@ hcmix_status hc_mix_layer_norm(const void* x, int64_t x_stride, hcmix_type type,
  *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy  (fp32 [N]).
  * dweight and dbias are given together, or both NULL: then no workspace is
  * needed.  Else `workspace` holds hc_mix_layer_norm_workspace_bytes(type, M, N)
- * bytes, 256-byte aligned; it needs no initialising. */
+ * bytes, 256-byte aligned; it needs no initialising.  The size never falls as M
+ * grows: a workspace for the largest call does for the others of its N and type. */
 size_t hc_mix_layer_norm_workspace_bytes(hcmix_type type, int64_t M, int64_t N);
 hcmix_status hc_mix_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x,
                                         int64_t x_stride, hcmix_type type, int64_t M, int64_t N,
