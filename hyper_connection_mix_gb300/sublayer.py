@@ -242,6 +242,9 @@ def hc_mix_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Te
             nbytes = L.hc_mix_layer_norm_workspace_bytes(code, M, N)
             workspace = _empty(nbytes, dtype=torch.uint8, device=device)
         else:
+            if (workspace.dtype is not torch.uint8 or workspace.device != device
+                    or not workspace.is_contiguous()):
+                raise ValueError("workspace must be contiguous uint8 on the device of the matrices")
             nbytes = workspace.numel()
     st = L.hc_mix_layer_norm_backward(pd, sd, px, sx, code, M, N, pm, pr, pw, ptype, dx.data_ptr(),
                                       _ptr(dweight), _ptr(dbias),

@@ -181,3 +181,34 @@ def test_a_stream_of_another_device_is_refused(cuda):
     with pytest.raises(ValueError):
         sub.hc_mix_layer_norm(Tensor((M, D), BF16, "cuda:0"), stream=Stream(300, "cuda:1"))
     assert not cuda.called
+
+
+class NonContiguous(Tensor):
+    def is_contiguous(self):
+        return False
+
+
+@pytest.mark.parametrize("workspace", [
+    Tensor(1 << 20, torch.uint8, "cuda:1"),          # another device's memory
+    NonContiguous(1 << 20, torch.uint8, "cuda:0"),   # fewer bytes than elements, or bytes apart
+    Tensor(1 << 20, F32, "cuda:0"),                  # elements that are not bytes
+], ids=["device", "strided", "type"])
+def test_workspaces_that_are_not_bytes_of_the_device_are_refused(cuda, workspace):
+    args, _ = entry_points("cuda:0")["hc_mix_layer_norm_backward"]
+    with pytest.raises(ValueError):
+        sub.hc_mix_layer_norm_backward(*args, workspace=workspace)
+    assert not cuda.called
+
+
+def test_a_host_workspace_is_refused(cuda):
+    args, _ = entry_points("cuda:0")["hc_mix_layer_norm_backward"]
+    workspace = Tensor(1 << 20, torch.uint8, "cpu")
+    with pytest.raises(ValueError):
+        sub.hc_mix_layer_norm_backward(*args, workspace=workspace)
+    assert not cuda.called
+
+
+def test_a_workspace_that_is_given_is_used(cuda):
+    args, _ = entry_points("cuda:0")["hc_mix_layer_norm_backward"]
+    sub.hc_mix_layer_norm_backward(*args, workspace=Tensor(1 << 20, torch.uint8, "cuda:0"))
+    assert len(cuda.called) == 1 and torch.uint8 not in {t.dtype for t in cuda.allocated}
