@@ -27,6 +27,7 @@ import torch
 from . import binding
 from .binding import HC, _check
 
+MOST_EXPERTS = 4096
 TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 # every symbol include/hcmix_sublayer.h declares
@@ -371,7 +372,8 @@ def hc_mix_expert_sort(ids: torch.Tensor, n_experts: int, stream=None):
     device = ids.device
     if stream is not None or device.index != _device():
         return _there(stream, device, hc_mix_expert_sort, ids, n_experts)
-    offsets = _empty(n_experts + 1 if n_experts > 0 else 1, dtype=_I32, device=device)
+    # the library refuses a number of experts outside 1 .. MOST_EXPERTS
+    offsets = _empty(min(max(n_experts, 0), MOST_EXPERTS) + 1, dtype=_I32, device=device)
     slots = _empty(shape, dtype=_I32, device=device)
     source = _empty(T * k, dtype=_I32, device=device)
     st = lib().hc_mix_expert_sort(ids.data_ptr(), 8 if wide else 4, T, k, n_experts,

@@ -212,3 +212,11 @@ def test_a_workspace_that_is_given_is_used(cuda):
     args, _ = entry_points("cuda:0")["hc_mix_layer_norm_backward"]
     sub.hc_mix_layer_norm_backward(*args, workspace=Tensor(1 << 20, torch.uint8, "cuda:0"))
     assert len(cuda.called) == 1 and torch.uint8 not in {t.dtype for t in cuda.allocated}
+
+
+@pytest.mark.parametrize("experts", [1 << 40, 4097, 0, -1, -(1 << 40)])
+def test_a_number_of_experts_that_the_library_refuses_allocates_little(cuda, experts):
+    """The refusal is the library's: it comes before memory for so many offsets is asked for."""
+    sub.hc_mix_expert_sort(Tensor((M, K), I64, "cuda:0"), experts)
+    assert len(cuda.called) == 1
+    assert max(t.numel() for t in cuda.allocated) <= 4097
