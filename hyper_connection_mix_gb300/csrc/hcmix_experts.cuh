@@ -252,12 +252,15 @@ __global__ void __launch_bounds__(256) hcmix_expert_combine_kernel(const RowsArg
   const int step = blockDim.x * kVec;
   const int64_t c = ((int64_t)(blockIdx.x % A.chunks) * kU * blockDim.x + threadIdx.x) * kVec;
   if (c >= A.D) return;
-  const int k = (int)A.k;
+  using Count = uint32_t;  // k can be 2^31 - 1
+  constexpr int64_t kPast = (int64_t)INT32_MAX + kBatch;  // and j passes k by a batch
+  static_assert((int64_t)(Count)kPast == kPast, "");
+  const Count k = (Count)A.k;
   const uint32_t rows = (uint32_t)A.rows;
   const int32_t* slots = A.slots + t * A.k;
   const float* weights = A.weights != nullptr ? A.weights + t * A.k : nullptr;
   float sum[kU * kVec] = {};
-  for (int j = 0; j < k; j += kBatch) {
+  for (Count j = 0; j < k; j += kBatch) {
     Cols<T, kVec, kU> q[kBatch];
     uint32_t s[kBatch];
 #pragma unroll
