@@ -74,7 +74,8 @@ class Sublayer:
                 ) if keep else out
 
     def backward(self, dout, kept):
-        """Gradients of x, up, weight, bias and router for the gradient of forward's result."""
+        """Gradients of x, up, weight, bias and router for the gradient of forward's result, with
+        pre, post and comb held: x's lacks its way through them."""
         x, pre, post, comb, h, mean, rstd, n, ids, chosen, offsets, slots, xs, ys, y = kept
         dx, dy, _, _ = sub.hc_mix_expand_backward(dout, x, y, post, comb)
         dys, dchosen = sub.hc_mix_expert_combine_backward(dy, ys, slots, offsets, chosen)

@@ -16,6 +16,11 @@ takes about 25 us of host time a call (a stream that is current, about 6).
 
 Matrices are 2-D CUDA tensors of one type (bf16, fp16 or fp32) with unit inner
 stride; coefficients, statistics and expert weights are contiguous fp32.
+
+Results carry no autograd graph, whether or not the inputs require gradients:
+each gradient is a call of its own, `hc_mix_..._backward`.  That of the mix
+statistics themselves (of hc_mix_fused) is not in the library, so dpre, dpost and
+dcomb are as far as a gradient goes towards x through them.
 """
 from __future__ import annotations
 
@@ -319,7 +324,8 @@ def hc_mix_collapse_backward(dh: torch.Tensor, x: torch.Tensor, pre: torch.Tenso
 def hc_mix_expand(x: torch.Tensor, y: torch.Tensor, post: torch.Tensor, comb: torch.Tensor,
                   out=None, stream=None) -> torch.Tensor:
     """The next streams [M, 4 * D]: stream i is post[:, i] y + sum_j
-    comb[:, i, j] x_j.  out may be x."""
+    comb[:, i, j] x_j.  out may be x.  A model whose weights mean the sum over
+    comb's first index passes comb.transpose(1, 2).contiguous()."""
     px, sx, code, M, K, dtype, device = _matrix(x, "x")
     if stream is not None or device.index != _device():
         return _there(stream, device, hc_mix_expand, x, y, post, comb, out)

@@ -88,7 +88,12 @@ hcmix_status hc_mix_collapse_backward(const void* dh, int64_t dh_stride, const v
                                       const float* pre, void* dx, float* dpre, void* stream);
 
 /* out_i = post[i] y + sum_j comb[i][j] x_j.  out may be x itself where its rows
- * are contiguous. */
+ * are contiguous.
+ * The sum is over comb's second index: comb[i] holds the weights of the streams in
+ * stream i of the result.  hc_mix_fused says how comb is made (its columns are
+ * divided last), not how a model applies it.  One whose weights mean the sum over
+ * the first index, out_j = post[j] y + sum_i comb[i][j] x_i, passes comb with these
+ * two indices exchanged, here and to the gradient, whose dcomb is exchanged too. */
 hcmix_status hc_mix_expand(const void* x, int64_t x_stride, const void* y, int64_t y_stride,
                            hcmix_type type, int64_t M, int64_t D, int hc, const float* post,
                            const float* comb, void* out, void* stream);
