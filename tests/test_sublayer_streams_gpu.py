@@ -67,3 +67,13 @@ def test_outputs_may_be_let_go_while_the_current_stream_reads_them(side):
     for other in others:  # would be given y's memory, and write it before it is read
         sub.hc_mix_layer_norm(other, stream=side)
     assert torch.equal(got, want)
+
+
+def test_the_default_stream_by_its_handle(side):
+    """Handle 0 is the default stream, also where another one is current."""
+    x = randn(64, 1024, seed=1)
+    want = sub.hc_mix_layer_norm(x)
+    with torch.cuda.stream(side):  # held back: what went there would not be done in time
+        got = sub.hc_mix_layer_norm(x, stream=0)
+    torch.cuda.default_stream().synchronize()
+    assert torch.equal(got, want)
