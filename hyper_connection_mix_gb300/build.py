@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libhcmix.so")
-SOURCES = ["hcmix_abi.cu", "hcmix_sublayer_abi.cu"]
+SOURCES = ["hcmix_abi.cu", "hcmix_sublayer_abi.cu", "hcmix_experts_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
