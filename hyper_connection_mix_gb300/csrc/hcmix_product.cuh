@@ -25,11 +25,20 @@ namespace hcmix {
 namespace sublayer {
 
 constexpr int kProductExperts = 4096;
-constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
+constexpr int kTileM = 128, kTileN = 256, kTileK = 64;  // kTileM: of one block
 constexpr int kBoxBytes = 64 * 128;  // 64 rows of 64 16-bit elements
-constexpr int kABytes = kTileM * kTileK * 2, kBBytes = kTileN * kTileK * 2;
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 4;
+// Blocks of one tile.  Operands that the tensor memory accelerator reads: a pair of blocks
+// with 256 features and half of B each (tcgen05 cta_group::2), so that a multiprocessor's
+// shared memory takes in and gives out two thirds of what a tile of 128 x 256 would need.
+template <bool kTma>
+constexpr int kPair = kTma ? 2 : 1;
+constexpr int kABytes = kTileM * kTileK * 2;
+template <bool kTma>
+constexpr int kStageBytes = kABytes + kTileN * kTileK * 2 / kPair<kTma>;
+template <bool kTma>
+constexpr int kStages = kTma ? 6 : 4;
+constexpr int kRingBytes = kStageBytes<true> * kStages<true>;
+static_assert(kRingBytes == kStageBytes<false> * kStages<false>, "one size of ring");
 constexpr int kPanel = 16;  // row tiles that take their turns at the same weights
 constexpr uint64_t kProductWaitNs = 2000000000ull;
 
@@ -51,6 +60,7 @@ struct ProductArgs {
   void* out;          // product: [R, M]; dweight: [E, N, M]
   void* saved;        // gated: [R, 2 M] or null
   int f16, out_f32;
+  int vec;            // rows of out (and saved) start on 16 bytes
 };
 
 enum class ProductMode { kRowsK, kRowsM, kWeight };  // A's contiguous index: k, m; dweight
@@ -58,16 +68,17 @@ enum class ProductMode { kRowsK, kRowsM, kWeight };  // A's contiguous index: k,
 static __device__ uint32_t g_product_error;
 
 struct ProductControl {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[6], empty[6];
+  uint64_t ready[6];  // dweight by pairs: both blocks' stages, their tails zeroed
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem;
   int abort;
   int scan[32];
 };
-constexpr size_t kExchangeBytes = 4 * 16 * 32 * 4;  // gated: a half chunk of each warp
+constexpr size_t kExchangeBytes = 2 * 4 * 2048;  // a warp's: half a chunk in fp32, a rounded one
 constexpr size_t product_smem(int E) {
-  return 1024 + (size_t)kStages * kStageBytes + kExchangeBytes + sizeof(ProductControl) +
+  return 1024 + (size_t)kRingBytes + kExchangeBytes + sizeof(ProductControl) +
          ((size_t)E + 1) * 4 + 64;
 }
 static_assert(product_smem(kProductExperts) <= 227 * 1024, "shared memory of a block");
@@ -122,18 +133,33 @@ __device__ __forceinline__ void count_tiles(const ProductArgs& A, int* cum, int*
   __syncthreads();
 }
 
-template <ProductMode kMode>
+// The MMA's N: a multiple of 16 for each block.
+template <bool kTma>
+__device__ __forceinline__ int round_rows(int n) {
+  constexpr int to = 16 * kPair<kTma>;
+  return (n + to - 1) / to * to;
+}
+
+// Features of a tile.
+template <bool kTma>
+__host__ __device__ __forceinline__ int tile_width(const ProductArgs& A) {
+  return (A.gated ? kTileM / 2 : kTileM) * kPair<kTma>;
+}
+
+template <bool kTma, ProductMode kMode>
 __device__ __forceinline__ int64_t tile_count(const ProductArgs& A, const int* cum) {
-  const int width = A.gated ? kTileM / 2 : kTileM;
+  const int width = tile_width<kTma>(A);
   const int64_t mt = (A.M + width - 1) / width;
   if (kMode == ProductMode::kWeight) return A.E * mt * ((A.N + kTileN - 1) / kTileN);
   return cum[A.E] * mt;
 }
 
-template <ProductMode kMode>
-__device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* cum, int64_t t) {
+// Tile t, with the features of block `rank` of the pair.
+template <bool kTma, ProductMode kMode>
+__device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* cum, int64_t t,
+                                               int rank) {
   ProductTile T;
-  const int width = A.gated ? kTileM / 2 : kTileM;
+  const int width = tile_width<kTma>(A);
   const int64_t mt = (A.M + width - 1) / width;
   int64_t m;
   if (kMode == ProductMode::kWeight) {
@@ -163,17 +189,16 @@ __device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* 
     int first, count;
     expert_rows(A, lo, first, count);
     // the expert's tiles are of like size, so that none of them is nearly empty
-    const int size = ((count + nt - 1) / nt + 15) / 16 * 16;
+    const int size = round_rows<kTma>((count + nt - 1) / nt);
     T.n0 = first + (int64_t)j * size;
     T.n = count - j * size < size ? count - j * size : size;
     T.k0 = 0, T.depth = A.K;
   }
-  T.m0 = (int)m * width;
+  T.m0 = (int)m * width + rank * (width / kPair<kTma>);
   T.m1 = A.gated ? A.M + T.m0 : T.m0 + kTileM / 2;
   return T;
 }
 
-__device__ __forceinline__ int round16(int n) { return (n + 15) & ~15; }
 
 // ---- plain loads: 64 x `rows` elements into the swizzled box at `dst`, element by
 // element, zeros outside of the matrix.  For matrices whose rows do not all start on
@@ -210,28 +235,200 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr) {
   return d;
 }
 
+template <bool kTma>
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                         bool add) {
+  if constexpr (kTma)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// An arrival at `bar`, in both blocks of a pair, when the MMAs so far are done.
+template <bool kTma>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  if constexpr (kTma)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+
+template <bool kTma>
+__device__ __forceinline__ void product_tmem_alloc(uint32_t dst) {
+  if constexpr (kTma) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(dst)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    sm100::tmem_alloc(dst, 512);
+    sm100::tmem_relinquish();
+  }
+}
+template <bool kTma>
+__device__ __forceinline__ void product_tmem_dealloc(uint32_t tmem) {
+  if constexpr (kTma)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  else
+    sm100::tmem_dealloc(tmem, 512);
+}
+
+// The address, in the pair's shared memory, of what block 0 has at `addr`.
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+// One arrival at a barrier of block 0.
+template <bool kTma>
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
+  if constexpr (kTma)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_leader(bar))
+                 : "memory");
+  else
+    sm100::mbar_arrive(bar);
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Boxes of a pair's block, complete at a barrier of either block.
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const void* map, int c0, int c1,
+                                             uint32_t bar, uint64_t policy) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
       : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const void* map, int c0, int c1, int c2,
+                                             uint32_t bar, uint64_t policy) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
       : "memory");
 }
 
-__device__ __forceinline__ void store_value(void* out, int64_t at, float v, bool f32, bool f16) {
-  if (f32)
-    static_cast<float*>(out)[at] = v;
-  else if (f16)
-    static_cast<__half*>(out)[at] = __float2half_rn(v);
-  else
-    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+// Waits for phase `parity` of a barrier at which threads and copies of both blocks of a
+// pair arrive; false when *abort is set or the time is up.
+__device__ __forceinline__ bool pair_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, const volatile int* abort,
+                                          uint64_t limit_ns) {
+  if (pair_try(bar, parity)) return true;
+  const uint64_t t0 = sm100::global_timer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (pair_try(bar, parity)) return true;
+    if ((i & 3u) == 0) {
+      if (*abort) return false;
+      if (sm100::global_timer_ns() - t0 > limit_ns) return false;
+    }
+  }
+}
+
+// ---- the epilogue's chunks: 32 lanes (features) x 32 columns (rows) of a tile.
+
+// Registers 8 j + i of column octet j: lanes lane / 4 + 8 (i / 2), columns 2 (lane % 4) + i % 2.
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, float (&v)[32]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[4 * h]), "=r"(r[4 * h + 1]), "=r"(r[4 * h + 2]), "=r"(r[4 * h + 3]),
+          "=r"(r[4 * h + 8]), "=r"(r[4 * h + 9]), "=r"(r[4 * h + 10]), "=r"(r[4 * h + 11]),
+          "=r"(r[4 * h + 16]), "=r"(r[4 * h + 17]), "=r"(r[4 * h + 18]), "=r"(r[4 * h + 19]),
+          "=r"(r[4 * h + 24]), "=r"(r[4 * h + 25]), "=r"(r[4 * h + 26]), "=r"(r[4 * h + 27])
+        : "r"(taddr + ((uint32_t)(16 * h) << 16))
+        : "memory");
+  sm100::tmem_wait_ld();
+}
+__device__ __forceinline__ void clear(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+}
+
+__device__ __forceinline__ uint32_t pack_pair(float a, float b, bool f16) {
+  if (f16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Rounds kOctets octets of columns and stores them as `cols` rows of out, `stride` elements
+// apart, from feature m on, as far as M.  `turn` is the warp's 2 KB of shared memory, in which
+// the chunk is turned over: a row's 32 features are four 16-byte blocks, exchanged so that
+// neither the transposing stores nor the loads meet in a bank.
+template <int kOctets = 4>
+__device__ __forceinline__ void store_chunk(const ProductArgs& A, uint32_t turn,
+                                            const float (&v)[8 * kOctets], uint16_t* out,
+                                            int64_t stride, int64_t row, int cols, int m, int M,
+                                            int lane) {
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < kOctets; ++j) {
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = pack_pair(v[8 * j + 2 * i], v[8 * j + 2 * i + 1], A.f16);
+    // lanes 8 b .. 8 b + 7 give the places of block b of rows 8 j .. 8 j + 7
+    const int r = 8 * j + lane % 8, b = lane / 8;
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     turn + r * 64 + ((b ^ (r >> 1 & 3)) << 4)),
+                 "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
+                 : "memory");
+  }
+  __syncwarp();
+  if (A.vec) {
+    const int b = lane % 4;
+    if (m + 8 * b < M) {
+      uint16_t* to = out + row * stride + m + 8 * b;
+#pragma unroll
+      for (int i = 0; i < kOctets; ++i) {
+        const int r = 8 * i + lane / 4;
+        const uint4 w = sm100::lds128(turn + r * 64 + ((b ^ (r >> 1 & 3)) << 4));
+        if (r < cols) *reinterpret_cast<uint4*>(to + r * stride) = w;
+      }
+    }
+  } else if (m + lane < M) {
+    uint16_t* to = out + row * stride + m + lane;
+    const int b = lane / 8;
+    for (int r = 0; r < 8 * kOctets && r < cols; ++r, to += stride) {
+      uint16_t w;
+      asm volatile("ld.shared.u16 %0, [%1];"
+                   : "=h"(w)
+                   : "r"(turn + r * 64 + ((b ^ (r >> 1 & 3)) << 4) + lane % 8 * 2)
+                   : "memory");
+      *to = w;
+    }
+  }
 }
 
 // Barrier `id` over `count` threads of whole warps, and whether all of them say yes.
@@ -259,87 +456,99 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
     hcmix_product_kernel(const __grid_constant__ ProductArgs A) {
   using namespace sm100;
   begin_kernel();
+  constexpr bool kAcross = kMode != ProductMode::kRowsK;   // A lies with m contiguous
+  constexpr bool kWeight = kMode == ProductMode::kWeight;  // and B with n
+  constexpr int kCtas = kPair<kTma>, kDepth = kStages<kTma>;
   extern __shared__ uint8_t product_shared[];
   const uint32_t raw = smem_u32(product_shared);
   const uint32_t stages = (raw + 1023) & ~1023u;
-  uint8_t* after = product_shared + (stages - raw) + kStages * kStageBytes;
+  uint8_t* after = product_shared + (stages - raw) + kRingBytes;
   float* exchange = reinterpret_cast<float*>(after);
   ProductControl& C = *reinterpret_cast<ProductControl*>(after + kExchangeBytes);
   int* cum = reinterpret_cast<int*>(after + kExchangeBytes + sizeof(ProductControl));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  constexpr bool kAcross = kMode != ProductMode::kRowsK;    // A lies with m contiguous
-  constexpr bool kWeight = kMode == ProductMode::kWeight;  // and B with n
+  const int rank = blockIdx.x % kCtas;
+  const int64_t first_tile = blockIdx.x / kCtas, tile_step = gridDim.x / kCtas;
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kDepth; ++s) {
       mbar_init(smem_u32(&C.full[s]), kTma ? 1 : kProducers);
       mbar_init(smem_u32(&C.empty[s]), 1);
+      mbar_init(smem_u32(&C.ready[s]), kCtas);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&C.acc_full[b]), 1);
-      mbar_init(smem_u32(&C.acc_empty[b]), 4);
+      mbar_init(smem_u32(&C.acc_empty[b]), 4 * kCtas);
     }
     mbar_init(smem_u32(&C.drain), 1);
     C.abort = 0;
     fence_mbarrier_init();
   }
-  if (warp == 2) {
-    tmem_alloc(smem_u32(&C.tmem), 512);
-    tmem_relinquish();
-  }
+  // a pair's barriers are there before its other block touches them
+  if (kCtas > 1) pair_sync();
+  if (warp == 2) product_tmem_alloc<kTma>(smem_u32(&C.tmem));
   if (!kWeight) count_tiles(A, cum, C.scan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = C.tmem;
-  const int64_t tiles = tile_count<kMode>(A, cum);
+  const int64_t tiles = tile_count<kTma, kMode>(A, cum);
   const volatile int* abort = &C.abort;
   const auto wait = [&](uint64_t& bar, uint32_t parity) {
-    if (mbar_wait(smem_u32(&bar), parity, abort, kProductWaitNs)) return true;
+    if (pair_wait(smem_u32(&bar), parity, abort, kProductWaitNs)) return true;
     record_device_error(&g_product_error, kDevWaitTimeout);
     *reinterpret_cast<volatile int*>(&C.abort) = 1;
     return false;
+  };
+  const auto finish = [&](uint64_t& bar, uint32_t parity) {  // also after an abort
+    const int none = 0;
+    pair_wait(smem_u32(&bar), parity, &none, kProductWaitNs / 4);
   };
 
   if (kTma ? warp == 0 : warp >= 8) {
     // ---- producer
     uint32_t it = 0;  // stages filled
     bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const ProductTile T = tile_at<kMode>(A, cum, t);
+    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+      const ProductTile T = tile_at<kTma, kMode>(A, cum, t, rank);
       const int blocks = (int)((T.depth + kTileK - 1) / kTileK);
-      const int n16 = round16(T.n);
+      const int n = round_rows<kTma>(T.n) / kCtas;    // this block's share of B
+      const int64_t n0 = T.n0 + rank * n;
       for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
-        const int s = it % kStages;
-        const uint32_t a = stages + s * kStageBytes, b = a + kABytes;
+        const int s = it % kDepth;
+        const uint32_t a = stages + s * kStageBytes<kTma>, b = a + kABytes;
         const int64_t k = T.k0 + (int64_t)kb * kTileK;
-        if (it >= kStages) ok = wait(C.empty[s], (it / kStages - 1) & 1);
+        if (it >= kDepth) ok = wait(C.empty[s], (it / kDepth - 1) & 1);
         if (!ok) break;
         if constexpr (kTma) {
           if (lane == 0) {
-            const uint32_t bar = smem_u32(&C.full[s]);
+            const int boxes = (n + 63) / 64;
+            const uint32_t bytes = kABytes + (kWeight ? boxes * kBoxBytes : n * 128);
             const uint64_t keep = l2_policy_evict_last();
-            const int nb = kWeight ? (n16 + 63) / 64 : 0;
-            const uint32_t bytes = kABytes + (kWeight ? nb * kBoxBytes : n16 * 128);
-            mbar_arrive_expect_tx(bar, bytes);
+            const uint32_t own = smem_u32(&C.full[s]), bar = kWeight ? own : in_leader(own);
+            // products: block 0 waits for both blocks' copies at once
+            if (kWeight)
+              mbar_arrive_expect_tx(own, bytes);
+            else if (rank == 0)
+              mbar_arrive_expect_tx(own, 2 * bytes);
             for (int h = 0; h < 2; ++h) {
               const int m = h ? T.m1 : T.m0;
               if (kWeight)
-                tma_load_2d(a + h * kBoxBytes, &A.a_map, m, (int)k, bar, keep);
+                pair_load_2d(a + h * kBoxBytes, &A.a_map, m, (int)k, bar, keep);
               else if (kAcross)
-                tma_load_3d(a + h * kBoxBytes, &A.a_map, m, (int)k, T.expert, bar, keep);
+                pair_load_3d(a + h * kBoxBytes, &A.a_map, m, (int)k, T.expert, bar, keep);
               else
-                tma_load_3d(a + h * kBoxBytes, &A.a_map, (int)k, m, T.expert, bar, keep);
+                pair_load_3d(a + h * kBoxBytes, &A.a_map, (int)k, m, T.expert, bar, keep);
             }
             if (kWeight) {
-              for (int i = 0; i < nb; ++i)
-                tma_load_2d(b + i * kBoxBytes, &A.b_map, (int)T.n0 + i * 64, (int)k, bar, keep);
+              for (int i = 0; i < boxes; ++i)
+                pair_load_2d(b + i * kBoxBytes, &A.b_map, (int)n0 + i * 64, (int)k, bar, keep);
             } else {
               int r = 0;
-              for (; r + 64 <= n16; r += 64)
-                tma_load_2d(b + r * 128, &A.b_map, (int)k, (int)T.n0 + r, bar, keep);
-              for (; r < n16; r += 16)
-                tma_load_2d(b + r * 128, &A.b16_map, (int)k, (int)T.n0 + r, bar, keep);
+              for (; r + 64 <= n; r += 64)
+                pair_load_2d(b + r * 128, &A.b_map, (int)k, (int)n0 + r, bar, keep);
+              for (; r < n; r += 16)
+                pair_load_2d(b + r * 128, &A.b16_map, (int)k, (int)n0 + r, bar, keep);
             }
           }
           __syncwarp();
@@ -355,10 +564,10 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
               load_box(a + h * kBoxBytes, A.a, T.expert, k, m, A.a.outer, 64, ptid, pthreads);
           }
           if (kWeight) {
-            for (int i = 0; i * 64 < n16; ++i)
-              load_box(b + i * kBoxBytes, A.b, 0, T.n0 + i * 64, k, k_end, 64, ptid, pthreads);
+            for (int i = 0; i * 64 < n; ++i)
+              load_box(b + i * kBoxBytes, A.b, 0, n0 + i * 64, k, k_end, 64, ptid, pthreads);
           } else {
-            load_box(b, A.b, 0, k, T.n0, T.n0 + T.n, n16, ptid, pthreads);
+            load_box(b, A.b, 0, k, n0, T.n0 + T.n, n, ptid, pthreads);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -366,41 +575,27 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
         }
       }
     }
-    if (kTma) {
+    if (kTma && (kWeight || rank == 0)) {
       // copies that nobody waited for (another role gave up) land before the block ends
-      for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
-        const int none = 0;
-        mbar_wait(smem_u32(&C.full[i % kStages]), (i / kStages) & 1, &none, kProductWaitNs / 4);
-      }
+      for (uint32_t i = it > kDepth ? it - kDepth : 0; i < it; ++i)
+        finish(C.full[i % kDepth], (i / kDepth) & 1);
     }
-  } else if (warp == 1) {
-    // ---- MMA
-    uint32_t it = 0, acc = 0;
+  } else if (kTma && kWeight && warp == 3) {
+    // ---- the last stage of an expert took rows of the next one along: they count as zeros
+    uint32_t it = 0;
     bool ok = true;
-    const uint32_t kind = A.f16 ? 0u : (1u << 7) | (1u << 10);
-    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const ProductTile T = tile_at<kMode>(A, cum, t);
+    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+      const ProductTile T = tile_at<kTma, kMode>(A, cum, t, rank);
       const int blocks = (int)((T.depth + kTileK - 1) / kTileK);
-      if (blocks == 0) continue;
-      const int n16 = round16(T.n);
-      const uint32_t idesc = (1u << 4) | kind | (kAcross ? 1u << 15 : 0u) |
-                             (kWeight ? 1u << 16 : 0u) | ((uint32_t)(n16 >> 3) << 17) |
-                             ((uint32_t)(kTileM >> 4) << 24);
-      const int buf = acc & 1;
-      if (acc >= 2) ok = __all_sync(0xffffffffu, wait(C.acc_empty[buf], (acc / 2 - 1) & 1));
-      tc_fence_after();
-      const uint32_t d = tmem + buf * kTileN;
+      const int boxes = 2 + (round_rows<kTma>(T.n) / kCtas + 63) / 64;
       for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
-        const int s = it % kStages;
-        ok = __all_sync(0xffffffffu, wait(C.full[s], (it / kStages) & 1));
+        const int s = it % kDepth;
+        ok = __all_sync(0xffffffffu, wait(C.full[s], (it / kDepth) & 1));
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t a = stages + s * kStageBytes, b = a + kABytes;
         const int left = (int)(T.depth - (int64_t)kb * kTileK);
-        const int steps = left >= kTileK ? kTileK / 16 : (left + 15) / 16;
-        if (kTma && kWeight && left < steps * 16) {
-          // the copy took rows of the next expert along: they count as zeros
-          const int boxes = 2 + (n16 + 63) / 64, gap = steps * 16 - left;
+        if (left < kTileK) {
+          const uint32_t a = stages + s * kStageBytes<kTma>;
+          const int gap = (left + 15) / 16 * 16 - left;  // of the last 16 that the MMA reads
           for (int i = lane; i < boxes * gap * 8; i += 32) {
             const int box = i / (gap * 8), in = i - box * (gap * 8);
             sts128(a + box * kBoxBytes + left * 128 + in * 16, make_uint4(0, 0, 0, 0));
@@ -408,35 +603,63 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
+        if (lane == 0) arrive_leader<kTma>(smem_u32(&C.ready[s]));
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---- MMA
+    uint32_t it = 0, acc = 0;
+    bool ok = true;
+    const uint32_t kind = A.f16 ? 0u : (1u << 7) | (1u << 10);
+    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+      const ProductTile T = tile_at<kTma, kMode>(A, cum, t, rank);
+      const int blocks = (int)((T.depth + kTileK - 1) / kTileK);
+      if (blocks == 0) continue;
+      const uint32_t idesc = (1u << 4) | kind | (kAcross ? 1u << 15 : 0u) |
+                             (kWeight ? 1u << 16 : 0u) |
+                             ((uint32_t)(round_rows<kTma>(T.n) >> 3) << 17) |
+                             ((uint32_t)(kTileM * kCtas >> 4) << 24);
+      const int buf = acc & 1;
+      if (acc >= 2) ok = __all_sync(0xffffffffu, wait(C.acc_empty[buf], (acc / 2 - 1) & 1));
+      tc_fence_after();
+      const uint32_t d = tmem + buf * kTileN;
+      for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
+        const int s = it % kDepth;
+        ok = __all_sync(0xffffffffu,
+                        wait(kTma && kWeight ? C.ready[s] : C.full[s], (it / kDepth) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = stages + s * kStageBytes<kTma>, b = a + kABytes;
+        const int64_t left = T.depth - (int64_t)kb * kTileK;
+        const int steps = left >= kTileK ? kTileK / 16 : (int)(left + 15) / 16;
         if (lane == 0) {
           const uint64_t da = kAcross ? desc_mn_sw128(a) : smem_desc_sw128(a);
           const uint64_t db = kWeight ? desc_mn_sw128(b) : smem_desc_sw128(b);
           // 16 k: 32 bytes of a row, or 16 rows
           for (int i = 0; i < steps; ++i)
-            mma_f16(d, da + i * (kAcross ? 128 : 2), db + i * (kWeight ? 128 : 2), idesc,
-                    kb > 0 || i > 0);
-          mma_commit(smem_u32(&C.empty[s]));
-          if (kb == blocks - 1) mma_commit(smem_u32(&C.acc_full[buf]));
+            mma_f16<kTma>(d, da + i * (kAcross ? 128 : 2), db + i * (kWeight ? 128 : 2), idesc,
+                          kb > 0 || i > 0);
+          mma_commit<kTma>(smem_u32(&C.empty[s]));
+          if (kb == blocks - 1) mma_commit<kTma>(smem_u32(&C.acc_full[buf]));
         }
         __syncwarp();
       }
       ++acc;
     }
-    if (!ok) {
-      const int none = 0;
-      if (lane == 0) mma_commit(smem_u32(&C.drain));
-      __syncwarp();
-      mbar_wait(smem_u32(&C.drain), 0, &none, kProductWaitNs / 4);
-    }
+    // what was issued is done before the block ends
+    if (lane == 0) mma_commit<kTma>(smem_u32(&C.drain));
+    __syncwarp();
+    finish(C.drain, 0);
   } else if (warp >= 4 && warp < 8) {
-    // ---- epilogue: lane 32 * w + lane of the tile
+    // ---- epilogue: TMEM lane 32 * w + lane
     const int w = warp - 4;
     uint32_t acc = 0;
     bool ok = true;
     float* mine = exchange + w * 16 * 32;
+    const uint32_t turn = smem_u32(exchange + (4 + w) * 16 * 32);
     const float* other = exchange + (w ^ 2) * 16 * 32;
-    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const ProductTile T = tile_at<kMode>(A, cum, t);
+    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+      const ProductTile T = tile_at<kTma, kMode>(A, cum, t, rank);
       const int buf = acc & 1;
       const bool any = T.depth > 0;
       if (any) {
@@ -447,52 +670,55 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + buf * kTileN;
-      const int m = T.m0 + w * 32 + lane;
+      const int64_t row = kWeight ? (int64_t)T.expert * A.N + T.n0 : T.n0;
       for (int c = 0; c < T.n; c += 32) {
-        uint32_t v[32];
-        if (any) {
-          tmem_ld32(d + c, v);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0;
-        }
         const int cols = T.n - c < 32 ? T.n - c : 32;
+        float v[32];
+        if (A.out_f32) {
+          if (any) {
+            tmem_ld32(d + c, reinterpret_cast<uint32_t(&)[32]>(v));
+            tmem_wait_ld();
+          } else {
+            clear(v);
+          }
+          const int m = T.m0 + w * 32 + lane;
+          float* out = static_cast<float*>(A.out) + (row + c) * A.M + m;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (i < cols && m < A.M) out[(int64_t)i * A.M] = v[i];
+          continue;
+        }
+        if (any)
+          tmem_ld_fragments(d + c, v);
+        else
+          clear(v);
         if (!A.gated) {
-          if (m < A.M) {
-            int64_t at = kWeight ? ((int64_t)T.expert * A.N + T.n0 + c) * A.M + m
-                                 : (T.n0 + c) * A.M + m;
-#pragma unroll
-            for (int i = 0; i < 32; ++i, at += A.M)
-              if (i < cols) store_value(A.out, at, __uint_as_float(v[i]), A.out_f32, A.f16);
-          }
+          store_chunk(A, turn, v, static_cast<uint16_t*>(A.out), A.M, row + c, cols,
+                      T.m0 + w * 32, A.M, lane);
         } else if constexpr (!kWeight) {
-          const int f = T.m0 + (w & 1) * 32 + lane;
-          if (A.saved != nullptr && f < A.M) {
-            int64_t at = (T.n0 + c) * (2 * (int64_t)A.M) + (w < 2 ? f : A.M + f);
-#pragma unroll
-            for (int i = 0; i < 32; ++i, at += 2 * (int64_t)A.M)
-              if (i < cols) store_value(A.saved, at, __uint_as_float(v[i]), false, A.f16);
-          }
+          const int f = T.m0 + (w & 1) * 32;
+          if (A.saved != nullptr)
+            store_chunk(A, turn, v, static_cast<uint16_t*>(A.saved) + (w < 2 ? 0 : A.M),
+                        2 * (int64_t)A.M, row + c, cols, f, A.M, lane);
           // g's warps give their upper 16 columns to u's, and get the lower ones of u
           named_bar_sync(1 + (w & 1), 64);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = __uint_as_float(w < 2 ? v[16 + i] : v[i]);
+          for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = w < 2 ? v[16 + i] : v[i];
           named_bar_sync(1 + (w & 1), 64);
-          int64_t at = (T.n0 + c + (w < 2 ? 0 : 16)) * A.M + f;
 #pragma unroll
-          for (int i = 0; i < 16; ++i, at += A.M) {
+          for (int i = 0; i < 16; ++i) {
             const float o = other[i * 32 + lane];
-            const float h = w < 2 ? silu(__uint_as_float(v[i])) * o
-                                  : silu(o) * __uint_as_float(v[16 + i]);
-            if (i + (w < 2 ? 0 : 16) < cols && f < A.M) store_value(A.out, at, h, false, A.f16);
+            v[i] = w < 2 ? silu(v[i]) * o : silu(o) * v[16 + i];
           }
+          const int c0 = w < 2 ? 0 : 16;
+          store_chunk<2>(A, turn, reinterpret_cast<float(&)[16]>(v),
+                         static_cast<uint16_t*>(A.out), A.M, row + c + c0, cols - c0, f, A.M, lane);
         }
       }
       if (any) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&C.acc_empty[buf]));
+        if (lane == 0) arrive_leader<kTma>(smem_u32(&C.acc_empty[buf]));
         ++acc;
       }
     }
@@ -500,7 +726,8 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
   // rows that no expert has
   if (!kWeight) {
     const int64_t end = clamp_offset(A.offsets[A.E], A.R);
-    const int64_t from = (int64_t)blockIdx.x * blockDim.x + tid, step = (int64_t)gridDim.x * blockDim.x;
+    const int64_t from = (int64_t)blockIdx.x * blockDim.x + tid,
+                  step = (int64_t)gridDim.x * blockDim.x;
     for (int64_t i = end * A.M + from; i < A.R * A.M; i += step)
       static_cast<uint16_t*>(A.out)[i] = 0;
     if (A.saved != nullptr)
@@ -509,10 +736,10 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 2) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
-  }
+  // no block of a pair ends while the other may still arrive at its barriers
+  if (kCtas > 1) pair_sync();
+  tc_fence_after();
+  if (warp == 2) product_tmem_dealloc<kTma>(tmem);
 }
 
 // ---- host side
@@ -570,28 +797,33 @@ hcmix_status launch_product(const ProductArgs& A, int64_t most_tiles, cudaStream
   int sms = 0;
   const hcmix_status st = device_sms(&sms);
   if (st != HCMIX_OK) return st;
-  const int64_t grid = most_tiles < sms ? (most_tiles > 0 ? most_tiles : 1) : sms;
-  return launch(hcmix_product_kernel<kTma, kMode>, dim3((unsigned)grid),
+  const int64_t most = sms / kPair<kTma>;
+  const int64_t grid = most_tiles < most ? (most_tiles > 0 ? most_tiles : 1) : most;
+  return launch(hcmix_product_kernel<kTma, kMode>, dim3((unsigned)grid * kPair<kTma>),
                 dim3(kProductThreads<kTma>), product_smem(A.E), product_smem(kProductExperts),
-                stream, A);
+                stream, A, kPair<kTma>);
+}
+
+template <bool kTma, ProductMode kMode>
+int64_t most_tiles(const ProductArgs& A) {
+  const int width = tile_width<kTma>(A);
+  const int64_t mt = (A.M + width - 1) / width;
+  return kMode == ProductMode::kWeight ? A.E * mt * ((A.N + kTileN - 1) / kTileN)
+                                       : mt * (A.R / kTileN + (A.R < A.E ? A.R : A.E));
 }
 
 // a, b, offsets, R, E, M, N, K, gated, out, saved and types are set.
 template <ProductMode kMode>
 hcmix_status run_product(ProductArgs& A, cudaStream_t stream) {
-  constexpr bool kWeight = kMode == ProductMode::kWeight;
-  const int width = A.gated ? kTileM / 2 : kTileM;
-  const int64_t mt = (A.M + width - 1) / width;
-  const int64_t tiles = kWeight ? A.E * mt * ((A.N + kTileN - 1) / kTileN)
-                                : mt * (A.R / kTileN + (A.R < A.E ? A.R : A.E));
-  const int a_experts = kWeight ? 0 : A.E;  // 0: a matrix of two dimensions
+  A.vec = vector_bytes(2, {{A.out, A.M}, {A.saved, A.M}}) == 16;
+  const int experts = kMode == ProductMode::kWeight ? 0 : A.E;  // 0: a is a matrix as b is
   // a box starts on 16 bytes: u's features, too, where they lie along the rows
   const bool starts = kMode != ProductMode::kRowsM || !A.gated || A.M % 8 == 0;
-  if (A.R > 0 && starts && tma_readable(A.a, a_experts) && tma_readable(A.b, 0) &&
-      make_box_map(&A.a_map, A.a, a_experts, A.f16, 64) &&
+  if (A.R > 0 && starts && tma_readable(A.a, experts) && tma_readable(A.b, 0) &&
+      make_box_map(&A.a_map, A.a, experts, A.f16, 64) &&
       make_box_map(&A.b_map, A.b, 0, A.f16, 64) && make_box_map(&A.b16_map, A.b, 0, A.f16, 16))
-    return launch_product<true, kMode>(A, tiles, stream);
-  return launch_product<false, kMode>(A, tiles, stream);
+    return launch_product<true, kMode>(A, most_tiles<true, kMode>(A), stream);
+  return launch_product<false, kMode>(A, most_tiles<false, kMode>(A), stream);
 }
 
 }  // namespace sublayer
