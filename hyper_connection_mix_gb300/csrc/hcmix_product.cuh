@@ -69,14 +69,15 @@ static __device__ uint32_t g_product_error;
 
 struct ProductControl {
   uint64_t full[6], empty[6];
-  uint64_t ready[6];  // dweight by pairs: both blocks' stages, their tails zeroed
+  uint64_t tail[6], ready[6];  // dweight by pairs: a block's last stage of a tile, and both's zeroed
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem;
   int abort;
   int scan[32];
 };
-constexpr size_t kExchangeBytes = 2 * 4 * 2048;  // a warp's: half a chunk in fp32, a rounded one
+constexpr int kTurnBytes = 2048;  // a storing warp's: half a chunk in fp32, or a rounded one
+constexpr size_t kExchangeBytes = 8 * kTurnBytes;
 constexpr size_t product_smem(int E) {
   return 1024 + (size_t)kRingBytes + kExchangeBytes + sizeof(ProductControl) +
          ((size_t)E + 1) * 4 + 64;
@@ -447,9 +448,10 @@ __device__ __forceinline__ bool barrier_all(uint32_t id, uint32_t count, bool ye
 
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
-constexpr int kProducers = 8;  // warps, where loads are plain
+constexpr int kStorers = 8;    // warps that store, two for each 32 lanes of TMEM
+constexpr int kProducers = 4;  // warps that load, where loads are plain
 template <bool kTma>
-constexpr int kProductThreads = kTma ? 256 : 256 + kProducers * 32;
+constexpr int kProductThreads = (4 + kStorers + (kTma ? 0 : kProducers)) * 32;
 
 template <bool kTma, ProductMode kMode>
 __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
@@ -474,11 +476,12 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
     for (int s = 0; s < kDepth; ++s) {
       mbar_init(smem_u32(&C.full[s]), kTma ? 1 : kProducers);
       mbar_init(smem_u32(&C.empty[s]), 1);
+      mbar_init(smem_u32(&C.tail[s]), 1);
       mbar_init(smem_u32(&C.ready[s]), kCtas);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&C.acc_full[b]), 1);
-      mbar_init(smem_u32(&C.acc_empty[b]), 4 * kCtas);
+      mbar_init(smem_u32(&C.acc_empty[b]), kStorers * kCtas);
     }
     mbar_init(smem_u32(&C.drain), 1);
     C.abort = 0;
@@ -505,9 +508,10 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
     pair_wait(smem_u32(&bar), parity, &none, kProductWaitNs / 4);
   };
 
-  if (kTma ? warp == 0 : warp >= 8) {
+  if (kTma ? warp == 0 : warp >= 4 + kStorers) {
     // ---- producer
     uint32_t it = 0;  // stages filled
+    uint32_t full_at = 0, tail_at = 0, tails = 0;  // a bit for each stage: phases, and the last use
     bool ok = true;
     for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
       const ProductTile T = tile_at<kTma, kMode>(A, cum, t, rank);
@@ -525,12 +529,17 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
             const int boxes = (n + 63) / 64;
             const uint32_t bytes = kABytes + (kWeight ? boxes * kBoxBytes : n * 128);
             const uint64_t keep = l2_policy_evict_last();
-            const uint32_t own = smem_u32(&C.full[s]), bar = kWeight ? own : in_leader(own);
-            // products: block 0 waits for both blocks' copies at once
-            if (kWeight)
+            // block 0 waits for both blocks' copies at once, but for the last rows of an expert,
+            // behind which each block has to zero its own
+            const bool tail = kWeight && T.depth - (int64_t)kb * kTileK < kTileK;
+            const uint32_t own = smem_u32(tail ? &C.tail[s] : &C.full[s]);
+            const uint32_t bar = tail ? own : in_leader(own);
+            if (tail)
               mbar_arrive_expect_tx(own, bytes);
             else if (rank == 0)
               mbar_arrive_expect_tx(own, 2 * bytes);
+            (tail ? tail_at : full_at) ^= 1u << s;
+            tails = (tails & ~(1u << s)) | (uint32_t)tail << s;
             for (int h = 0; h < 2; ++h) {
               const int m = h ? T.m1 : T.m0;
               if (kWeight)
@@ -553,7 +562,7 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
           }
           __syncwarp();
         } else {
-          const int ptid = tid - 256;
+          const int ptid = tid - (4 + kStorers) * 32;
           constexpr int pthreads = kProducers * 32;
           const int64_t k_end = T.k0 + T.depth;
           for (int h = 0; h < 2; ++h) {
@@ -575,40 +584,43 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
         }
       }
     }
-    if (kTma && (kWeight || rank == 0)) {
+    if (kTma && lane == 0) {
       // copies that nobody waited for (another role gave up) land before the block ends
-      for (uint32_t i = it > kDepth ? it - kDepth : 0; i < it; ++i)
-        finish(C.full[i % kDepth], (i / kDepth) & 1);
+      for (uint32_t i = it > kDepth ? it - kDepth : 0; i < it; ++i) {
+        const int s = i % kDepth;
+        if (tails >> s & 1)
+          finish(C.tail[s], ~(tail_at >> s) & 1);
+        else if (rank == 0)
+          finish(C.full[s], ~(full_at >> s) & 1);
+      }
     }
   } else if (kTma && kWeight && warp == 3) {
     // ---- the last stage of an expert took rows of the next one along: they count as zeros
-    uint32_t it = 0;
+    uint32_t it = 0, tail_at = 0;
     bool ok = true;
     for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
       const ProductTile T = tile_at<kTma, kMode>(A, cum, t, rank);
-      const int blocks = (int)((T.depth + kTileK - 1) / kTileK);
+      it += (uint32_t)(T.depth / kTileK);
+      const int left = (int)(T.depth % kTileK);
+      if (left == 0) continue;
+      const int s = it++ % kDepth;
+      ok = __all_sync(0xffffffffu, wait(C.tail[s], tail_at >> s & 1));
+      tail_at ^= 1u << s;
+      if (!ok) break;
+      const uint32_t a = stages + s * kStageBytes<kTma>;
       const int boxes = 2 + (round_rows<kTma>(T.n) / kCtas + 63) / 64;
-      for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
-        const int s = it % kDepth;
-        ok = __all_sync(0xffffffffu, wait(C.full[s], (it / kDepth) & 1));
-        if (!ok) break;
-        const int left = (int)(T.depth - (int64_t)kb * kTileK);
-        if (left < kTileK) {
-          const uint32_t a = stages + s * kStageBytes<kTma>;
-          const int gap = (left + 15) / 16 * 16 - left;  // of the last 16 that the MMA reads
-          for (int i = lane; i < boxes * gap * 8; i += 32) {
-            const int box = i / (gap * 8), in = i - box * (gap * 8);
-            sts128(a + box * kBoxBytes + left * 128 + in * 16, make_uint4(0, 0, 0, 0));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (lane == 0) arrive_leader<kTma>(smem_u32(&C.ready[s]));
+      const int gap = (left + 15) / 16 * 16 - left;  // of the last 16 that the MMA reads
+      for (int i = lane; i < boxes * gap * 8; i += 32) {
+        const int box = i / (gap * 8), in = i - box * (gap * 8);
+        sts128(a + box * kBoxBytes + left * 128 + in * 16, make_uint4(0, 0, 0, 0));
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_leader<kTma>(smem_u32(&C.ready[s]));
     }
   } else if (warp == 1 && rank == 0) {
     // ---- MMA
-    uint32_t it = 0, acc = 0;
+    uint32_t it = 0, acc = 0, full_at = 0, tail_at = 0;
     bool ok = true;
     const uint32_t kind = A.f16 ? 0u : (1u << 7) | (1u << 10);
     for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
@@ -625,12 +637,14 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
       const uint32_t d = tmem + buf * kTileN;
       for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
         const int s = it % kDepth;
-        ok = __all_sync(0xffffffffu,
-                        wait(kTma && kWeight ? C.ready[s] : C.full[s], (it / kDepth) & 1));
+        const int64_t left = T.depth - (int64_t)kb * kTileK;
+        const bool tail = kTma && kWeight && left < kTileK;
+        ok = __all_sync(0xffffffffu, tail ? wait(C.ready[s], tail_at >> s & 1)
+                                          : wait(C.full[s], full_at >> s & 1));
+        (tail ? tail_at : full_at) ^= 1u << s;
         if (!ok) break;
         tc_fence_after();
         const uint32_t a = stages + s * kStageBytes<kTma>, b = a + kABytes;
-        const int64_t left = T.depth - (int64_t)kb * kTileK;
         const int steps = left >= kTileK ? kTileK / 16 : (int)(left + 15) / 16;
         if (lane == 0) {
           const uint64_t da = kAcross ? desc_mn_sw128(a) : smem_desc_sw128(a);
@@ -650,14 +664,15 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
     if (lane == 0) mma_commit<kTma>(smem_u32(&C.drain));
     __syncwarp();
     finish(C.drain, 0);
-  } else if (warp >= 4 && warp < 8) {
-    // ---- epilogue: TMEM lane 32 * w + lane
-    const int w = warp - 4;
+  } else if (warp >= 4 && warp < 4 + kStorers) {
+    // ---- epilogue: TMEM lanes 32 * w on, every other chunk of 32 columns
+    const int w = warp % 4, half = (warp - 4) / 4;
+    const int bar = 1 + (w & 1) + 2 * half;  // of g's and u's warp
     uint32_t acc = 0;
     bool ok = true;
-    float* mine = exchange + w * 16 * 32;
-    const uint32_t turn = smem_u32(exchange + (4 + w) * 16 * 32);
-    const float* other = exchange + (w ^ 2) * 16 * 32;
+    float* mine = exchange + (warp - 4) * (kTurnBytes / 4);
+    const float* other = exchange + (half * 4 + (w ^ 2)) * (kTurnBytes / 4);
+    const uint32_t turn = smem_u32(mine);
     for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
       const ProductTile T = tile_at<kTma, kMode>(A, cum, t, rank);
       const int buf = acc & 1;
@@ -665,13 +680,13 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
       if (any) {
         // g's and u's warps go on together, or both leave
         ok = wait(C.acc_full[buf], (acc / 2) & 1);
-        ok = A.gated ? barrier_all(1 + (w & 1), 64, ok) : __all_sync(0xffffffffu, ok);
+        ok = A.gated ? barrier_all(bar, 64, ok) : __all_sync(0xffffffffu, ok);
       }
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + buf * kTileN;
       const int64_t row = kWeight ? (int64_t)T.expert * A.N + T.n0 : T.n0;
-      for (int c = 0; c < T.n; c += 32) {
+      for (int c = 32 * half; c < T.n; c += 64) {
         const int cols = T.n - c < 32 ? T.n - c : 32;
         float v[32];
         if (A.out_f32) {
@@ -701,15 +716,16 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
             store_chunk(A, turn, v, static_cast<uint16_t*>(A.saved) + (w < 2 ? 0 : A.M),
                         2 * (int64_t)A.M, row + c, cols, f, A.M, lane);
           // g's warps give their upper 16 columns to u's, and get the lower ones of u
-          named_bar_sync(1 + (w & 1), 64);
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = w < 2 ? v[16 + i] : v[i];
-          named_bar_sync(1 + (w & 1), 64);
+          named_bar_sync(bar, 64);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float o = other[i * 32 + lane];
             v[i] = w < 2 ? silu(v[i]) * o : silu(o) * v[16 + i];
           }
+          named_bar_sync(bar, 64);  // both have read
           const int c0 = w < 2 ? 0 : 16;
           store_chunk<2>(A, turn, reinterpret_cast<float(&)[16]>(v),
                          static_cast<uint16_t*>(A.out), A.M, row + c + c0, cols - c0, f, A.M, lane);
