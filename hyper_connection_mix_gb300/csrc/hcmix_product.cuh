@@ -236,37 +236,80 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr) {
   return d;
 }
 
+// By a whole converged warp, issued by the lane that elect.sync picks (a branch on the lane
+// would keep the descriptors out of uniform registers): MMAs of 16 k, and of the 64 of a stage,
+// whose descriptors step by kA and kB.
 template <bool kTma>
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        bool add) {
+__device__ __forceinline__ void mma_16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool add) {
   if constexpr (kTma)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred e, p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred e, p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
-// An arrival at `bar`, in both blocks of a pair, when the MMAs so far are done.
+template <bool kTma, int kA, int kB>
+__device__ __forceinline__ void mma_64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool add) {
+  if constexpr (kTma)
+    asm volatile(
+        "{\n\t.reg .pred e, p, q;\n\t"
+        ".reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 q, %4, %4;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.u64 a, %1, %5;\n\tadd.u64 b, %2, %6;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.u64 a, %1, %7;\n\tadd.u64 b, %2, %8;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.u64 a, %1, %9;\n\tadd.u64 b, %2, %10;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, q;}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "n"(kA), "n"(kB), "n"(2 * kA),
+        "n"(2 * kB), "n"(3 * kA), "n"(3 * kB)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred e, p, q;\n\t"
+        ".reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 q, %4, %4;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.u64 a, %1, %5;\n\tadd.u64 b, %2, %6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.u64 a, %1, %7;\n\tadd.u64 b, %2, %8;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.u64 a, %1, %9;\n\tadd.u64 b, %2, %10;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "n"(kA), "n"(kB), "n"(2 * kA),
+        "n"(2 * kB), "n"(3 * kA), "n"(3 * kB)
+        : "memory");
+}
+// An arrival at `bar`, in both blocks of a pair, when the elected lane's MMAs so far are done.
 template <bool kTma>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   if constexpr (kTma)
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-        "[%0], %1;" ::"r"(bar),
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+        ".multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
         "h"((uint16_t)3)
         : "memory");
   else
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
+    sm100::umma_commit_warp(bar);
 }
 
 template <bool kTma>
@@ -645,24 +688,23 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t a = stages + s * kStageBytes<kTma>, b = a + kABytes;
-        const int steps = left >= kTileK ? kTileK / 16 : (int)(left + 15) / 16;
-        if (lane == 0) {
-          const uint64_t da = kAcross ? desc_mn_sw128(a) : smem_desc_sw128(a);
-          const uint64_t db = kWeight ? desc_mn_sw128(b) : smem_desc_sw128(b);
-          // 16 k: 32 bytes of a row, or 16 rows
-          for (int i = 0; i < steps; ++i)
-            mma_f16<kTma>(d, da + i * (kAcross ? 128 : 2), db + i * (kWeight ? 128 : 2), idesc,
-                          kb > 0 || i > 0);
-          mma_commit<kTma>(smem_u32(&C.empty[s]));
-          if (kb == blocks - 1) mma_commit<kTma>(smem_u32(&C.acc_full[buf]));
+        const uint64_t da = kAcross ? desc_mn_sw128(a) : smem_desc_sw128(a);
+        const uint64_t db = kWeight ? desc_mn_sw128(b) : smem_desc_sw128(b);
+        // 16 k: 32 bytes of a row, or 16 rows
+        constexpr int kA = kAcross ? 128 : 2, kB = kWeight ? 128 : 2;
+        if (left >= kTileK) {
+          mma_64<kTma, kA, kB>(d, da, db, idesc, kb > 0);
+        } else {
+          for (int i = 0; i * 16 < left; ++i)
+            mma_16<kTma>(d, da + i * kA, db + i * kB, idesc, kb > 0 || i > 0);
         }
-        __syncwarp();
+        mma_commit<kTma>(smem_u32(&C.empty[s]));
+        if (kb == blocks - 1) mma_commit<kTma>(smem_u32(&C.acc_full[buf]));
       }
       ++acc;
     }
     // what was issued is done before the block ends
-    if (lane == 0) mma_commit<kTma>(smem_u32(&C.drain));
-    __syncwarp();
+    mma_commit<kTma>(smem_u32(&C.drain));
     finish(C.drain, 0);
   } else if (warp >= 4 && warp < 4 + kStorers) {
     // ---- epilogue: TMEM lanes 32 * w on, every other chunk of 32 columns
