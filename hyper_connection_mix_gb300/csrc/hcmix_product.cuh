@@ -15,6 +15,10 @@
 // one thread issues the MMAs, and four warps store a tile while the next is computed.
 #pragma once
 
+#ifndef QUAD
+#define QUAD 0
+#endif
+
 #include <cuda.h>
 
 #include "hcmix_common.cuh"
@@ -27,18 +31,19 @@ namespace sublayer {
 constexpr int kProductExperts = 4096;
 constexpr int kTileM = 128, kTileN = 256, kTileK = 64;  // kTileM: of one block
 constexpr int kBoxBytes = 64 * 128;  // 64 rows of 64 16-bit elements
-// Blocks of one tile.  Operands that the tensor memory accelerator reads: a pair of blocks
-// with 256 features and half of B each (tcgen05 cta_group::2), so that a multiprocessor's
-// shared memory takes in and gives out two thirds of what a tile of 128 x 256 would need.
-template <bool kTma>
-constexpr int kPair = kTma ? 2 : 1;
+// kCtas, the blocks that work together:
+//   1  operands whose rows do not all start on 16 bytes, by plain loads;
+//   2  a pair: tcgen05 cta_group::2 with 256 features, and half of B in each block, so that
+//      a multiprocessor's shared memory takes in and gives out two thirds of what a tile of
+//      128 x 256 would need;
+//   4  two pairs with neighbouring features and the same rows, each of which is read once and
+//      sent to both.
 constexpr int kABytes = kTileM * kTileK * 2;
-template <bool kTma>
-constexpr int kStageBytes = kABytes + kTileN * kTileK * 2 / kPair<kTma>;
-template <bool kTma>
-constexpr int kStages = kTma ? 6 : 4;
-constexpr int kRingBytes = kStageBytes<true> * kStages<true>;
-static_assert(kRingBytes == kStageBytes<false> * kStages<false>, "one size of ring");
+__host__ __device__ constexpr int kMmaCtas(int ctas) { return ctas > 1 ? 2 : 1; }
+__host__ __device__ constexpr int kStageBytes(int ctas) { return kABytes + kTileN * kTileK * 2 / kMmaCtas(ctas); }
+__host__ __device__ constexpr int kStages(int ctas) { return ctas > 1 ? 6 : 4; }
+constexpr int kRingBytes = kStageBytes(2) * kStages(2);
+static_assert(kRingBytes == kStageBytes(1) * kStages(1), "one size of ring");
 constexpr int kPanel = 16;  // row tiles that take their turns at the same weights
 constexpr uint64_t kProductWaitNs = 2000000000ull;
 
@@ -67,7 +72,21 @@ enum class ProductMode { kRowsK, kRowsM, kWeight };  // A's contiguous index: k,
 
 static __device__ uint32_t g_product_error;
 
+// A tile, as the scheduling warp tells the others.
+struct alignas(16) ProductTile {
+  int expert;
+  int m0, m1;  // origins of the two halves (64 lanes each) of the block's A
+  int n;       // valid rows of B; 0: no more tiles
+  int n0;      // the first, or the first outer feature
+  int k0;      // dweight: the expert's first row
+  int depth;   // of k
+  int unused;
+};
+
+constexpr int kQueue = 4;  // tiles told ahead
 struct ProductControl {
+  ProductTile tile[kQueue];
+  uint64_t told[kQueue], taken[kQueue];
   uint64_t full[6], empty[6];
   uint64_t tail[6], ready[6];  // dweight by pairs: a block's last stage of a tile, and both's zeroed
   uint64_t acc_full[2], acc_empty[2];
@@ -83,15 +102,6 @@ constexpr size_t product_smem(int E) {
          ((size_t)E + 1) * 4 + 64;
 }
 static_assert(product_smem(kProductExperts) <= 227 * 1024, "shared memory of a block");
-
-struct ProductTile {
-  int expert;
-  int m0, m1;     // origins of the two halves (64 lanes each) of A
-  int64_t n0;     // first row of B, or first outer feature
-  int n;          // valid ones
-  int64_t k0;     // dweight: the expert's first row
-  int64_t depth;  // of k
-};
 
 __device__ __forceinline__ int clamp_offset(int v, int64_t R) {
   return v < 0 ? 0 : v > R ? (int)R : v;
@@ -135,42 +145,42 @@ __device__ __forceinline__ void count_tiles(const ProductArgs& A, int* cum, int*
 }
 
 // The MMA's N: a multiple of 16 for each block.
-template <bool kTma>
+template <int kCtas>
 __device__ __forceinline__ int round_rows(int n) {
-  constexpr int to = 16 * kPair<kTma>;
+  constexpr int to = 16 * kMmaCtas(kCtas);
   return (n + to - 1) / to * to;
 }
 
 // Features of a tile.
-template <bool kTma>
+template <int kCtas>
 __host__ __device__ __forceinline__ int tile_width(const ProductArgs& A) {
-  return (A.gated ? kTileM / 2 : kTileM) * kPair<kTma>;
+  return (A.gated ? kTileM / 2 : kTileM) * kCtas;
 }
 
-template <bool kTma, ProductMode kMode>
+template <int kCtas, ProductMode kMode>
 __device__ __forceinline__ int64_t tile_count(const ProductArgs& A, const int* cum) {
-  const int width = tile_width<kTma>(A);
+  const int width = tile_width<kCtas>(A);
   const int64_t mt = (A.M + width - 1) / width;
   if (kMode == ProductMode::kWeight) return A.E * mt * ((A.N + kTileN - 1) / kTileN);
   return cum[A.E] * mt;
 }
 
-// Tile t, with the features of block `rank` of the pair.
-template <bool kTma, ProductMode kMode>
+// Tile t, with the features of block `rank`.
+template <int kCtas, ProductMode kMode>
 __device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* cum, int64_t t,
                                                int rank) {
-  ProductTile T;
-  const int width = tile_width<kTma>(A);
+  ProductTile T = {};
+  const int width = tile_width<kCtas>(A);
   const int64_t mt = (A.M + width - 1) / width;
   int64_t m;
+  int first, count;
   if (kMode == ProductMode::kWeight) {
     const int64_t nt = (A.N + kTileN - 1) / kTileN;
     T.expert = (int)(t / (mt * nt));
     const int64_t rest = t - T.expert * (mt * nt);
     m = rest / nt;
-    T.n0 = (rest - m * nt) * kTileN;
-    T.n = A.N - T.n0 < kTileN ? (int)(A.N - T.n0) : kTileN;
-    int first, count;
+    T.n0 = (int)(rest - m * nt) * kTileN;
+    T.n = A.N - T.n0 < kTileN ? A.N - T.n0 : kTileN;
     expert_rows(A, T.expert, first, count);
     T.k0 = first, T.depth = count;
   } else {
@@ -180,6 +190,7 @@ __device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* 
       if (cum[mid] * mt <= t) lo = mid; else hi = mid;
     }
     T.expert = lo;
+    expert_rows(A, lo, first, count);
     const int64_t local = t - cum[lo] * mt;
     const int nt = cum[lo + 1] - cum[lo];
     const int panel = (int)(local / (kPanel * mt));
@@ -187,19 +198,16 @@ __device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* 
     const int64_t rest = local - panel * (kPanel * mt);
     m = rest / pn;
     const int j = panel * kPanel + (int)(rest - m * pn);
-    int first, count;
-    expert_rows(A, lo, first, count);
     // the expert's tiles are of like size, so that none of them is nearly empty
-    const int size = round_rows<kTma>((count + nt - 1) / nt);
-    T.n0 = first + (int64_t)j * size;
+    const int size = round_rows<kCtas>((count + nt - 1) / nt);
+    T.n0 = first + j * size;
     T.n = count - j * size < size ? count - j * size : size;
-    T.k0 = 0, T.depth = A.K;
+    T.depth = A.K;
   }
-  T.m0 = (int)m * width + rank * (width / kPair<kTma>);
+  T.m0 = (int)m * width + rank * (width / kCtas);
   T.m1 = A.gated ? A.M + T.m0 : T.m0 + kTileM / 2;
   return T;
 }
-
 
 // ---- plain loads: 64 x `rows` elements into the swizzled box at `dst`, element by
 // element, zeros outside of the matrix.  For matrices whose rows do not all start on
@@ -297,16 +305,16 @@ __device__ __forceinline__ void mma_64(uint32_t d, uint64_t a, uint64_t b, uint3
         "n"(2 * kB), "n"(3 * kA), "n"(3 * kB)
         : "memory");
 }
-// An arrival at `bar`, in both blocks of a pair, when the elected lane's MMAs so far are done.
+// An arrival at `bar`, in the blocks of `mask`, when the elected lane's MMAs so far are done.
 template <bool kTma>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t mask) {
   if constexpr (kTma)
     asm volatile(
         "{\n\t.reg .pred e;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
         ".multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"((uint16_t)mask)
         : "memory");
   else
     sm100::umma_commit_warp(bar);
@@ -331,13 +339,19 @@ __device__ __forceinline__ void product_tmem_dealloc(uint32_t tmem) {
     sm100::tmem_dealloc(tmem, 512);
 }
 
-// The address, in the pair's shared memory, of what block 0 has at `addr`.
+// The address, in the cluster's shared memory, of what the first block of this block's pair
+// has at `addr`.
 __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
   uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  asm("{\n\t.reg .u32 c;\n\t"
+      "mov.u32 c, %%cluster_ctarank;\n\t"
+      "and.b32 c, c, 0xfffffffe;\n\t"
+      "mapa.shared::cluster.u32 %0, %1, c;\n\t}"
+      : "=r"(r)
+      : "r"(addr));
   return r;
 }
-// One arrival at a barrier of block 0.
+// One arrival at a barrier of that block.
 template <bool kTma>
 __device__ __forceinline__ void arrive_leader(uint32_t bar) {
   if constexpr (kTma)
@@ -346,7 +360,7 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar) {
   else
     sm100::mbar_arrive(bar);
 }
-__device__ __forceinline__ void pair_sync() {
+__device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -366,6 +380,18 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const void* map, int 
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+// A box for the same place in all blocks of `mask`, complete at the same barrier of each (of
+// each one's pair, where `bar` is the leader's).
+__device__ __forceinline__ void pair_send_2d(uint32_t dst, const void* map, int c0, int c1,
+                                             uint32_t bar, uint32_t mask, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".multicast::cluster.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "h"((uint16_t)mask),
+      "l"(policy)
       : "memory");
 }
 
@@ -493,17 +519,21 @@ __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __e
 
 constexpr int kStorers = 8;    // warps that store, two for each 32 lanes of TMEM
 constexpr int kProducers = 4;  // warps that load, where loads are plain
-template <bool kTma>
-constexpr int kProductThreads = (4 + kStorers + (kTma ? 0 : kProducers)) * 32;
+constexpr int kProductThreads(int ctas) {
+  return (4 + kStorers + (ctas > 1 ? 0 : kProducers)) * 32;
+}
 
-template <bool kTma, ProductMode kMode>
-__global__ void __launch_bounds__(kProductThreads<kTma>, 1)
+// Warps: 0 copies, 1 MMAs, 2 tells the tiles, 3 zeroes behind an expert's last rows (dweight),
+// 4 .. 11 store; 12 .. 15 load where loads are plain.
+template <int kCtas, ProductMode kMode>
+__global__ void __launch_bounds__(kProductThreads(kCtas), 1)
     hcmix_product_kernel(const __grid_constant__ ProductArgs A) {
   using namespace sm100;
   begin_kernel();
+  constexpr bool kTma = kCtas > 1;
   constexpr bool kAcross = kMode != ProductMode::kRowsK;   // A lies with m contiguous
   constexpr bool kWeight = kMode == ProductMode::kWeight;  // and B with n
-  constexpr int kCtas = kPair<kTma>, kDepth = kStages<kTma>;
+  constexpr int kMma = kMmaCtas(kCtas), kDepth = kStages(kCtas);
   extern __shared__ uint8_t product_shared[];
   const uint32_t raw = smem_u32(product_shared);
   const uint32_t stages = (raw + 1023) & ~1023u;
@@ -512,33 +542,37 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
   ProductControl& C = *reinterpret_cast<ProductControl*>(after + kExchangeBytes);
   int* cum = reinterpret_cast<int*>(after + kExchangeBytes + sizeof(ProductControl));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int rank = blockIdx.x % kCtas;
-  const int64_t first_tile = blockIdx.x / kCtas, tile_step = gridDim.x / kCtas;
+  const int rank = blockIdx.x % kCtas, half_rank = rank % kMma;
+  const bool leader = half_rank == 0;  // of a pair
 
   if (tid == 0) {
+    const int takers = kStorers + (kTma ? 1 : kProducers) + leader + (kTma && kWeight);
+    for (int q = 0; q < kQueue; ++q) {
+      mbar_init(smem_u32(&C.told[q]), 1);
+      mbar_init(smem_u32(&C.taken[q]), takers);
+    }
     for (int s = 0; s < kDepth; ++s) {
       mbar_init(smem_u32(&C.full[s]), kTma ? 1 : kProducers);
-      mbar_init(smem_u32(&C.empty[s]), 1);
+      mbar_init(smem_u32(&C.empty[s]), kCtas / kMma);
       mbar_init(smem_u32(&C.tail[s]), 1);
-      mbar_init(smem_u32(&C.ready[s]), kCtas);
+      mbar_init(smem_u32(&C.ready[s]), kMma);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&C.acc_full[b]), 1);
-      mbar_init(smem_u32(&C.acc_empty[b]), kStorers * kCtas);
+      mbar_init(smem_u32(&C.acc_empty[b]), kStorers * kMma);
     }
     mbar_init(smem_u32(&C.drain), 1);
     C.abort = 0;
     fence_mbarrier_init();
   }
-  // a pair's barriers are there before its other block touches them
-  if (kCtas > 1) pair_sync();
+  // the cluster's barriers are there before its other blocks touch them
+  if (kTma) cluster_sync();
   if (warp == 2) product_tmem_alloc<kTma>(smem_u32(&C.tmem));
   if (!kWeight) count_tiles(A, cum, C.scan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = C.tmem;
-  const int64_t tiles = tile_count<kTma, kMode>(A, cum);
   const volatile int* abort = &C.abort;
   const auto wait = [&](uint64_t& bar, uint32_t parity) {
     if (pair_wait(smem_u32(&bar), parity, abort, kProductWaitNs)) return true;
@@ -550,21 +584,32 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
     const int none = 0;
     pair_wait(smem_u32(&bar), parity, &none, kProductWaitNs / 4);
   };
+  // The next tile, by a whole warp; false behind the last, and after an abort.
+  uint32_t turns = 0;
+  const auto next = [&](ProductTile& T) {
+    const int q = turns % kQueue;
+    if (!__all_sync(0xffffffffu, wait(C.told[q], (turns / kQueue) & 1))) return false;
+    T = C.tile[q];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&C.taken[q]));
+    ++turns;
+    return T.n > 0;
+  };
+  ProductTile T;
 
   if (kTma ? warp == 0 : warp >= 4 + kStorers) {
     // ---- producer
     uint32_t it = 0;  // stages filled
     uint32_t full_at = 0, tail_at = 0, tails = 0;  // a bit for each stage: phases, and the last use
     bool ok = true;
-    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-      const ProductTile T = tile_at<kTma, kMode>(A, cum, t, rank);
-      const int blocks = (int)((T.depth + kTileK - 1) / kTileK);
-      const int n = round_rows<kTma>(T.n) / kCtas;    // this block's share of B
-      const int64_t n0 = T.n0 + rank * n;
+    while (ok && next(T)) {
+      const int blocks = (T.depth + kTileK - 1) / kTileK;
+      const int n = round_rows<kCtas>(T.n) / kMma;  // this block's share of B
+      const int n0 = T.n0 + half_rank * n;
       for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
         const int s = it % kDepth;
-        const uint32_t a = stages + s * kStageBytes<kTma>, b = a + kABytes;
-        const int64_t k = T.k0 + (int64_t)kb * kTileK;
+        const uint32_t a = stages + s * kStageBytes(kCtas), b = a + kABytes;
+        const int k = T.k0 + kb * kTileK;
         if (it >= kDepth) ok = wait(C.empty[s], (it / kDepth - 1) & 1);
         if (!ok) break;
         if constexpr (kTma) {
@@ -574,40 +619,58 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
             const uint64_t keep = l2_policy_evict_last();
             // block 0 waits for both blocks' copies at once, but for the last rows of an expert,
             // behind which each block has to zero its own
-            const bool tail = kWeight && T.depth - (int64_t)kb * kTileK < kTileK;
+            const bool tail = kWeight && T.depth - kb * kTileK < kTileK;
             const uint32_t own = smem_u32(tail ? &C.tail[s] : &C.full[s]);
             const uint32_t bar = tail ? own : in_leader(own);
             if (tail)
               mbar_arrive_expect_tx(own, bytes);
-            else if (rank == 0)
+            else if (leader)
               mbar_arrive_expect_tx(own, 2 * bytes);
             (tail ? tail_at : full_at) ^= 1u << s;
             tails = (tails & ~(1u << s)) | (uint32_t)tail << s;
             for (int h = 0; h < 2; ++h) {
               const int m = h ? T.m1 : T.m0;
               if (kWeight)
-                pair_load_2d(a + h * kBoxBytes, &A.a_map, m, (int)k, bar, keep);
+                pair_load_2d(a + h * kBoxBytes, &A.a_map, m, k, bar, keep);
               else if (kAcross)
-                pair_load_3d(a + h * kBoxBytes, &A.a_map, m, (int)k, T.expert, bar, keep);
+                pair_load_3d(a + h * kBoxBytes, &A.a_map, m, k, T.expert, bar, keep);
               else
-                pair_load_3d(a + h * kBoxBytes, &A.a_map, (int)k, m, T.expert, bar, keep);
+                pair_load_3d(a + h * kBoxBytes, &A.a_map, k, m, T.expert, bar, keep);
             }
-            if (kWeight) {
-              for (int i = 0; i < boxes; ++i)
-                pair_load_2d(b + i * kBoxBytes, &A.b_map, (int)n0 + i * 64, (int)k, bar, keep);
+            if constexpr (kCtas == 2) {
+              if (kWeight) {
+                for (int i = 0; i < boxes; ++i)
+                  pair_load_2d(b + i * kBoxBytes, &A.b_map, n0 + i * 64, k, bar, keep);
+              } else {
+                int r = 0;
+                for (; r + 64 <= n; r += 64)
+                  pair_load_2d(b + r * 128, &A.b_map, k, n0 + r, bar, keep);
+                for (; r < n; r += 16)
+                  pair_load_2d(b + r * 128, &A.b16_map, k, n0 + r, bar, keep);
+              }
             } else {
-              int r = 0;
-              for (; r + 64 <= n; r += 64)
-                pair_load_2d(b + r * 128, &A.b_map, (int)k, (int)n0 + r, bar, keep);
-              for (; r < n; r += 16)
-                pair_load_2d(b + r * 128, &A.b16_map, (int)k, (int)n0 + r, bar, keep);
+              // the block of the other pair that needs the same share sends the rest of it
+              const uint32_t mask = 5u << half_rank;
+              const int second = rank / 2;
+              if (kWeight) {
+                const int most = (boxes + 1) / 2;
+                for (int i = second ? most : 0; i < (second ? boxes : most); ++i)
+                  pair_send_2d(b + i * kBoxBytes, &A.b_map, n0 + i * 64, k, bar, mask, keep);
+              } else {
+                const int most = (n / 16 + 1) / 2 * 16, end = second ? n : most;
+                int r = second ? most : 0;
+                for (; r + 64 <= end; r += 64)
+                  pair_send_2d(b + r * 128, &A.b_map, k, n0 + r, bar, mask, keep);
+                for (; r < end; r += 16)
+                  pair_send_2d(b + r * 128, &A.b16_map, k, n0 + r, bar, mask, keep);
+              }
             }
           }
           __syncwarp();
         } else {
           const int ptid = tid - (4 + kStorers) * 32;
           constexpr int pthreads = kProducers * 32;
-          const int64_t k_end = T.k0 + T.depth;
+          const int k_end = T.k0 + T.depth;
           for (int h = 0; h < 2; ++h) {
             const int m = h ? T.m1 : T.m0;
             if (kAcross)
@@ -633,7 +696,7 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
         const int s = i % kDepth;
         if (tails >> s & 1)
           finish(C.tail[s], ~(tail_at >> s) & 1);
-        else if (rank == 0)
+        else if (leader)
           finish(C.full[s], ~(full_at >> s) & 1);
       }
     }
@@ -641,17 +704,16 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
     // ---- the last stage of an expert took rows of the next one along: they count as zeros
     uint32_t it = 0, tail_at = 0;
     bool ok = true;
-    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-      const ProductTile T = tile_at<kTma, kMode>(A, cum, t, rank);
-      it += (uint32_t)(T.depth / kTileK);
-      const int left = (int)(T.depth % kTileK);
+    while (ok && next(T)) {
+      it += T.depth / kTileK;
+      const int left = T.depth % kTileK;
       if (left == 0) continue;
       const int s = it++ % kDepth;
       ok = __all_sync(0xffffffffu, wait(C.tail[s], tail_at >> s & 1));
       tail_at ^= 1u << s;
       if (!ok) break;
-      const uint32_t a = stages + s * kStageBytes<kTma>;
-      const int boxes = 2 + (round_rows<kTma>(T.n) / kCtas + 63) / 64;
+      const uint32_t a = stages + s * kStageBytes(kCtas);
+      const int boxes = 2 + (round_rows<kCtas>(T.n) / kMma + 63) / 64;
       const int gap = (left + 15) / 16 * 16 - left;  // of the last 16 that the MMA reads
       for (int i = lane; i < boxes * gap * 8; i += 32) {
         const int box = i / (gap * 8), in = i - box * (gap * 8);
@@ -661,33 +723,33 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
       __syncwarp();
       if (lane == 0) arrive_leader<kTma>(smem_u32(&C.ready[s]));
     }
-  } else if (warp == 1 && rank == 0) {
+  } else if (warp == 1 && leader) {
     // ---- MMA
     uint32_t it = 0, acc = 0, full_at = 0, tail_at = 0;
+    const uint32_t pair = 3u << (rank & ~1);
     bool ok = true;
     const uint32_t kind = A.f16 ? 0u : (1u << 7) | (1u << 10);
-    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-      const ProductTile T = tile_at<kTma, kMode>(A, cum, t, rank);
-      const int blocks = (int)((T.depth + kTileK - 1) / kTileK);
+    while (ok && next(T)) {
+      const int blocks = (T.depth + kTileK - 1) / kTileK;
       if (blocks == 0) continue;
       const uint32_t idesc = (1u << 4) | kind | (kAcross ? 1u << 15 : 0u) |
                              (kWeight ? 1u << 16 : 0u) |
-                             ((uint32_t)(round_rows<kTma>(T.n) >> 3) << 17) |
-                             ((uint32_t)(kTileM * kCtas >> 4) << 24);
+                             ((uint32_t)(round_rows<kCtas>(T.n) >> 3) << 17) |
+                             ((uint32_t)(kTileM * kMma >> 4) << 24);
       const int buf = acc & 1;
       if (acc >= 2) ok = __all_sync(0xffffffffu, wait(C.acc_empty[buf], (acc / 2 - 1) & 1));
       tc_fence_after();
       const uint32_t d = tmem + buf * kTileN;
       for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
         const int s = it % kDepth;
-        const int64_t left = T.depth - (int64_t)kb * kTileK;
+        const int left = T.depth - kb * kTileK;
         const bool tail = kTma && kWeight && left < kTileK;
         ok = __all_sync(0xffffffffu, tail ? wait(C.ready[s], tail_at >> s & 1)
                                           : wait(C.full[s], full_at >> s & 1));
         (tail ? tail_at : full_at) ^= 1u << s;
         if (!ok) break;
         tc_fence_after();
-        const uint32_t a = stages + s * kStageBytes<kTma>, b = a + kABytes;
+        const uint32_t a = stages + s * kStageBytes(kCtas), b = a + kABytes;
         const uint64_t da = kAcross ? desc_mn_sw128(a) : smem_desc_sw128(a);
         const uint64_t db = kWeight ? desc_mn_sw128(b) : smem_desc_sw128(b);
         // 16 k: 32 bytes of a row, or 16 rows
@@ -698,13 +760,13 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
           for (int i = 0; i * 16 < left; ++i)
             mma_16<kTma>(d, da + i * kA, db + i * kB, idesc, kb > 0 || i > 0);
         }
-        mma_commit<kTma>(smem_u32(&C.empty[s]));
-        if (kb == blocks - 1) mma_commit<kTma>(smem_u32(&C.acc_full[buf]));
+        mma_commit<kTma>(smem_u32(&C.empty[s]), (1u << kCtas) - 1);
+        if (kb == blocks - 1) mma_commit<kTma>(smem_u32(&C.acc_full[buf]), pair);
       }
       ++acc;
     }
     // what was issued is done before the block ends
-    mma_commit<kTma>(smem_u32(&C.drain));
+    mma_commit<kTma>(smem_u32(&C.drain), pair);
     finish(C.drain, 0);
   } else if (warp >= 4 && warp < 4 + kStorers) {
     // ---- epilogue: TMEM lanes 32 * w on, every other chunk of 32 columns
@@ -715,12 +777,14 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
     float* mine = exchange + (warp - 4) * (kTurnBytes / 4);
     const float* other = exchange + (half * 4 + (w ^ 2)) * (kTurnBytes / 4);
     const uint32_t turn = smem_u32(mine);
-    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
-      const ProductTile T = tile_at<kTma, kMode>(A, cum, t, rank);
+    for (;;) {
+      // g's and u's warps go on together, or both leave
+      bool have = next(T);
+      if (A.gated) have = barrier_all(bar, 64, have);
+      if (!have) break;
       const int buf = acc & 1;
       const bool any = T.depth > 0;
       if (any) {
-        // g's and u's warps go on together, or both leave
         ok = wait(C.acc_full[buf], (acc / 2) & 1);
         ok = A.gated ? barrier_all(bar, 64, ok) : __all_sync(0xffffffffu, ok);
       }
@@ -780,6 +844,24 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
         ++acc;
       }
     }
+  } else if (warp == 2) {
+    // ---- the tiles, in turn over the clusters
+    const int64_t tiles = tile_count<kCtas, kMode>(A, cum);
+    bool ok = true;
+    for (int64_t t = blockIdx.x / kCtas; ok; t += gridDim.x / kCtas, ++turns) {
+      const int q = turns % kQueue;
+      const bool more = t < tiles;
+      if (more) T = tile_at<kCtas, kMode>(A, cum, t, rank);
+      if (turns >= kQueue) ok = __all_sync(0xffffffffu, wait(C.taken[q], (turns / kQueue - 1) & 1));
+      if (!ok) break;
+      if (lane == 0) {
+        if (!more) T.n = 0;
+        C.tile[q] = T;
+        mbar_arrive(smem_u32(&C.told[q]));
+      }
+      __syncwarp();
+      if (!more) break;
+    }
   }
   // rows that no expert has
   if (!kWeight) {
@@ -794,8 +876,8 @@ __global__ void __launch_bounds__(kProductThreads<kTma>, 1)
   }
   tc_fence_before();
   __syncthreads();
-  // no block of a pair ends while the other may still arrive at its barriers
-  if (kCtas > 1) pair_sync();
+  // no block ends while others may still arrive at its barriers or send to it
+  if (kTma) cluster_sync();
   tc_fence_after();
   if (warp == 2) product_tmem_dealloc<kTma>(tmem);
 }
@@ -850,24 +932,20 @@ inline hcmix_status device_sms(int* sms) {
   return checked(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
 }
 
-template <bool kTma, ProductMode kMode>
-hcmix_status launch_product(const ProductArgs& A, int64_t most_tiles, cudaStream_t stream) {
+template <int kCtas, ProductMode kMode>
+hcmix_status launch_product(const ProductArgs& A, cudaStream_t stream) {
   int sms = 0;
   const hcmix_status st = device_sms(&sms);
   if (st != HCMIX_OK) return st;
-  const int64_t most = sms / kPair<kTma>;
-  const int64_t grid = most_tiles < most ? (most_tiles > 0 ? most_tiles : 1) : most;
-  return launch(hcmix_product_kernel<kTma, kMode>, dim3((unsigned)grid * kPair<kTma>),
-                dim3(kProductThreads<kTma>), product_smem(A.E), product_smem(kProductExperts),
-                stream, A, kPair<kTma>);
-}
-
-template <bool kTma, ProductMode kMode>
-int64_t most_tiles(const ProductArgs& A) {
-  const int width = tile_width<kTma>(A);
-  const int64_t mt = (A.M + width - 1) / width;
-  return kMode == ProductMode::kWeight ? A.E * mt * ((A.N + kTileN - 1) / kTileN)
-                                       : mt * (A.R / kTileN + (A.R < A.E ? A.R : A.E));
+  const int width = tile_width<kCtas>(A);
+  const int64_t mt = (A.M + width - 1) / width, most = sms / kCtas;
+  const int64_t tiles = kMode == ProductMode::kWeight
+                            ? A.E * mt * ((A.N + kTileN - 1) / kTileN)
+                            : mt * (A.R / kTileN + (A.R < A.E ? A.R : A.E));
+  const int64_t grid = tiles < most ? (tiles > 0 ? tiles : 1) : most;
+  return launch(hcmix_product_kernel<kCtas, kMode>, dim3((unsigned)grid * kCtas),
+                dim3(kProductThreads(kCtas)), product_smem(A.E), product_smem(kProductExperts),
+                stream, A, kCtas);
 }
 
 // a, b, offsets, R, E, M, N, K, gated, out, saved and types are set.
@@ -880,8 +958,8 @@ hcmix_status run_product(ProductArgs& A, cudaStream_t stream) {
   if (A.R > 0 && starts && tma_readable(A.a, experts) && tma_readable(A.b, 0) &&
       make_box_map(&A.a_map, A.a, experts, A.f16, 64) &&
       make_box_map(&A.b_map, A.b, 0, A.f16, 64) && make_box_map(&A.b16_map, A.b, 0, A.f16, 16))
-    return launch_product<true, kMode>(A, most_tiles<true, kMode>(A), stream);
-  return launch_product<false, kMode>(A, most_tiles<false, kMode>(A), stream);
+    return launch_product<QUAD ? 4 : 2, kMode>(A, stream);
+  return launch_product<1, kMode>(A, stream);
 }
 
 }  // namespace sublayer
