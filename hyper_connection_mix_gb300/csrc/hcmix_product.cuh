@@ -21,6 +21,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "hcmix_common.cuh"
 #include "hcmix_sm100.cuh"
 #include "hcmix_vec.cuh"
@@ -925,20 +927,51 @@ inline bool make_box_map(CUtensorMap* map, const Matrix3& X, int experts, bool f
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-inline hcmix_status device_sms(int* sms) {
-  int dev = 0;
-  const hcmix_status st = checked(cudaGetDevice(&dev));
+// The clusters that the current device runs at a time (of four blocks fewer than a quarter of
+// its multiprocessors: 36 on 152).  Asked for once a device.
+template <int kCtas, ProductMode kMode>
+hcmix_status resident_clusters(int* clusters) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0, n = 0;
+  hcmix_status st = checked(cudaGetDevice(&dev));
   if (st != HCMIX_OK) return st;
-  return checked(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+  const bool keep = dev >= 0 && dev < kDevices;
+  if (keep && (n = known[dev].load(std::memory_order_relaxed)) > 0) {
+    *clusters = n;
+    return HCMIX_OK;
+  }
+  auto kernel = hcmix_product_kernel<kCtas, kMode>;
+  const size_t smem = product_smem(kProductExperts);
+  st = checked(
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  if (st != HCMIX_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCtas);
+  cfg.blockDim = dim3(kProductThreads(kCtas));
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  st = checked(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg));
+  if (st != HCMIX_OK) return st;
+  if (n < 1) return HCMIX_ERR_CUDA;
+  if (keep) known[dev].store(n, std::memory_order_relaxed);
+  *clusters = n;
+  return HCMIX_OK;
 }
 
 template <int kCtas, ProductMode kMode>
 hcmix_status launch_product(const ProductArgs& A, cudaStream_t stream) {
-  int sms = 0;
-  const hcmix_status st = device_sms(&sms);
+  int most = 0;
+  const hcmix_status st = resident_clusters<kCtas, kMode>(&most);
   if (st != HCMIX_OK) return st;
   const int width = tile_width<kCtas>(A);
-  const int64_t mt = (A.M + width - 1) / width, most = sms / kCtas;
+  const int64_t mt = (A.M + width - 1) / width;
   const int64_t tiles = kMode == ProductMode::kWeight
                             ? A.E * mt * ((A.N + kTileN - 1) / kTileN)
                             : mt * (A.R / kTileN + (A.R < A.E ? A.R : A.E));
