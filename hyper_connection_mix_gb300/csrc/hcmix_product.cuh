@@ -33,6 +33,8 @@ namespace sublayer {
 constexpr int kProductExperts = 4096;
 constexpr int kTileM = 128, kTileN = 256, kTileK = 64;  // kTileM: of one block
 constexpr int kBoxBytes = 64 * 128;  // 64 rows of 64 16-bit elements
+enum class ProductMode { kRowsK, kRowsM, kWeight };  // A's contiguous index: k, m; dweight
+
 // kCtas, the blocks that work together:
 //   1  operands whose rows do not all start on 16 bytes, by plain loads;
 //   2  a pair: tcgen05 cta_group::2 with 256 features, and half of B in each block, so that
@@ -70,7 +72,6 @@ struct ProductArgs {
   int vec;            // rows of out (and saved) start on 16 bytes
 };
 
-enum class ProductMode { kRowsK, kRowsM, kWeight };  // A's contiguous index: k, m; dweight
 
 static __device__ uint32_t g_product_error;
 
@@ -97,13 +98,22 @@ struct ProductControl {
   int abort;
   int scan[32];
 };
-constexpr int kTurnBytes = 2048;  // a storing warp's: half a chunk in fp32, or a rounded one
-constexpr size_t kExchangeBytes = 8 * kTurnBytes;
-constexpr size_t product_smem(int E) {
-  return 1024 + (size_t)kRingBytes + kExchangeBytes + sizeof(ProductControl) +
-         ((size_t)E + 1) * 4 + 64;
+// Warps that store.  A chunk of 32 x 32 takes a warp about 0.5 us, most of it latency: eight
+// warps keep up with a tile's MMAs where k is long, and sixteen with the stores of dweight,
+// whose k may be an expert's few rows.
+__host__ __device__ constexpr int kStorers(int ctas, ProductMode mode) {
+  return ctas > 1 && mode == ProductMode::kWeight ? 16 : 8;
 }
-static_assert(product_smem(kProductExperts) <= 227 * 1024, "shared memory of a block");
+constexpr int kTurnBytes = 2048;  // a storing warp's: half a chunk in fp32, or a rounded one
+// Shared memory of a block; dweight needs no table of the experts' tiles.
+template <int kCtas, ProductMode kMode>
+constexpr size_t product_smem(int E) {
+  return 1024 + (size_t)kRingBytes + kStorers(kCtas, kMode) * kTurnBytes + sizeof(ProductControl) +
+         (kMode == ProductMode::kWeight ? 0 : ((size_t)E + 1) * 4);
+}
+static_assert(product_smem<2, ProductMode::kRowsK>(kProductExperts) <= 227 * 1024 &&
+                  product_smem<2, ProductMode::kWeight>(kProductExperts) <= 227 * 1024,
+              "shared memory of a block");
 
 __device__ __forceinline__ int clamp_offset(int v, int64_t R) {
   return v < 0 ? 0 : v > R ? (int)R : v;
@@ -362,6 +372,17 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar) {
   else
     sm100::mbar_arrive(bar);
 }
+// The same from a thread that has read what it was to read (tcgen05.wait::ld) and has written
+// nothing that the barrier is to publish.  A release would wait for its earlier global stores,
+// about a microsecond.
+template <bool kTma>
+__device__ __forceinline__ void arrive_leader_read(uint32_t bar) {
+  if constexpr (kTma)
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_leader(bar))
+                 : "memory");
+  else
+    sm100::mbar_arrive(bar);
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -446,57 +467,63 @@ __device__ __forceinline__ void clear(float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = 0.0f;
 }
 
-__device__ __forceinline__ uint32_t pack_pair(float a, float b, bool f16) {
-  if (f16) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+template <typename T>
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+  typename PairOf<T>::type p;
+  pair_from_f32(p, a, b);
+  return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+// A storing warp's 2 KB, in which a chunk is turned over: a row's 32 features are four 16-byte
+// blocks, exchanged so that neither the transposing stores nor the loads meet in a bank.
+struct Turn {
+  uint32_t base, put, get;
+  __device__ __forceinline__ Turn(uint32_t at, int lane)
+      : base(at),
+        // lanes 8 b .. 8 b + 7 give the places of block b of rows 0 .. 7
+        put(at + lane % 8 * 64 + ((lane / 8 ^ (lane >> 1 & 3)) << 4)),
+        // lanes 4 r .. 4 r + 3 read row r
+        get(at + lane / 4 * 64 + ((lane % 4 ^ (lane >> 3 & 3)) << 4)) {}
+};
+
 // Rounds kOctets octets of columns and stores them as `cols` rows of out, `stride` elements
-// apart, from feature m on, as far as M.  `turn` is the warp's 2 KB of shared memory, in which
-// the chunk is turned over: a row's 32 features are four 16-byte blocks, exchanged so that
-// neither the transposing stores nor the loads meet in a bank.
-template <int kOctets = 4>
-__device__ __forceinline__ void store_chunk(const ProductArgs& A, uint32_t turn,
+// apart, from feature m on, as far as M.
+template <typename T, int kOctets = 4>
+__device__ __forceinline__ void store_chunk(const ProductArgs& A, const Turn& turn,
                                             const float (&v)[8 * kOctets], uint16_t* out,
                                             int64_t stride, int64_t row, int cols, int m, int M,
                                             int lane) {
   __syncwarp();
 #pragma unroll
-  for (int j = 0; j < kOctets; ++j) {
-    uint32_t p[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = pack_pair(v[8 * j + 2 * i], v[8 * j + 2 * i + 1], A.f16);
-    // lanes 8 b .. 8 b + 7 give the places of block b of rows 8 j .. 8 j + 7
-    const int r = 8 * j + lane % 8, b = lane / 8;
+  for (int j = 0; j < kOctets; ++j)
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                     turn + r * 64 + ((b ^ (r >> 1 & 3)) << 4)),
-                 "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
+                     turn.put + 512 * j),
+                 "r"(pack_pair<T>(v[8 * j], v[8 * j + 1])),
+                 "r"(pack_pair<T>(v[8 * j + 2], v[8 * j + 3])),
+                 "r"(pack_pair<T>(v[8 * j + 4], v[8 * j + 5])),
+                 "r"(pack_pair<T>(v[8 * j + 6], v[8 * j + 7]))
                  : "memory");
-  }
   __syncwarp();
   if (A.vec) {
-    const int b = lane % 4;
-    if (m + 8 * b < M) {
-      uint16_t* to = out + row * stride + m + 8 * b;
+    m += lane % 4 * 8;
+    if (m < M) {
+      uint16_t* to = out + (row + lane / 4) * stride + m;
+      if (cols >= 8 * kOctets) {
 #pragma unroll
-      for (int i = 0; i < kOctets; ++i) {
-        const int r = 8 * i + lane / 4;
-        const uint4 w = sm100::lds128(turn + r * 64 + ((b ^ (r >> 1 & 3)) << 4));
-        if (r < cols) *reinterpret_cast<uint4*>(to + r * stride) = w;
+        for (int i = 0; i < kOctets; ++i, to += 8 * stride)
+          *reinterpret_cast<uint4*>(to) = sm100::lds128(turn.get + 512 * i);
+      } else {
+        for (int i = 0; 8 * i + lane / 4 < cols; ++i, to += 8 * stride)
+          *reinterpret_cast<uint4*>(to) = sm100::lds128(turn.get + 512 * i);
       }
     }
   } else if (m + lane < M) {
     uint16_t* to = out + row * stride + m + lane;
-    const int b = lane / 8;
     for (int r = 0; r < 8 * kOctets && r < cols; ++r, to += stride) {
       uint16_t w;
       asm volatile("ld.shared.u16 %0, [%1];"
                    : "=h"(w)
-                   : "r"(turn + r * 64 + ((b ^ (r >> 1 & 3)) << 4) + lane % 8 * 2)
+                   : "r"(turn.base + r * 64 + ((lane / 8 ^ (r >> 1 & 3)) << 4) + lane % 8 * 2)
                    : "memory");
       *to = w;
     }
@@ -519,16 +546,17 @@ __device__ __forceinline__ bool barrier_all(uint32_t id, uint32_t count, bool ye
 
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
-constexpr int kStorers = 8;    // warps that store, two for each 32 lanes of TMEM
 constexpr int kProducers = 4;  // warps that load, where loads are plain
-constexpr int kProductThreads(int ctas) {
-  return (4 + kStorers + (ctas > 1 ? 0 : kProducers)) * 32;
+constexpr int kProductThreads(int ctas, ProductMode mode) {
+  return (4 + kStorers(ctas, mode) +
+          (ctas == 1 ? kProducers : mode == ProductMode::kWeight ? 1 : 0)) * 32;
 }
 
-// Warps: 0 copies, 1 MMAs, 2 tells the tiles, 3 zeroes behind an expert's last rows (dweight),
-// 4 .. 11 store; 12 .. 15 load where loads are plain.
+// Warps: 0 copies, 1 MMAs, 2 tells the tiles, 3 and the last zero behind experts' last rows
+// (dweight; they take turns, since one takes about 2 us from a stage's arrival to the next),
+// 4 on store, and behind them kProducers load where loads are plain.
 template <int kCtas, ProductMode kMode>
-__global__ void __launch_bounds__(kProductThreads(kCtas), 1)
+__global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     hcmix_product_kernel(const __grid_constant__ ProductArgs A) {
   using namespace sm100;
   begin_kernel();
@@ -536,19 +564,20 @@ __global__ void __launch_bounds__(kProductThreads(kCtas), 1)
   constexpr bool kAcross = kMode != ProductMode::kRowsK;   // A lies with m contiguous
   constexpr bool kWeight = kMode == ProductMode::kWeight;  // and B with n
   constexpr int kMma = kMmaCtas(kCtas), kDepth = kStages(kCtas);
+  constexpr int kStore = kStorers(kCtas, kMode);
   extern __shared__ uint8_t product_shared[];
   const uint32_t raw = smem_u32(product_shared);
   const uint32_t stages = (raw + 1023) & ~1023u;
   uint8_t* after = product_shared + (stages - raw) + kRingBytes;
   float* exchange = reinterpret_cast<float*>(after);
-  ProductControl& C = *reinterpret_cast<ProductControl*>(after + kExchangeBytes);
-  int* cum = reinterpret_cast<int*>(after + kExchangeBytes + sizeof(ProductControl));
+  ProductControl& C = *reinterpret_cast<ProductControl*>(after + kStore * kTurnBytes);
+  int* cum = reinterpret_cast<int*>(after + kStore * kTurnBytes + sizeof(ProductControl));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int rank = blockIdx.x % kCtas, half_rank = rank % kMma;
   const bool leader = half_rank == 0;  // of a pair
 
   if (tid == 0) {
-    const int takers = kStorers + (kTma ? 1 : kProducers) + leader + (kTma && kWeight);
+    const int takers = kStore + (kTma ? 1 : kProducers) + leader + (kTma && kWeight ? 2 : 0);
     for (int q = 0; q < kQueue; ++q) {
       mbar_init(smem_u32(&C.told[q]), 1);
       mbar_init(smem_u32(&C.taken[q]), takers);
@@ -557,11 +586,11 @@ __global__ void __launch_bounds__(kProductThreads(kCtas), 1)
       mbar_init(smem_u32(&C.full[s]), kTma ? 1 : kProducers);
       mbar_init(smem_u32(&C.empty[s]), kCtas / kMma);
       mbar_init(smem_u32(&C.tail[s]), 1);
-      mbar_init(smem_u32(&C.ready[s]), kMma);
+      mbar_init(smem_u32(&C.ready[s]), 2 * kMma);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&C.acc_full[b]), 1);
-      mbar_init(smem_u32(&C.acc_empty[b]), kStorers * kMma);
+      mbar_init(smem_u32(&C.acc_empty[b]), kStore * kMma);
     }
     mbar_init(smem_u32(&C.drain), 1);
     C.abort = 0;
@@ -599,7 +628,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas), 1)
   };
   ProductTile T;
 
-  if (kTma ? warp == 0 : warp >= 4 + kStorers) {
+  if (kTma ? warp == 0 : warp >= 4 + kStore) {
     // ---- producer
     uint32_t it = 0;  // stages filled
     uint32_t full_at = 0, tail_at = 0, tails = 0;  // a bit for each stage: phases, and the last use
@@ -670,7 +699,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas), 1)
           }
           __syncwarp();
         } else {
-          const int ptid = tid - (4 + kStorers) * 32;
+          const int ptid = tid - (4 + kStore) * 32;
           constexpr int pthreads = kProducers * 32;
           const int k_end = T.k0 + T.depth;
           for (int h = 0; h < 2; ++h) {
@@ -694,33 +723,38 @@ __global__ void __launch_bounds__(kProductThreads(kCtas), 1)
     }
     if (kTma && lane == 0) {
       // copies that nobody waited for (another role gave up) land before the block ends
-      for (uint32_t i = it > kDepth ? it - kDepth : 0; i < it; ++i) {
-        const int s = i % kDepth;
+      for (uint32_t last = it > kDepth ? it - kDepth : 0; last < it; ++last) {
+        const int s = last % kDepth;
         if (tails >> s & 1)
           finish(C.tail[s], ~(tail_at >> s) & 1);
         else if (leader)
           finish(C.full[s], ~(full_at >> s) & 1);
       }
     }
-  } else if (kTma && kWeight && warp == 3) {
+  } else if (kTma && kWeight && (warp == 3 || warp == 4 + kStore)) {
     // ---- the last stage of an expert took rows of the next one along: they count as zeros
-    uint32_t it = 0, tail_at = 0;
+    uint32_t it = 0, tail_at = 0, tails = 0;
     bool ok = true;
     while (ok && next(T)) {
       it += T.depth / kTileK;
       const int left = T.depth % kTileK;
       if (left == 0) continue;
       const int s = it++ % kDepth;
+      // Both warps wait for every stage, and the MMAs for both warps: a wait by parity takes a
+      // phase for another if its barrier is not the phase before, or is two ahead.
       ok = __all_sync(0xffffffffu, wait(C.tail[s], tail_at >> s & 1));
       tail_at ^= 1u << s;
       if (!ok) break;
-      const uint32_t a = stages + s * kStageBytes(kCtas);
-      const int boxes = 2 + (round_rows<kCtas>(T.n) / kMma + 63) / 64;
-      const int gap = (left + 15) / 16 * 16 - left;  // of the last 16 that the MMA reads
-      for (int i = lane; i < boxes * gap * 8; i += 32) {
-        const int box = i / (gap * 8), in = i - box * (gap * 8);
-        sts128(a + box * kBoxBytes + left * 128 + in * 16, make_uint4(0, 0, 0, 0));
+      if ((tails++ & 1) != (warp == 3 ? 0u : 1u)) {  // the other's turn
+        if (lane == 0) arrive_leader_read<kTma>(smem_u32(&C.ready[s]));
+        continue;
       }
+      const int boxes = 2 + (round_rows<kCtas>(T.n) / kMma + 63) / 64;
+      // of the last 16 rows that the MMA reads
+      const uint32_t from = left * 128 + lane * 16, to = (left + 15) / 16 * 16 * 128;
+      for (int i = 0; i < boxes; ++i)
+        for (uint32_t at = from; at < to; at += 512)
+          sts128(stages + s * kStageBytes(kCtas) + i * kBoxBytes + at, make_uint4(0, 0, 0, 0));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive_leader<kTma>(smem_u32(&C.ready[s]));
@@ -770,15 +804,17 @@ __global__ void __launch_bounds__(kProductThreads(kCtas), 1)
     // what was issued is done before the block ends
     mma_commit<kTma>(smem_u32(&C.drain), pair);
     finish(C.drain, 0);
-  } else if (warp >= 4 && warp < 4 + kStorers) {
-    // ---- epilogue: TMEM lanes 32 * w on, every other chunk of 32 columns
+  } else if (warp >= 4 && warp < 4 + kStore) {
+    // ---- epilogue: TMEM lanes 32 * w on, chunks of 32 columns in turn
     const int w = warp % 4, half = (warp - 4) / 4;
     const int bar = 1 + (w & 1) + 2 * half;  // of g's and u's warp
     uint32_t acc = 0;
     bool ok = true;
     float* mine = exchange + (warp - 4) * (kTurnBytes / 4);
     const float* other = exchange + (half * 4 + (w ^ 2)) * (kTurnBytes / 4);
-    const uint32_t turn = smem_u32(mine);
+    const Turn turn(smem_u32(mine), lane);
+    const auto store_tiles = [&](auto zero) {
+    using T16 = decltype(zero);
     for (;;) {
       // g's and u's warps go on together, or both leave
       bool have = next(T);
@@ -794,7 +830,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas), 1)
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + buf * kTileN;
       const int64_t row = kWeight ? (int64_t)T.expert * A.N + T.n0 : T.n0;
-      for (int c = 32 * half; c < T.n; c += 64) {
+      for (int c = 32 * half; c < T.n; c += 8 * kStore) {
         const int cols = T.n - c < 32 ? T.n - c : 32;
         float v[32];
         if (A.out_f32) {
@@ -816,12 +852,12 @@ __global__ void __launch_bounds__(kProductThreads(kCtas), 1)
         else
           clear(v);
         if (!A.gated) {
-          store_chunk(A, turn, v, static_cast<uint16_t*>(A.out), A.M, row + c, cols,
+          store_chunk<T16>(A, turn, v, static_cast<uint16_t*>(A.out), A.M, row + c, cols,
                       T.m0 + w * 32, A.M, lane);
         } else if constexpr (!kWeight) {
           const int f = T.m0 + (w & 1) * 32;
           if (A.saved != nullptr)
-            store_chunk(A, turn, v, static_cast<uint16_t*>(A.saved) + (w < 2 ? 0 : A.M),
+            store_chunk<T16>(A, turn, v, static_cast<uint16_t*>(A.saved) + (w < 2 ? 0 : A.M),
                         2 * (int64_t)A.M, row + c, cols, f, A.M, lane);
           // g's warps give their upper 16 columns to u's, and get the lower ones of u
           __syncwarp();
@@ -835,34 +871,42 @@ __global__ void __launch_bounds__(kProductThreads(kCtas), 1)
           }
           named_bar_sync(bar, 64);  // both have read
           const int c0 = w < 2 ? 0 : 16;
-          store_chunk<2>(A, turn, reinterpret_cast<float(&)[16]>(v),
+          store_chunk<T16, 2>(A, turn, reinterpret_cast<float(&)[16]>(v),
                          static_cast<uint16_t*>(A.out), A.M, row + c + c0, cols - c0, f, A.M, lane);
         }
       }
       if (any) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader<kTma>(smem_u32(&C.acc_empty[buf]));
+        if (lane == 0) arrive_leader_read<kTma>(smem_u32(&C.acc_empty[buf]));
         ++acc;
       }
     }
+    };
+    if (A.f16)
+      store_tiles(__half{});
+    else
+      store_tiles(__nv_bfloat16{});
   } else if (warp == 2) {
-    // ---- the tiles, in turn over the clusters
-    const int64_t tiles = tile_count<kCtas, kMode>(A, cum);
-    bool ok = true;
-    for (int64_t t = blockIdx.x / kCtas; ok; t += gridDim.x / kCtas, ++turns) {
-      const int q = turns % kQueue;
-      const bool more = t < tiles;
-      if (more) T = tile_at<kCtas, kMode>(A, cum, t, rank);
-      if (turns >= kQueue) ok = __all_sync(0xffffffffu, wait(C.taken[q], (turns / kQueue - 1) & 1));
-      if (!ok) break;
-      if (lane == 0) {
-        if (!more) T.n = 0;
-        C.tile[q] = T;
-        mbar_arrive(smem_u32(&C.told[q]));
+    // ---- the tiles, in turn over the clusters.  Finding one takes loads and divisions, about
+    // a microsecond: the lanes find 32 at a time.
+    const int64_t tiles = tile_count<kCtas, kMode>(A, cum), step = gridDim.x / kCtas;
+    bool ok = true, more = true;
+    for (int64_t t0 = blockIdx.x / kCtas; ok && more; t0 += 32 * step) {
+      const int64_t t = t0 + lane * step;
+      if (t < tiles) T = tile_at<kCtas, kMode>(A, cum, t, rank);
+      else T.n = 0;
+      for (int i = 0; ok && more && i < 32; ++i, ++turns) {
+        const int q = turns % kQueue;
+        if (turns >= kQueue)
+          ok = __all_sync(0xffffffffu, wait(C.taken[q], (turns / kQueue - 1) & 1));
+        if (!ok) break;
+        if (lane == i) {
+          C.tile[q] = T;
+          mbar_arrive(smem_u32(&C.told[q]));
+        }
+        more = __shfl_sync(0xffffffffu, T.n, i) > 0;
       }
-      __syncwarp();
-      if (!more) break;
     }
   }
   // rows that no expert has
@@ -942,13 +986,13 @@ hcmix_status resident_clusters(int* clusters) {
     return HCMIX_OK;
   }
   auto kernel = hcmix_product_kernel<kCtas, kMode>;
-  const size_t smem = product_smem(kProductExperts);
+  const size_t smem = product_smem<kCtas, kMode>(kProductExperts);
   st = checked(
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
   if (st != HCMIX_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCtas);
-  cfg.blockDim = dim3(kProductThreads(kCtas));
+  cfg.blockDim = dim3(kProductThreads(kCtas, kMode));
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -977,8 +1021,8 @@ hcmix_status launch_product(const ProductArgs& A, cudaStream_t stream) {
                             : mt * (A.R / kTileN + (A.R < A.E ? A.R : A.E));
   const int64_t grid = tiles < most ? (tiles > 0 ? tiles : 1) : most;
   return launch(hcmix_product_kernel<kCtas, kMode>, dim3((unsigned)grid * kCtas),
-                dim3(kProductThreads(kCtas)), product_smem(A.E), product_smem(kProductExperts),
-                stream, A, kCtas);
+                dim3(kProductThreads(kCtas, kMode)), product_smem<kCtas, kMode>(A.E),
+                product_smem<kCtas, kMode>(kProductExperts), stream, A, kCtas);
 }
 
 // a, b, offsets, R, E, M, N, K, gated, out, saved and types are set.
