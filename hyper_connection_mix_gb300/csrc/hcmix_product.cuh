@@ -221,6 +221,17 @@ __device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* 
   return T;
 }
 
+// dweight by pairs: an expert's last 64 rows, if they are fewer, are zeroed behind before they
+// are multiplied, which takes about 2 us from their arrival.  So they are copied up to
+// kTailLead stages early and still multiplied last.  Their place among the tile's stages; the
+// number of stages where there are none such.
+constexpr int kTailLead = 3;
+__device__ __forceinline__ int tail_place(int depth) {
+  const int blocks = (depth + kTileK - 1) / kTileK;
+  if (depth % kTileK == 0) return blocks;
+  return blocks - 1 < kTailLead ? 0 : blocks - 1 - kTailLead;
+}
+
 // ---- plain loads: 64 x `rows` elements into the swizzled box at `dst`, element by
 // element, zeros outside of the matrix.  For matrices whose rows do not all start on
 // 16 bytes.
@@ -637,8 +648,10 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       const int blocks = (T.depth + kTileK - 1) / kTileK;
       const int n = round_rows<kCtas>(T.n) / kMma;  // this block's share of B
       const int n0 = T.n0 + half_rank * n;
-      for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
+      const int place = kTma && kWeight ? tail_place(T.depth) : blocks;
+      for (int i = 0; ok && i < blocks; ++i, ++it) {
         const int s = it % kDepth;
+        const int kb = i < place ? i : i == place ? blocks - 1 : i - 1;
         const uint32_t a = stages + s * kStageBytes(kCtas), b = a + kABytes;
         const int k = T.k0 + kb * kTileK;
         if (it >= kDepth) ok = wait(C.empty[s], (it / kDepth - 1) & 1);
@@ -650,7 +663,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
             const uint64_t keep = l2_policy_evict_last();
             // block 0 waits for both blocks' copies at once, but for the last rows of an expert,
             // behind which each block has to zero its own
-            const bool tail = kWeight && T.depth - kb * kTileK < kTileK;
+            const bool tail = i == place;
             const uint32_t own = smem_u32(tail ? &C.tail[s] : &C.full[s]);
             const uint32_t bar = tail ? own : in_leader(own);
             if (tail)
@@ -670,8 +683,8 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
             }
             if constexpr (kCtas == 2) {
               if (kWeight) {
-                for (int i = 0; i < boxes; ++i)
-                  pair_load_2d(b + i * kBoxBytes, &A.b_map, n0 + i * 64, k, bar, keep);
+                for (int j = 0; j < boxes; ++j)
+                  pair_load_2d(b + j * kBoxBytes, &A.b_map, n0 + j * 64, k, bar, keep);
               } else {
                 int r = 0;
                 for (; r + 64 <= n; r += 64)
@@ -685,8 +698,8 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
               const int second = rank / 2;
               if (kWeight) {
                 const int most = (boxes + 1) / 2;
-                for (int i = second ? most : 0; i < (second ? boxes : most); ++i)
-                  pair_send_2d(b + i * kBoxBytes, &A.b_map, n0 + i * 64, k, bar, mask, keep);
+                for (int j = second ? most : 0; j < (second ? boxes : most); ++j)
+                  pair_send_2d(b + j * kBoxBytes, &A.b_map, n0 + j * 64, k, bar, mask, keep);
               } else {
                 const int most = (n / 16 + 1) / 2 * 16, end = second ? n : most;
                 int r = second ? most : 0;
@@ -710,8 +723,8 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
               load_box(a + h * kBoxBytes, A.a, T.expert, k, m, A.a.outer, 64, ptid, pthreads);
           }
           if (kWeight) {
-            for (int i = 0; i * 64 < n; ++i)
-              load_box(b + i * kBoxBytes, A.b, 0, n0 + i * 64, k, k_end, 64, ptid, pthreads);
+            for (int j = 0; j * 64 < n; ++j)
+              load_box(b + j * kBoxBytes, A.b, 0, n0 + j * 64, k, k_end, 64, ptid, pthreads);
           } else {
             load_box(b, A.b, 0, k, n0, T.n0 + T.n, n, ptid, pthreads);
           }
@@ -736,10 +749,9 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     uint32_t it = 0, tail_at = 0, tails = 0;
     bool ok = true;
     while (ok && next(T)) {
-      it += T.depth / kTileK;
-      const int left = T.depth % kTileK;
+      const int left = T.depth % kTileK, s = (it + tail_place(T.depth)) % kDepth;
+      it += (T.depth + kTileK - 1) / kTileK;
       if (left == 0) continue;
-      const int s = it++ % kDepth;
       // Both warps wait for every stage, and the MMAs for both warps: a wait by parity takes a
       // phase for another if its barrier is not the phase before, or is two ahead.
       ok = __all_sync(0xffffffffu, wait(C.tail[s], tail_at >> s & 1));
@@ -776,10 +788,11 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       if (acc >= 2) ok = __all_sync(0xffffffffu, wait(C.acc_empty[buf], (acc / 2 - 1) & 1));
       tc_fence_after();
       const uint32_t d = tmem + buf * kTileN;
-      for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
-        const int s = it % kDepth;
+      const int place = kTma && kWeight ? tail_place(T.depth) : blocks;
+      for (int kb = 0; ok && kb < blocks; ++kb) {
+        const bool tail = place < blocks && kb == blocks - 1;
+        const int s = (it + (tail ? place : kb < place ? kb : kb + 1)) % kDepth;
         const int left = T.depth - kb * kTileK;
-        const bool tail = kTma && kWeight && left < kTileK;
         ok = __all_sync(0xffffffffu, tail ? wait(C.ready[s], tail_at >> s & 1)
                                           : wait(C.full[s], full_at >> s & 1));
         (tail ? tail_at : full_at) ^= 1u << s;
@@ -799,6 +812,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
         mma_commit<kTma>(smem_u32(&C.empty[s]), (1u << kCtas) - 1);
         if (kb == blocks - 1) mma_commit<kTma>(smem_u32(&C.acc_full[buf]), pair);
       }
+      it += blocks;
       ++acc;
     }
     // what was issued is done before the block ends

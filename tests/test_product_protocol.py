@@ -20,7 +20,7 @@ import random
 
 import pytest
 
-DEPTH, QUEUE, STORERS = 6, 4, 2  # STORERS: two stand for a block's eight or sixteen
+DEPTH, QUEUE, LEAD, STORERS = 6, 4, 3, 2  # STORERS: two stand for a block's eight or sixteen
 
 
 class Bar:
@@ -83,9 +83,13 @@ class Cluster:
             b["told"][turn % QUEUE].arrive()
 
     def stages(self, depth):
-        """(stage of the tile, whether it is a tail)"""
+        """(place in the ring, whether it is a tail), in the order in which they are multiplied;
+        they are copied in the order of their places."""
         whole = int(depth)
-        return [(i, False) for i in range(whole)] + ([(whole, True)] if depth > whole else [])
+        if depth == whole or not self.weight:
+            return [(i, False) for i in range(whole + (depth > whole))]
+        tail = max(0, whole - LEAD)
+        return [(i, False) for i in range(whole + 1) if i != tail] + [(tail, True)]
 
     def producer(self, c):
         it, b = 0, self.bars[c]
@@ -93,8 +97,7 @@ class Cluster:
         used = {"full": [0] * DEPTH, "tail": [0] * DEPTH}
         for turn, depth in enumerate(self.tiles):
             yield from self.next(c, turn)
-            for _, tail in self.stages(depth):
-                tail = tail and self.weight
+            for _, tail in sorted(self.stages(depth)):
                 s = it % DEPTH
                 if it >= DEPTH:
                     yield from self.wait(b["empty"][s], it // DEPTH - 1)
@@ -127,11 +130,12 @@ class Cluster:
         uses = [0] * DEPTH
         for turn, depth in enumerate(self.tiles):
             yield from self.next(c, turn)
-            it += int(depth)
+            stages = self.stages(depth)
+            it += len(stages)
             if depth == int(depth):
                 continue
-            s = it % DEPTH
-            it += 1
+            mark = it - len(stages) + stages[-1][0]
+            s = mark % DEPTH
             phase, mine = uses[s], tails % 2 == which
             uses[s] += 1
             tails += 1
@@ -143,7 +147,7 @@ class Cluster:
                 self.bars[c & ~1]["ready"][s].arrive()
                 continue
             st = self.stage[c][s]
-            if st["it"] != it - 1 or st["parts"] != 1 + self.ctas // 2:
+            if st["it"] != mark or st["parts"] != 1 + self.ctas // 2:
                 self.errors.append(f"zeroed behind stage {s} of block {c} before its copies had landed")
             st["zeroed"] = True
             yield None
@@ -161,16 +165,16 @@ class Cluster:
             buf = acc % 2
             if acc >= 2:
                 yield from self.wait(b["acc_empty"][buf], acc // 2 - 1)
-            for i, tail in stages:
-                s = it % DEPTH
-                name = "ready" if tail and self.weight else "full"
+            for i, (place, tail) in enumerate(stages):
+                s = (it + place) % DEPTH
+                name = "ready" if tail else "full"
                 yield from self.wait(b[name][s], uses[name][s])
                 uses[name][s] += 1
-                self.pipes[p].append(("read", s, it, tail and self.weight, buf))
+                self.pipes[p].append(("read", s, it + place, tail, buf))
                 self.pipes[p].append(("empty", s))
                 if i == len(stages) - 1:
                     self.pipes[p].append(("acc", buf))
-                it += 1
+            it += len(stages)
             acc += 1
         yield from self.next(c, len(self.tiles))
 
