@@ -125,10 +125,10 @@ hcmix_status hc_mix_expert_product_weight_backward(const void* dys, int64_t dys_
     HCMIX_TRY(check_matrix(dys, dys_stride, N, 2));
     HCMIX_TRY(check_matrix(xs, xs_stride, K, 2));
   }
-  // the result's contiguous index is the lanes': k, or n where dweight is transposed
+  // the result's outer index is the lanes': n, or k where dweight is transposed
   const Matrix3 x = matrix(xs, xs_stride, 0, K, R), dy = matrix(dys, dys_stride, 0, N, R);
   ProductArgs A = {};
-  A.a = transposed ? dy : x, A.b = transposed ? x : dy;
+  A.a = transposed ? x : dy, A.b = transposed ? dy : x;
   A.offsets = offsets, A.R = R, A.E = (int)E;
   A.M = A.a.inner, A.N = A.b.inner;
   A.out = dweight, A.f16 = type == HCMIX_F16, A.out_f32 = grad_type == HCMIX_F32;

@@ -6,11 +6,11 @@
 //
 //   product            m: features of W[e]      n: rows of xs     k: width of xs
 //   its dxs            m: width of W[e]         n: rows of dys    k: features
-//   its dweight        m: inner index of dW[e]  n: its outer one  k: rows of the expert
+//   its dweight        m: outer index of dW[e]  n: its inner one  k: rows of the expert
 //
 // With the rows as the MMA's N, which may be any multiple of 16, an expert of few rows
-// costs few columns and not a whole tile of 128; and a warp's lanes are neighbours in
-// the row-major result.  fp32 accumulation in TMEM over all of k, one rounding at the
+// costs few columns and not a whole tile of 128.  The products' tiles are turned over in shared
+// memory on their way out; dweight's leave as they are, in boxes of 64 columns.  fp32 accumulation in TMEM over all of k, one rounding at the
 // store.  Blocks are persistent: a producer fills a ring of 64-wide slices of A and B,
 // one thread issues the MMAs, and four warps store a tile while the next is computed.
 #pragma once
@@ -46,8 +46,7 @@ constexpr int kABytes = kTileM * kTileK * 2;
 __host__ __device__ constexpr int kMmaCtas(int ctas) { return ctas > 1 ? 2 : 1; }
 __host__ __device__ constexpr int kStageBytes(int ctas) { return kABytes + kTileN * kTileK * 2 / kMmaCtas(ctas); }
 __host__ __device__ constexpr int kStages(int ctas) { return ctas > 1 ? 6 : 4; }
-constexpr int kRingBytes = kStageBytes(2) * kStages(2);
-static_assert(kRingBytes == kStageBytes(1) * kStages(1), "one size of ring");
+constexpr int kMostStages = 6;
 constexpr int kPanel = 16;  // row tiles that take their turns at the same weights
 constexpr uint64_t kProductWaitNs = 2000000000ull;
 
@@ -60,13 +59,14 @@ struct Matrix3 {
 
 struct ProductArgs {
   CUtensorMap a_map, b_map, b16_map;  // boxes of 64 x 64, and of 64 x 16
+  CUtensorMap out_map;                // dweight: boxes of 32 rows of 128 bytes
   Matrix3 a, b;
   const int32_t* offsets;
   int64_t R;
   int E;
   int M, N, K;        // extents of m, n and k; product: N unused, dweight: K unused
   int gated;          // A's rows M .. 2 M - 1 are u's features, those before g's
-  void* out;          // product: [R, M]; dweight: [E, N, M]
+  void* out;          // product: [R, M]; dweight: [E, M, N]
   void* saved;        // gated: [R, 2 M] or null
   int f16, out_f32;
   int vec;            // rows of out (and saved) start on 16 bytes
@@ -90,26 +90,26 @@ constexpr int kQueue = 4;  // tiles told ahead
 struct ProductControl {
   ProductTile tile[kQueue];
   uint64_t told[kQueue], taken[kQueue];
-  uint64_t full[6], empty[6];
-  uint64_t tail[6], ready[6];  // dweight by pairs: a block's last stage of a tile, and both's zeroed
+  uint64_t full[kMostStages], empty[kMostStages];
+  // dweight by pairs: a block's last stage of a tile, and both blocks' zeroed ones
+  uint64_t tail[kMostStages], ready[kMostStages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem;
   int abort;
   int scan[32];
 };
-// Warps that store.  A chunk of 32 x 32 takes a warp about 0.5 us, most of it latency: eight
-// warps keep up with a tile's MMAs where k is long, and sixteen with the stores of dweight,
-// whose k may be an expert's few rows.
-__host__ __device__ constexpr int kStorers(int ctas, ProductMode mode) {
-  return ctas > 1 && mode == ProductMode::kWeight ? 16 : 8;
+constexpr int kStorers = 8;  // warps that store: two for each 32 lanes of TMEM
+// A storing warp's shared memory: half a chunk of 32 x 32 in fp32 or a rounded one; dweight: a
+// box of 32 rows of 128 bytes.
+__host__ __device__ constexpr int kTurnBytes(ProductMode mode) {
+  return mode == ProductMode::kWeight ? 4096 : 2048;
 }
-constexpr int kTurnBytes = 2048;  // a storing warp's: half a chunk in fp32, or a rounded one
 // Shared memory of a block; dweight needs no table of the experts' tiles.
 template <int kCtas, ProductMode kMode>
 constexpr size_t product_smem(int E) {
-  return 1024 + (size_t)kRingBytes + kStorers(kCtas, kMode) * kTurnBytes + sizeof(ProductControl) +
-         (kMode == ProductMode::kWeight ? 0 : ((size_t)E + 1) * 4);
+  return 1024 + (size_t)kStages(kCtas) * kStageBytes(kCtas) +
+         kStorers * kTurnBytes(kMode) + sizeof(ProductControl) + (kMode == ProductMode::kWeight ? 0 : ((size_t)E + 1) * 4);
 }
 static_assert(product_smem<2, ProductMode::kRowsK>(kProductExperts) <= 227 * 1024 &&
                   product_smem<2, ProductMode::kWeight>(kProductExperts) <= 227 * 1024,
@@ -541,6 +541,54 @@ __device__ __forceinline__ void store_chunk(const ProductArgs& A, const Turn& tu
   }
 }
 
+// A lane's 32 values as `cols` neighbours of a row, one by one.
+template <typename T>
+__device__ __forceinline__ void store_row(T* to, const float (&v)[32], int cols) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < cols) to[i] = from_f32<T>(v[i]);
+}
+
+// A lane's kCount values, 64 bytes, as a half of its row of the warp's box.
+template <typename T, int kCount>
+__device__ __forceinline__ void put_row(uint32_t box, const float (&v)[32], int first, int half,
+                                        int lane) {
+  constexpr int kPer = 16 / (int)sizeof(T);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    Packed<T, kPer> p;
+    float f[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) f[k] = v[first + b * kPer + k];
+    p.pack(f);
+    sm100::sts128(box + lane * 128 + ((4 * half + b ^ (lane & 7)) << 4),
+                  *reinterpret_cast<const uint4*>(&p));
+  }
+}
+
+// By a whole warp: its box in shared memory as rows m .. m + 31 of an expert's result, from
+// column n on, as far as the result goes; and the wait until the box may be written again.
+__device__ __forceinline__ void box_store(const void* map, uint32_t box, int n, int m, int expert,
+                                          int lane) {
+  sm100::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(n), "r"(m), "r"(expert), "r"(box)
+        : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+__device__ __forceinline__ void box_free(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ void box_end(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // Barrier `id` over `count` threads of whole warps, and whether all of them say yes.
 __device__ __forceinline__ bool barrier_all(uint32_t id, uint32_t count, bool yes) {
   uint32_t r;
@@ -559,7 +607,7 @@ __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __e
 
 constexpr int kProducers = 4;  // warps that load, where loads are plain
 constexpr int kProductThreads(int ctas, ProductMode mode) {
-  return (4 + kStorers(ctas, mode) +
+  return (4 + kStorers +
           (ctas == 1 ? kProducers : mode == ProductMode::kWeight ? 1 : 0)) * 32;
 }
 
@@ -575,20 +623,20 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   constexpr bool kAcross = kMode != ProductMode::kRowsK;   // A lies with m contiguous
   constexpr bool kWeight = kMode == ProductMode::kWeight;  // and B with n
   constexpr int kMma = kMmaCtas(kCtas), kDepth = kStages(kCtas);
-  constexpr int kStore = kStorers(kCtas, kMode);
+  constexpr int kTurns = kStorers * kTurnBytes(kMode);
   extern __shared__ uint8_t product_shared[];
   const uint32_t raw = smem_u32(product_shared);
   const uint32_t stages = (raw + 1023) & ~1023u;
-  uint8_t* after = product_shared + (stages - raw) + kRingBytes;
+  uint8_t* after = product_shared + (stages - raw) + kDepth * kStageBytes(kCtas);
   float* exchange = reinterpret_cast<float*>(after);
-  ProductControl& C = *reinterpret_cast<ProductControl*>(after + kStore * kTurnBytes);
-  int* cum = reinterpret_cast<int*>(after + kStore * kTurnBytes + sizeof(ProductControl));
+  ProductControl& C = *reinterpret_cast<ProductControl*>(after + kTurns);
+  int* cum = reinterpret_cast<int*>(after + kTurns + sizeof(ProductControl));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int rank = blockIdx.x % kCtas, half_rank = rank % kMma;
   const bool leader = half_rank == 0;  // of a pair
 
   if (tid == 0) {
-    const int takers = kStore + (kTma ? 1 : kProducers) + leader + (kTma && kWeight ? 2 : 0);
+    const int takers = kStorers + (kTma ? 1 : kProducers) + leader + (kTma && kWeight ? 2 : 0);
     for (int q = 0; q < kQueue; ++q) {
       mbar_init(smem_u32(&C.told[q]), 1);
       mbar_init(smem_u32(&C.taken[q]), takers);
@@ -601,7 +649,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&C.acc_full[b]), 1);
-      mbar_init(smem_u32(&C.acc_empty[b]), kStore * kMma);
+      mbar_init(smem_u32(&C.acc_empty[b]), kStorers * kMma);
     }
     mbar_init(smem_u32(&C.drain), 1);
     C.abort = 0;
@@ -639,7 +687,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   };
   ProductTile T;
 
-  if (kTma ? warp == 0 : warp >= 4 + kStore) {
+  if (kTma ? warp == 0 : warp >= 4 + kStorers) {
     // ---- producer
     uint32_t it = 0;  // stages filled
     uint32_t full_at = 0, tail_at = 0, tails = 0;  // a bit for each stage: phases, and the last use
@@ -712,7 +760,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
           }
           __syncwarp();
         } else {
-          const int ptid = tid - (4 + kStore) * 32;
+          const int ptid = tid - (4 + kStorers) * 32;
           constexpr int pthreads = kProducers * 32;
           const int k_end = T.k0 + T.depth;
           for (int h = 0; h < 2; ++h) {
@@ -744,7 +792,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
           finish(C.full[s], ~(full_at >> s) & 1);
       }
     }
-  } else if (kTma && kWeight && (warp == 3 || warp == 4 + kStore)) {
+  } else if (kTma && kWeight && (warp == 3 || warp == 4 + kStorers)) {
     // ---- the last stage of an expert took rows of the next one along: they count as zeros
     uint32_t it = 0, tail_at = 0, tails = 0;
     bool ok = true;
@@ -818,14 +866,14 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     // what was issued is done before the block ends
     mma_commit<kTma>(smem_u32(&C.drain), pair);
     finish(C.drain, 0);
-  } else if (warp >= 4 && warp < 4 + kStore) {
+  } else if (warp >= 4 && warp < 4 + kStorers) {
     // ---- epilogue: TMEM lanes 32 * w on, chunks of 32 columns in turn
     const int w = warp % 4, half = (warp - 4) / 4;
     const int bar = 1 + (w & 1) + 2 * half;  // of g's and u's warp
     uint32_t acc = 0;
     bool ok = true;
-    float* mine = exchange + (warp - 4) * (kTurnBytes / 4);
-    const float* other = exchange + (half * 4 + (w ^ 2)) * (kTurnBytes / 4);
+    float* mine = exchange + (warp - 4) * (kTurnBytes(kMode) / 4);
+    const float* other = exchange + (half * 4 + (w ^ 2)) * (kTurnBytes(kMode) / 4);
     const Turn turn(smem_u32(mine), lane);
     const auto store_tiles = [&](auto zero) {
     using T16 = decltype(zero);
@@ -843,24 +891,43 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + buf * kTileN;
-      const int64_t row = kWeight ? (int64_t)T.expert * A.N + T.n0 : T.n0;
-      for (int c = 32 * half; c < T.n; c += 8 * kStore) {
+      if constexpr (kWeight) {
+        const int m0 = T.m0 + w * 32;
+        for (int c = 64 * half; c < T.n && m0 < A.M; c += 128) {
+          if (A.vec) box_free(lane);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[32];
+            if (any) {
+              tmem_ld32(d + c + 32 * h, reinterpret_cast<uint32_t(&)[32]>(v));
+              tmem_wait_ld();
+            } else {
+              clear(v);
+            }
+            const int n = T.n0 + c + 32 * h, cols = A.N - n < 32 ? A.N - n : 32;
+            const int64_t at = ((int64_t)T.expert * A.M + m0 + lane) * A.N + n;
+            if (!A.vec) {
+              if (m0 + lane >= A.M) continue;
+              if (A.out_f32)
+                store_row(static_cast<float*>(A.out) + at, v, cols);
+              else
+                store_row(static_cast<T16*>(A.out) + at, v, cols);
+            } else if (A.out_f32) {  // a box of 32 columns
+              put_row<float, 16>(turn.base, v, 0, 0, lane);
+              put_row<float, 16>(turn.base, v, 16, 1, lane);
+              if (cols > 0) box_store(&A.out_map, turn.base, n, m0, T.expert, lane);
+              if (h == 0) box_free(lane);
+            } else {
+              put_row<T16, 32>(turn.base, v, 0, h, lane);
+              if (h == 1) box_store(&A.out_map, turn.base, n - 32, m0, T.expert, lane);
+            }
+          }
+        }
+      } else {
+      const int64_t row = T.n0;
+      for (int c = 32 * half; c < T.n; c += 8 * kStorers) {
         const int cols = T.n - c < 32 ? T.n - c : 32;
         float v[32];
-        if (A.out_f32) {
-          if (any) {
-            tmem_ld32(d + c, reinterpret_cast<uint32_t(&)[32]>(v));
-            tmem_wait_ld();
-          } else {
-            clear(v);
-          }
-          const int m = T.m0 + w * 32 + lane;
-          float* out = static_cast<float*>(A.out) + (row + c) * A.M + m;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < cols && m < A.M) out[(int64_t)i * A.M] = v[i];
-          continue;
-        }
         if (any)
           tmem_ld_fragments(d + c, v);
         else
@@ -868,7 +935,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
         if (!A.gated) {
           store_chunk<T16>(A, turn, v, static_cast<uint16_t*>(A.out), A.M, row + c, cols,
                       T.m0 + w * 32, A.M, lane);
-        } else if constexpr (!kWeight) {
+        } else {
           const int f = T.m0 + (w & 1) * 32;
           if (A.saved != nullptr)
             store_chunk<T16>(A, turn, v, static_cast<uint16_t*>(A.saved) + (w < 2 ? 0 : A.M),
@@ -889,6 +956,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
                          static_cast<uint16_t*>(A.out), A.M, row + c + c0, cols - c0, f, A.M, lane);
         }
       }
+      }
       if (any) {
         tc_fence_before();
         __syncwarp();
@@ -901,6 +969,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       store_tiles(__half{});
     else
       store_tiles(__nv_bfloat16{});
+    if (kWeight && A.vec) box_end(lane);
   } else if (warp == 2) {
     // ---- the tiles, in turn over the clusters.  Finding one takes loads and divisions, about
     // a microsecond: the lanes find 32 at a time.
@@ -985,6 +1054,24 @@ inline bool make_box_map(CUtensorMap* map, const Matrix3& X, int experts, bool f
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// dweight's boxes; false where its rows do not start on 16 bytes.
+inline bool make_out_map(ProductArgs& A) {
+  EncodeFn fn = encode_fn();
+  const int size = A.out_f32 ? 4 : 2;
+  const cuuint64_t row = (cuuint64_t)A.N * size, expert = row * A.M;
+  if (fn == nullptr || row % 16 != 0 || reinterpret_cast<uintptr_t>(A.out) % 16 != 0) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)A.N, (cuuint64_t)A.M, (cuuint64_t)A.E};
+  const cuuint64_t strides[2] = {row, expert};
+  const cuuint32_t box[3] = {128u / size, 32, 1};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  const CUtensorMapDataType type = A.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : A.f16   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return fn(&A.out_map, type, 3, A.out, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The clusters that the current device runs at a time (of four blocks fewer than a quarter of
 // its multiprocessors: 36 on 152).  Asked for once a device.
 template <int kCtas, ProductMode kMode>
@@ -1042,7 +1129,10 @@ hcmix_status launch_product(const ProductArgs& A, cudaStream_t stream) {
 // a, b, offsets, R, E, M, N, K, gated, out, saved and types are set.
 template <ProductMode kMode>
 hcmix_status run_product(ProductArgs& A, cudaStream_t stream) {
-  A.vec = vector_bytes(2, {{A.out, A.M}, {A.saved, A.M}}) == 16;
+  if (kMode == ProductMode::kWeight)
+    A.vec = make_out_map(A);
+  else
+    A.vec = vector_bytes(2, {{A.out, A.M}, {A.saved, A.M}}) == 16;
   const int experts = kMode == ProductMode::kWeight ? 0 : A.E;  // 0: a is a matrix as b is
   // a box starts on 16 bytes: u's features, too, where they lie along the rows
   const bool starts = kMode != ProductMode::kRowsM || !A.gated || A.M % 8 == 0;

@@ -20,7 +20,7 @@ import random
 
 import pytest
 
-DEPTH, QUEUE, LEAD, STORERS = 6, 4, 3, 2  # STORERS: two stand for a block's eight or sixteen
+QUEUE, LEAD, STORERS = 4, 3, 2  # STORERS: two stand for a block's eight or sixteen
 
 
 class Bar:
@@ -47,6 +47,7 @@ class Cluster:
     def __init__(self, ctas, depths, weight, seed, planted=None):
         """`depths`: of each tile, in stages and, as a half, a last one that is not whole."""
         self.rnd, self.ctas, self.tiles, self.weight, self.planted = random.Random(seed), ctas, depths, weight, planted
+        self.depth = 6
         self.copies, self.pipes = [], [[] for _ in range(ctas // 2)]
         self.errors = []
         tailers = 2 if weight else 0
@@ -56,11 +57,11 @@ class Cluster:
             mk = lambda n, count, what: [Bar(count, f"{what}{i} of block {c}") for i in range(n)]  # noqa: E731
             self.bars.append({
                 "told": mk(QUEUE, 1, "told"), "taken": mk(QUEUE, STORERS + 1 + lead + tailers, "taken"),
-                "full": mk(DEPTH, 1, "full"), "empty": mk(DEPTH, ctas // 2, "empty"),
-                "tail": mk(DEPTH, 1, "tail"), "ready": mk(DEPTH, 4, "ready"),
+                "full": mk(self.depth, 1, "full"), "empty": mk(self.depth, ctas // 2, "empty"),
+                "tail": mk(self.depth, 1, "tail"), "ready": mk(self.depth, 4, "ready"),
                 "acc_full": mk(2, 1, "acc_full"), "acc_empty": mk(2, 2 * STORERS, "acc_empty")})
         # per block and slot: what lies there, and the MMAs (a pair's) that still have to read it
-        self.stage = [[{"it": None, "parts": 0, "zeroed": False, "readers": 0} for _ in range(DEPTH)] for _ in range(ctas)]
+        self.stage = [[{"it": None, "parts": 0, "zeroed": False, "readers": 0} for _ in range(self.depth)] for _ in range(ctas)]
         self.acc_unread = [[0, 0] for _ in range(ctas // 2)]
 
     # ---- roles, as generators that yield (barrier, phase) where they wait
@@ -94,13 +95,13 @@ class Cluster:
     def producer(self, c):
         it, b = 0, self.bars[c]
         lead = self.bars[c & ~1]
-        used = {"full": [0] * DEPTH, "tail": [0] * DEPTH}
+        used = {"full": [0] * self.depth, "tail": [0] * self.depth}
         for turn, depth in enumerate(self.tiles):
             yield from self.next(c, turn)
             for _, tail in sorted(self.stages(depth)):
-                s = it % DEPTH
-                if it >= DEPTH:
-                    yield from self.wait(b["empty"][s], it // DEPTH - 1)
+                s = it % self.depth
+                if it >= self.depth:
+                    yield from self.wait(b["empty"][s], it // self.depth - 1)
                 name = "tail" if tail else "full"
                 shares = self.ctas // 2   # A and this block's part of its share of B; the rest is sent here
                 if tail:
@@ -127,7 +128,7 @@ class Cluster:
 
     def tailer(self, c, which):
         it, tails, b = 0, 0, self.bars[c]
-        uses = [0] * DEPTH
+        uses = [0] * self.depth
         for turn, depth in enumerate(self.tiles):
             yield from self.next(c, turn)
             stages = self.stages(depth)
@@ -135,7 +136,7 @@ class Cluster:
             if depth == int(depth):
                 continue
             mark = it - len(stages) + stages[-1][0]
-            s = mark % DEPTH
+            s = mark % self.depth
             phase, mine = uses[s], tails % 2 == which
             uses[s] += 1
             tails += 1
@@ -156,7 +157,7 @@ class Cluster:
 
     def mma(self, c):
         it, acc, b, p = 0, 0, self.bars[c], c // 2
-        uses = {"full": [0] * DEPTH, "ready": [0] * DEPTH}
+        uses = {"full": [0] * self.depth, "ready": [0] * self.depth}
         for turn, depth in enumerate(self.tiles):
             yield from self.next(c, turn)
             stages = self.stages(depth)
@@ -166,7 +167,7 @@ class Cluster:
             if acc >= 2:
                 yield from self.wait(b["acc_empty"][buf], acc // 2 - 1)
             for i, (place, tail) in enumerate(stages):
-                s = (it + place) % DEPTH
+                s = (it + place) % self.depth
                 name = "ready" if tail else "full"
                 yield from self.wait(b[name][s], uses[name][s])
                 uses[name][s] += 1
