@@ -15,10 +15,6 @@
 // one thread issues the MMAs, and four warps store a tile while the next is computed.
 #pragma once
 
-#ifndef QUAD
-#define QUAD 0
-#endif
-
 #include <cuda.h>
 
 #include <atomic>
@@ -47,7 +43,13 @@ __host__ __device__ constexpr int kMmaCtas(int ctas) { return ctas > 1 ? 2 : 1; 
 __host__ __device__ constexpr int kStageBytes(int ctas) { return kABytes + kTileN * kTileK * 2 / kMmaCtas(ctas); }
 __host__ __device__ constexpr int kStages(int ctas) { return ctas > 1 ? 6 : 4; }
 constexpr int kMostStages = 6;
-constexpr int kPanel = 16;  // row tiles that take their turns at the same weights
+// Row tiles of a panel, whose rows are read again for each of the features' tiles: few enough to
+// stay in L2 (32 experts of 512 rows 5120 -> 4096: panels of 20 MB 409 us, 40 MB 424, 80 MB 455).
+constexpr int64_t kPanelBytes = 20 << 20;
+inline int panel_tiles(int64_t K) {
+  const int64_t n = kPanelBytes / (kTileN * K * 2);
+  return (int)(n < 8 ? 8 : n > 64 ? 64 : n);
+}
 constexpr uint64_t kProductWaitNs = 2000000000ull;
 
 // One operand as it lies in memory: rows of contiguous elements.
@@ -65,6 +67,7 @@ struct ProductArgs {
   int64_t R;
   int E;
   int M, N, K;        // extents of m, n and k; product: N unused, dweight: K unused
+  int panel;          // product: row tiles that take turns at the same features
   int gated;          // A's rows M .. 2 M - 1 are u's features, those before g's
   void* out;          // product: [R, M]; dweight: [E, M, N]
   void* saved;        // gated: [R, 2 M] or null
@@ -196,20 +199,20 @@ __device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* 
     expert_rows(A, T.expert, first, count);
     T.k0 = first, T.depth = count;
   } else {
-    int lo = 0, hi = A.E;  // cum[lo] * mt <= t < cum[hi] * mt
+    // a panel's row tiles take turns at each of the features' tiles
+    const int64_t panel = t / (A.panel * mt), rest = t - panel * (A.panel * mt);
+    const int64_t q0 = panel * A.panel;
+    const int64_t pn = cum[A.E] - q0 < A.panel ? cum[A.E] - q0 : A.panel;
+    m = rest / pn;
+    const int q = (int)(q0 + rest - m * pn);
+    int lo = 0, hi = A.E;  // cum[lo] <= q < cum[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (cum[mid] * mt <= t) lo = mid; else hi = mid;
+      if (cum[mid] <= q) lo = mid; else hi = mid;
     }
     T.expert = lo;
     expert_rows(A, lo, first, count);
-    const int64_t local = t - cum[lo] * mt;
-    const int nt = cum[lo + 1] - cum[lo];
-    const int panel = (int)(local / (kPanel * mt));
-    const int pn = nt - panel * kPanel < kPanel ? nt - panel * kPanel : kPanel;
-    const int64_t rest = local - panel * (kPanel * mt);
-    m = rest / pn;
-    const int j = panel * kPanel + (int)(rest - m * pn);
+    const int nt = cum[lo + 1] - cum[lo], j = q - cum[lo];
     // the expert's tiles are of like size, so that none of them is nearly empty
     const int size = round_rows<kCtas>((count + nt - 1) / nt);
     T.n0 = first + j * size;
@@ -1110,37 +1113,67 @@ hcmix_status resident_clusters(int* clusters) {
   return HCMIX_OK;
 }
 
+// The tiles that a call's clusters have to expect: the experts' rows are known on the device
+// only, and are taken to be shared out evenly.
 template <int kCtas, ProductMode kMode>
-hcmix_status launch_product(const ProductArgs& A, cudaStream_t stream) {
-  int most = 0;
-  const hcmix_status st = resident_clusters<kCtas, kMode>(&most);
-  if (st != HCMIX_OK) return st;
+int64_t expected_tiles(const ProductArgs& A) {
+  const int width = tile_width<kCtas>(A);
+  const int64_t mt = (A.M + width - 1) / width;
+  if (kMode == ProductMode::kWeight) return A.E * mt * ((A.N + kTileN - 1) / kTileN);
+  const int64_t some = A.R < A.E ? A.R : A.E;
+  return mt * some * ((A.R / (some > 0 ? some : 1) + kTileN - 1) / kTileN);
+}
+
+template <int kCtas, ProductMode kMode>
+hcmix_status launch_product(const ProductArgs& A, int clusters, cudaStream_t stream) {
   const int width = tile_width<kCtas>(A);
   const int64_t mt = (A.M + width - 1) / width;
   const int64_t tiles = kMode == ProductMode::kWeight
                             ? A.E * mt * ((A.N + kTileN - 1) / kTileN)
                             : mt * (A.R / kTileN + (A.R < A.E ? A.R : A.E));
-  const int64_t grid = tiles < most ? (tiles > 0 ? tiles : 1) : most;
+  const int64_t grid = tiles < clusters ? (tiles > 0 ? tiles : 1) : clusters;
   return launch(hcmix_product_kernel<kCtas, kMode>, dim3((unsigned)grid * kCtas),
                 dim3(kProductThreads(kCtas, kMode)), product_smem<kCtas, kMode>(A.E),
                 product_smem<kCtas, kMode>(kProductExperts), stream, A, kCtas);
 }
 
-// a, b, offsets, R, E, M, N, K, gated, out, saved and types are set.
+// Clusters of four blocks read the rows once for two pairs: a full tile takes them 0.87 of the
+// time (16384 rows 5120 -> 5120: 431 us, pairs 469 us; 8 experts of 4096 rows 2048 -> 5120: 370 us
+// and 399 us), though the device runs 36 of them on 144 of its 152 multiprocessors.  Their
+// tiles are twice as wide, so that a call of few tiles may take more rounds of them
+// (19456 rows 5120 -> 512: 84 us, pairs 69 us).  dweight: 0.92 (16384 rows: 483 us, pairs 522 us);
+// with few rows an expert its stores count, and pairs do as well.
+template <ProductMode kMode>
+hcmix_status launch_clusters(const ProductArgs& A, cudaStream_t stream) {
+  int twos = 0, fours = 0;
+  hcmix_status st = resident_clusters<2, kMode>(&twos);
+  if (st == HCMIX_OK) st = resident_clusters<4, kMode>(&fours);
+  if (st != HCMIX_OK) return st;
+  constexpr int kPercent = kMode == ProductMode::kWeight ? 92 : 87;
+  const int64_t by_two = (expected_tiles<2, kMode>(A) + twos - 1) / twos;
+  const int64_t by_four = (expected_tiles<4, kMode>(A) + fours - 1) / fours;
+  return by_four * kPercent <= by_two * 100 ? launch_product<4, kMode>(A, fours, stream)
+                                            : launch_product<2, kMode>(A, twos, stream);
+}
+
+// a, b, offsets, R, E, M, N, K, gated, out and types are set.
 template <ProductMode kMode>
 hcmix_status run_product(ProductArgs& A, cudaStream_t stream) {
   if (kMode == ProductMode::kWeight)
     A.vec = make_out_map(A);
   else
     A.vec = vector_bytes(2, {{A.out, A.M}, {A.saved, A.M}}) == 16;
+  A.panel = panel_tiles(A.K);
   const int experts = kMode == ProductMode::kWeight ? 0 : A.E;  // 0: a is a matrix as b is
   // a box starts on 16 bytes: u's features, too, where they lie along the rows
   const bool starts = kMode != ProductMode::kRowsM || !A.gated || A.M % 8 == 0;
   if (A.R > 0 && starts && tma_readable(A.a, experts) && tma_readable(A.b, 0) &&
       make_box_map(&A.a_map, A.a, experts, A.f16, 64) &&
       make_box_map(&A.b_map, A.b, 0, A.f16, 64) && make_box_map(&A.b16_map, A.b, 0, A.f16, 16))
-    return launch_product<QUAD ? 4 : 2, kMode>(A, stream);
-  return launch_product<1, kMode>(A, stream);
+    return launch_clusters<kMode>(A, stream);
+  int ones = 0;
+  const hcmix_status st = resident_clusters<1, kMode>(&ones);
+  return st == HCMIX_OK ? launch_product<1, kMode>(A, ones, stream) : st;
 }
 
 }  // namespace sublayer
