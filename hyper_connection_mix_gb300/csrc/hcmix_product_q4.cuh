@@ -1,12 +1,16 @@
 // Products of few rows with experts' weights of 4 bits: w = (code - 8) scale, a scale for
 // each group of 32 to 256 along k.  Bound by reading the codes of the experts that have rows.
 //
-// A warp takes 16 features of W (16 of g and of u where the product is gated) and 8 rows
-// as mma.m16n8k16 tiles, features as M.  The order of k within a tile is free as long as
-// both operands have it: a thread's word of 8 codes of one feature, k = 8 t .. 8 t + 7 of a
-// block of 32, gives its registers of two tiles, and one 16-byte load of a row the same k.
-// A code becomes 1 + code / 16 by two bit operations; 1.5 taken off (exact), it is
-// (code - 8) / 16.  Sums of a group are fp32, and are scaled and added in fp32.
+// A block of eight warps takes units of 32 features (16 of g and the same 16 of u where the
+// product is gated) and 8 kTiles rows, one after the other from a range of its own; its warps
+// share out a unit's k in chunks of 128, and add their sums in shared memory.  Codes come ahead
+// through a ring of chunks of each warp's own (cp.async), without regard to the units' ends.
+//
+// The products are mma.m16n8k16, features as M.  The order of k within a tile is free as long
+// as both operands have it: a lane's word of 8 codes of one feature, k = 8 t .. 8 t + 7 of a
+// block of 32, gives its registers of two tiles, and one 16-byte load of a row the same k.  A
+// code's bits under 128's (bf16) or 1024's (fp16) exponent are 128 + code, and less 136 they are
+// code - 8, exactly.  Sums of a group are fp32, and are scaled and added in fp32.
 #pragma once
 
 #include "hcmix_vec.cuh"
@@ -30,12 +34,12 @@ template <typename T>
 struct Codes;
 template <>
 struct Codes<__nv_bfloat16> {
-  // codes i and i + 4 of a word, as bits 3..6 of 1.0's fraction
+  using Pair = __nv_bfloat162;
+  // codes i and i + 4 of a word, less 8
   static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
-    const uint32_t s = i == 0 ? w << 3 : w >> (4 * i - 3);
-    uint32_t v = (s & 0x00780078u) | 0x3F803F80u;
-    __nv_bfloat162 h = *reinterpret_cast<__nv_bfloat162*>(&v);
-    h = __hsub2(h, __nv_bfloat162(__ushort_as_bfloat16(0x3FC0), __ushort_as_bfloat16(0x3FC0)));
+    uint32_t v = (w >> 4 * i & 0x000F000Fu) | 0x43004300u;
+    const uint32_t c = 0x43084308u;  // 136
+    Pair h = __hsub2(*reinterpret_cast<Pair*>(&v), *reinterpret_cast<const Pair*>(&c));
     return *reinterpret_cast<uint32_t*>(&h);
   }
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -49,11 +53,17 @@ struct Codes<__nv_bfloat16> {
 };
 template <>
 struct Codes<__half> {
+  using Pair = __half2;
+  // the odd i need no shift: 1024 + 16 code, over 16 and less 72
   static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
-    const uint32_t s = i < 2 ? w << (6 - 4 * i) : w >> (4 * i - 6);
-    uint32_t v = (s & 0x03C003C0u) | 0x3C003C00u;
-    __half2 h = *reinterpret_cast<__half2*>(&v);
-    h = __hsub2(h, __half2(__ushort_as_half(0x3E00), __ushort_as_half(0x3E00)));
+    const uint32_t s = i < 2 ? w : w >> 8;
+    uint32_t v = (s & (i % 2 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+    Pair h = *reinterpret_cast<Pair*>(&v);
+    const uint32_t less = 0x64086408u, over = 0x2C002C00u, base = 0xD480D480u;  // 1032, 1/16, -72
+    if (i % 2)
+      h = __hfma2(h, *reinterpret_cast<const Pair*>(&over), *reinterpret_cast<const Pair*>(&base));
+    else
+      h = __hsub2(h, *reinterpret_cast<const Pair*>(&less));
     return *reinterpret_cast<uint32_t*>(&h);
   }
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -66,112 +76,308 @@ struct Codes<__half> {
   }
 };
 
-constexpr int kQ4Warps = 4;  // they share out k
+constexpr int kQ4Warps = 8, kQ4Chunk = 128, kQ4Depth = 5;
+constexpr int kQ4Box = 32 * kQ4Chunk / 2;  // bytes of a chunk: 32 features
+
+// A unit's place: experts in turn, blocks of their rows in turn, features in turn.
+struct Q4Place {
+  int e, row, end, f;  // the expert, the block's first row, the expert's last + 1, the feature
+};
 
 __device__ __forceinline__ int q4_offset(int v, int64_t R) {
   return v < 0 ? 0 : v > R ? (int)R : v;
 }
 
-template <typename T, bool kGated>
-__global__ void __launch_bounds__(kQ4Warps * 32) hcmix_product_q4_kernel(const Q4Args A) {
-  begin_kernel();
-  constexpr int kHalves = kGated ? 2 : 1;
-  __shared__ float part[kQ4Warps][kHalves][4][32];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const int F = kGated ? A.N / 2 : A.N;
-  const int64_t ft = (F + 15) / 16, tiles = ft * A.E;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int e = (int)(tile / ft), f0 = (int)(tile - e * ft) * 16;
+template <int kRows>
+struct Q4Plan {
+  const Q4Args& A;
+  int features;  // outputs
+  int per;       // of a unit
+  int across;    // units side by side
+
+  __device__ __forceinline__ Q4Plan(const Q4Args& a)
+      : A(a), features(a.gated ? a.N / 2 : a.N), per(a.gated ? 16 : 32) {
+    across = (features + per - 1) / per;
+  }
+  __device__ __forceinline__ int blocks(int e) const {
     const int first = q4_offset(A.offsets[e], A.R), last = q4_offset(A.offsets[e + 1], A.R);
-    for (int r0 = first; r0 < last; r0 += 8) {
-      const T* x = static_cast<const T*>(A.xs) + (int64_t)(r0 + g) * A.xs_stride;
-      const bool has = r0 + g < last;
-      float total[kHalves][4] = {};
-      const int groups = A.K / A.group;
-      for (int q = warp; q < groups; q += kQ4Warps) {
-        float acc[kHalves][4] = {};
-        for (int k = q * A.group; k < (q + 1) * A.group; k += 32) {
-          uint32_t xw[4] = {};
-          const T* xk = x + k + 8 * t;
-          if (has) {
-            if (A.vec) {
-              const uint4 v = *reinterpret_cast<const uint4*>(xk);
-              xw[0] = v.x, xw[1] = v.y, xw[2] = v.z, xw[3] = v.w;
-            } else {
-              const uint16_t* p = reinterpret_cast<const uint16_t*>(xk);
+    return last > first ? (last - first + kRows - 1) / kRows : 0;
+  }
+  // The first block of rows of expert e, or of the next one that has rows.
+  __device__ __forceinline__ void enter(Q4Place& p, int e) const {
+    for (p.e = e; p.e < A.E; ++p.e) {
+      p.row = q4_offset(A.offsets[p.e], A.R);
+      p.end = q4_offset(A.offsets[p.e + 1], A.R);
+      if (p.end > p.row) break;
+    }
+    p.f = 0;
+  }
+  __device__ __forceinline__ void next(Q4Place& p) const {
+    p.f += per;
+    if (p.f < features) return;
+    p.f = 0;
+    p.row += kRows;
+    if (p.row >= p.end) enter(p, p.e + 1);
+  }
+};
+
+template <typename T, int kTiles>
+struct Q4Operands {  // of a chunk: rows' k and features' scales, as a lane holds them
+  uint4 x[kTiles][4];
+  T scale[4];  // rows g and g + 8 of both tiles of features, block t's
+};
+
+template <typename T, int kTiles, bool kGated>
+__global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 2 : 1)
+    hcmix_product_q4_kernel(const Q4Args A) {
+  begin_kernel();
+  constexpr int kRows = 8 * kTiles;
+  extern __shared__ __align__(16) uint8_t q4_shared[];
+  __shared__ int sums[kQ4Warps], start_of[4];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
+  const uint32_t ring =
+      (uint32_t)__cvta_generic_to_shared(q4_shared) + warp * (kQ4Depth * kQ4Box);
+  float* parts = reinterpret_cast<float*>(q4_shared + kQ4Warps * kQ4Depth * kQ4Box);
+  const Q4Plan<kRows> plan(A);
+
+  // ---- the block's range of units, and the place where it begins
+  const int each = (A.E + kQ4Warps * 32 - 1) / (kQ4Warps * 32);
+  const int e0 = tid * each < A.E ? tid * each : A.E, e1 = e0 + each < A.E ? e0 + each : A.E;
+  int here = 0;
+  for (int e = e0; e < e1; ++e) here += plan.blocks(e);
+  int upto = here;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) xw[i] = p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int s = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += s;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int all = 0;
+  for (int w = 0; w < kQ4Warps; ++w) {
+    if (w < warp) upto += sums[w];
+    all += sums[w];
+  }
+  const int64_t units = (int64_t)all * plan.across;
+  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  const int block0 = (int)(u0 / plan.across);
+  if (u0 < u1 && block0 >= upto - here && block0 < upto) {
+    int left = block0 - (upto - here), e = e0;
+    for (; left >= plan.blocks(e); ++e) left -= plan.blocks(e);
+    start_of[0] = e;
+    start_of[1] = q4_offset(A.offsets[e], A.R) + left * kRows;
+    start_of[2] = q4_offset(A.offsets[e + 1], A.R);
+    start_of[3] = (int)(u0 - (int64_t)block0 * plan.across) * plan.per;
+  }
+  __syncthreads();
+  const int chunks = (A.K + kQ4Chunk - 1) / kQ4Chunk;
+  const int turns = (chunks + kQ4Warps - 1) / kQ4Warps;  // of a warp at a unit
+  const int64_t steps = (u1 - u0) * turns;
+  const int groups = A.K / A.group;
+  const T* scales = static_cast<const T*>(A.scales);
+
+  if (steps > 0) {
+    const Q4Place start = {start_of[0], start_of[1], start_of[2], start_of[3]};
+    // Feature r of a unit's 32, clamped to those that there are.
+    const auto feature = [&](const Q4Place& p, int r) {
+      const int f = kGated ? p.f + r % 16 : p.f + r;
+      const int in = f < plan.features ? f : plan.features - 1;
+      return (int64_t)p.e * A.N + (kGated && r >= 16 ? plan.features + in : in);
+    };
+    // ---- codes of one chunk into a box of the ring: feature r's 64 bytes are four blocks of
+    // 16, exchanged so that eight features' words of a block lie in different banks
+    Q4Place ahead = start;
+    int ahead_turn = 0;
+    int64_t sent = 0;
+    const auto send = [&]() {
+      if (sent < steps) {
+        const int k = (warp + ahead_turn * kQ4Warps) * kQ4Chunk;
+        const uint32_t box = ring + (int)(sent % kQ4Depth) * kQ4Box;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + g;
+          if (k + 32 * t < A.K)
+            asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(
+                             box + r * 64 + ((t ^ (r >> 1 & 3)) << 4)),
+                         "l"(A.codes + feature(ahead, r) * (A.K / 2) + k / 2 + 16 * t)
+                         : "memory");
+        }
+        if (++ahead_turn == turns) {
+          ahead_turn = 0;
+          plan.next(ahead);
+        }
+        ++sent;
+      }
+      async_commit();
+    };
+    // ---- rows and scales of one chunk into registers
+    Q4Place near = start;
+    int near_turn = 0;
+    int64_t loaded = 0;
+    const auto load = [&](Q4Operands<T, kTiles>& o) {
+      if (loaded >= steps) return;
+      const int k = (warp + near_turn * kQ4Warps) * kQ4Chunk;
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) {
+        const int row = near.row + 8 * n + g;
+        const T* x = static_cast<const T*>(A.xs) + row * A.xs_stride + k + 8 * t;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (row < near.end && k + 32 * b < A.K) {
+            if (A.vec) {
+              v = *reinterpret_cast<const uint4*>(x + 32 * b);
+            } else {
+              const uint16_t* p = reinterpret_cast<const uint16_t*>(x + 32 * b);
+              v.x = p[0] | (uint32_t)p[1] << 16, v.y = p[2] | (uint32_t)p[3] << 16;
+              v.z = p[4] | (uint32_t)p[5] << 16, v.w = p[6] | (uint32_t)p[7] << 16;
             }
           }
+          o.x[n][b] = v;
+        }
+      }
+      const int q = (k + 32 * t) / A.group;
 #pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            uint32_t w[2];
+      for (int i = 0; i < 4; ++i)
+        o.scale[i] = scales[feature(near, 8 * i + g) * groups + (q < groups ? q : groups - 1)];
+      if (++near_turn == turns) {
+        near_turn = 0;
+        plan.next(near);
+      }
+      ++loaded;
+    };
+
+    Q4Operands<T, kTiles> now, then;
+    for (int i = 0; i < kQ4Depth - 1; ++i) send();
+    load(now);
+    Q4Place at = start;
+    const bool per_block = A.group == 32, per_two = A.group == 64;
+    float total[2][kTiles][4];
+    int turn = 0, buf = 0;
+    for (int64_t step = 0; step < steps; ++step) {
+      send();
+      load(then);
+      if (turn == 0) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              int f = f0 + g + 8 * i;
-              f = (f < F ? f : F - 1) + h * F;
-              w[i] = *reinterpret_cast<const uint32_t*>(
-                  A.codes + ((int64_t)e * A.N + f) * (A.K / 2) + k / 2 + 4 * t);
-            }
+        for (int i = 0; i < 2 * kTiles * 4; ++i) (&total[0][0][0])[i] = 0.0f;
+      }
+      async_wait<kQ4Depth - 1>();
+      __syncwarp();
+      const int k = (warp + turn * kQ4Warps) * kQ4Chunk;
+      const uint32_t box = ring + (int)(step % kQ4Depth) * kQ4Box;
+      float acc[2][kTiles][4] = {};
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const uint32_t a[4] = {Codes<T>::pair(w[0], 2 * s), Codes<T>::pair(w[1], 2 * s),
-                                     Codes<T>::pair(w[0], 2 * s + 1),
-                                     Codes<T>::pair(w[1], 2 * s + 1)};
-              Codes<T>::mma(acc[h], a, __byte_perm(xw[s], xw[s + 2], 0x5410),
-                            __byte_perm(xw[s], xw[s + 2], 0x7632));
-            }
+      for (int b = 0; b < 4; ++b) {
+        if (k + 32 * b >= A.K) break;
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("ld.shared.u32 %0, [%1];"
+                       : "=r"(w[i])
+                       : "r"(box + (8 * i + g) * 64 + ((b ^ (g >> 1 & 3)) << 4) + 4 * t)
+                       : "memory");
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            a[h][0] = Codes<T>::pair(w[2 * h], 2 * s), a[h][1] = Codes<T>::pair(w[2 * h + 1], 2 * s);
+            a[h][2] = Codes<T>::pair(w[2 * h], 2 * s + 1);
+            a[h][3] = Codes<T>::pair(w[2 * h + 1], 2 * s + 1);
+          }
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n) {
+            const uint4& x = now.x[n][b];
+            const uint32_t lo = s ? x.y : x.x, hi = s ? x.w : x.z;
+            const uint32_t b0 = __byte_perm(lo, hi, 0x5410), b1 = __byte_perm(lo, hi, 0x7632);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) Codes<T>::mma(acc[h][n], a[h], b0, b1);
           }
         }
+        if (b == 3 || k + 32 * (b + 1) >= A.K || per_block || (per_two && b == 1)) {
+          // a group ends, or the chunk
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            int f = f0 + g + 8 * i;
-            f = (f < F ? f : F - 1) + h * F;
-            const float s = 16.0f * to_f32(static_cast<const T*>(
-                                        A.scales)[((int64_t)e * A.N + f) * groups + q]);
-            total[h][2 * i] = fmaf(s, acc[h][2 * i], total[h][2 * i]);
-            total[h][2 * i + 1] = fmaf(s, acc[h][2 * i + 1], total[h][2 * i + 1]);
-          }
+            for (int i = 0; i < 2; ++i) {
+              const float s =
+                  __shfl_sync(0xffffffffu, to_f32(now.scale[2 * h + i]), (lane & ~3) | b);
+#pragma unroll
+              for (int n = 0; n < kTiles; ++n) {
+                total[h][n][2 * i] = fmaf(s, acc[h][n][2 * i], total[h][n][2 * i]);
+                total[h][n][2 * i + 1] = fmaf(s, acc[h][n][2 * i + 1], total[h][n][2 * i + 1]);
+                acc[h][n][2 * i] = acc[h][n][2 * i + 1] = 0.0f;
+              }
+            }
+        }
       }
+      __syncwarp();
+      now = then;
+      if (++turn < turns) continue;
+      turn = 0;
+      // ---- the warps' sums: value v = (h, n, i) of a lane
+      constexpr int kValues = 2 * kTiles * 4;
+      float* part = parts + buf * (kQ4Warps * kValues * 32);
+      buf ^= 1;  // the next unit's, which no thread writes before all have passed the barrier
+#pragma unroll
+      for (int v = 0; v < kValues; ++v)
+        part[(warp * kValues + v) * 32 + lane] = (&total[0][0][0])[v];
       __syncthreads();
+      constexpr int kOut = kGated ? kValues / 2 : kValues;
+      for (int o = tid; o < kOut * 32; o += kQ4Warps * 32) {
+        const int v = o / 32, h = v / (4 * kTiles), n = v / 4 % kTiles, i = v % 4;
+        const auto sum = [&](int of) {
+          float s = 0.0f;
 #pragma unroll
-      for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[warp][h][i][lane] = total[h][i];
-      __syncthreads();
-      // value i of a lane: feature g + 8 (i / 2), row 2 t + i % 2
-      const int i = warp;
-      static_assert(kQ4Warps == 4, "a warp for each value");
-      float v[kHalves];
-#pragma unroll
-      for (int h = 0; h < kHalves; ++h)
-        v[h] = (part[0][h][i][lane] + part[1][h][i][lane]) +
-               (part[2][h][i][lane] + part[3][h][i][lane]);
-      const int f = f0 + g + 8 * (i / 2), r = r0 + 2 * t + i % 2;
-      if (f < F && r < last) {
-        float o = v[0];
-        if (kGated) o = __fdividef(v[0], 1.0f + __expf(-v[0])) * v[kHalves - 1];
-        static_cast<T*>(A.out)[(int64_t)r * F + f] = from_f32<T>(o);
+          for (int w = 0; w < kQ4Warps; ++w) s += part[(w * kValues + of) * 32 + lane];
+          return s;
+        };
+        // feature g + 8 (i / 2) of the tile, row 2 t + i % 2
+        const int f = at.f + (kGated ? 0 : 16 * h) + g + 8 * (i / 2);
+        const int row = at.row + 8 * n + 2 * t + i % 2;
+        float y = sum(v);
+        if (kGated) y = __fdividef(y, 1.0f + __expf(-y)) * sum(v + 4 * kTiles);
+        if (f < plan.features && row < at.end)
+          static_cast<T*>(A.out)[(int64_t)row * plan.features + f] = from_f32<T>(y);
       }
+      plan.next(at);
     }
   }
+  // rows that no expert has
   const int64_t end = q4_offset(A.offsets[A.E], A.R), step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = end * F + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < A.R * F; i += step)
+  for (int64_t i = end * plan.features + (int64_t)blockIdx.x * blockDim.x + tid;
+       i < A.R * plan.features; i += step)
     static_cast<T*>(A.out)[i] = from_f32<T>(0.0f);
 }
 
+template <int kTiles>
+constexpr size_t kQ4Smem = kQ4Warps * kQ4Depth * kQ4Box + 2 * kQ4Warps * (8 * kTiles) * 32 * 4;
+
+template <typename T, int kTiles>
+hcmix_status launch_product_q4(const Q4Args& A, int sms, cudaStream_t stream) {
+  const int64_t features = A.gated ? A.N / 2 : A.N, per = A.gated ? 16 : 32;
+  // no more blocks than units: row blocks are at most the rows
+  const int64_t most = (features + per - 1) / per * A.R;
+  const int64_t grid = (int64_t)sms * (kTiles == 1 ? 2 : 1);
+  const dim3 blocks((unsigned)(most < grid ? most : grid));
+  const auto go = [&](auto kernel) {
+    return launch(kernel, blocks, dim3(kQ4Warps * 32), kQ4Smem<kTiles>, kQ4Smem<kTiles>, stream, A);
+  };
+  return A.gated ? go(hcmix_product_q4_kernel<T, kTiles, true>)
+                 : go(hcmix_product_q4_kernel<T, kTiles, false>);
+}
+
 inline hcmix_status run_product_q4(const Q4Args& A, hcmix_type type, cudaStream_t stream) {
-  const int64_t F = A.gated ? A.N / 2 : A.N;
-  const int64_t tiles = (F + 15) / 16 * A.E;
-  const dim3 grid((unsigned)(tiles < (1 << 30) ? tiles : (1 << 30)));
+  int dev = 0, sms = 0;
+  hcmix_status st = checked(cudaGetDevice(&dev));
+  if (st == HCMIX_OK)
+    st = checked(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  if (st != HCMIX_OK) return st;
+  // rows of an expert, were they shared out evenly
+  const bool few = A.R <= 8 * (A.R < A.E ? A.R : (int64_t)A.E);
   const auto go = [&](auto z) {
     using T = decltype(z);
-    return A.gated ? launch(hcmix_product_q4_kernel<T, true>, grid, dim3(kQ4Warps * 32), 0, 0,
-                            stream, A)
-                   : launch(hcmix_product_q4_kernel<T, false>, grid, dim3(kQ4Warps * 32), 0, 0,
-                            stream, A);
+    return few ? launch_product_q4<T, 1>(A, sms, stream) : launch_product_q4<T, 4>(A, sms, stream);
   };
   return type == HCMIX_BF16 ? go(__nv_bfloat16{}) : go(__half{});
 }
