@@ -173,35 +173,49 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 2 : 1)
   const int chunks = (A.K + kQ4Chunk - 1) / kQ4Chunk;
   const int turns = (chunks + kQ4Warps - 1) / kQ4Warps;  // of a warp at a unit
   const int64_t steps = (u1 - u0) * turns;
-  const int groups = A.K / A.group;
+  const int shift = 31 - __clz(A.group), groups = A.K >> shift;
   const T* scales = static_cast<const T*>(A.scales);
 
   if (steps > 0) {
     const Q4Place start = {start_of[0], start_of[1], start_of[2], start_of[3]};
-    // Feature r of a unit's 32, clamped to those that there are.
-    const auto feature = [&](const Q4Place& p, int r) {
-      const int f = kGated ? p.f + r % 16 : p.f + r;
-      const int in = f < plan.features ? f : plan.features - 1;
-      return (int64_t)p.e * A.N + (kGated && r >= 16 ? plan.features + in : in);
+    // Feature r of a unit's 32 among its expert's, clamped to those that there are.
+    const int most = plan.features - 1;
+    const auto feature = [&](int f, int r) {
+      const int in = f + (kGated ? r % 16 : r);
+      return (in < most ? in : most) + (kGated && r >= 16 ? plan.features : 0);
     };
     // ---- codes of one chunk into a box of the ring: feature r's 64 bytes are four blocks of
     // 16, exchanged so that eight features' words of a block lie in different banks
     Q4Place ahead = start;
-    int ahead_turn = 0;
+    int ahead_turn = 0, slot = 0;
     int64_t sent = 0;
+    const uint32_t to = ring + g * 64 + ((t ^ (g >> 1 & 3)) << 4);
+    const uint8_t* codes = nullptr;  // of ahead's expert
     const auto send = [&]() {
       if (sent < steps) {
-        const int k = (warp + ahead_turn * kQ4Warps) * kQ4Chunk;
-        const uint32_t box = ring + (int)(sent % kQ4Depth) * kQ4Box;
+        if (ahead_turn == 0) {
+          codes = A.codes + (int64_t)ahead.e * A.N * (A.K / 2) + 16 * t;
+          // the unit's scales will be asked for a chunk ahead only: they are on their way to L2
+          // by then.  32 (16 and 16) neighbouring features' lie side by side.
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * i + g;
-          if (k + 32 * t < A.K)
+          for (int h = 0; h < (kGated ? 2 : 1); ++h) {
+            const int f0 = feature(ahead.f, 16 * h), f1 = feature(ahead.f, 16 * h + plan.per - 1);
+            const T* from = scales + ((int64_t)ahead.e * A.N + f0) * groups;
+            const int n = (f1 - f0 + 1) * groups;
+            for (int i = tid * 64; i < n; i += kQ4Warps * 32 * 64)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+          }
+        }
+        const int k = (warp + ahead_turn * kQ4Warps) * kQ4Chunk;
+        if (k + 32 * t < A.K) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
             asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(
-                             box + r * 64 + ((t ^ (r >> 1 & 3)) << 4)),
-                         "l"(A.codes + feature(ahead, r) * (A.K / 2) + k / 2 + 16 * t)
+                             to + slot * kQ4Box + i * 512),
+                         "l"(codes + (int64_t)feature(ahead.f, 8 * i + g) * (A.K / 2) + k / 2)
                          : "memory");
         }
+        if (++slot == kQ4Depth) slot = 0;
         if (++ahead_turn == turns) {
           ahead_turn = 0;
           plan.next(ahead);
@@ -214,17 +228,23 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 2 : 1)
     Q4Place near = start;
     int near_turn = 0;
     int64_t loaded = 0;
+    const T* of_expert = nullptr;  // scales
+    const T* of_row = nullptr;     // the lane's first row, its k of a chunk's first block
     const auto load = [&](Q4Operands<T, kTiles>& o) {
       if (loaded >= steps) return;
+      if (near_turn == 0) {
+        of_expert = scales + (int64_t)near.e * A.N * groups;
+        of_row = static_cast<const T*>(A.xs) + (near.row + g) * A.xs_stride + 8 * t;
+      }
       const int k = (warp + near_turn * kQ4Warps) * kQ4Chunk;
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
-        const int row = near.row + 8 * n + g;
-        const T* x = static_cast<const T*>(A.xs) + row * A.xs_stride + k + 8 * t;
+        const bool has = near.row + 8 * n + g < near.end;
+        const T* x = of_row + (int64_t)(8 * n) * A.xs_stride + k;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (row < near.end && k + 32 * b < A.K) {
+          if (has && k + 32 * b < A.K) {
             if (A.vec) {
               v = *reinterpret_cast<const uint4*>(x + 32 * b);
             } else {
@@ -236,10 +256,11 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 2 : 1)
           o.x[n][b] = v;
         }
       }
-      const int q = (k + 32 * t) / A.group;
+      int q = (k + 32 * t) >> shift;
+      q = q < groups ? q : groups - 1;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        o.scale[i] = scales[feature(near, 8 * i + g) * groups + (q < groups ? q : groups - 1)];
+        o.scale[i] = of_expert[(int64_t)feature(near.f, 8 * i + g) * groups + q];
       if (++near_turn == turns) {
         near_turn = 0;
         plan.next(near);
@@ -253,7 +274,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 2 : 1)
     Q4Place at = start;
     const bool per_block = A.group == 32, per_two = A.group == 64;
     float total[2][kTiles][4];
-    int turn = 0, buf = 0;
+    int turn = 0, buf = 0, from = 0;
+    const uint32_t words = ring + g * 64 + 4 * t;
     for (int64_t step = 0; step < steps; ++step) {
       send();
       load(then);
@@ -264,7 +286,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 2 : 1)
       async_wait<kQ4Depth - 1>();
       __syncwarp();
       const int k = (warp + turn * kQ4Warps) * kQ4Chunk;
-      const uint32_t box = ring + (int)(step % kQ4Depth) * kQ4Box;
+      const uint32_t box = words + from * kQ4Box;
+      if (++from == kQ4Depth) from = 0;
       float acc[2][kTiles][4] = {};
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
@@ -274,7 +297,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 2 : 1)
         for (int i = 0; i < 4; ++i)
           asm volatile("ld.shared.u32 %0, [%1];"
                        : "=r"(w[i])
-                       : "r"(box + (8 * i + g) * 64 + ((b ^ (g >> 1 & 3)) << 4) + 4 * t)
+                       : "r"(box + i * 512 + ((b ^ (g >> 1 & 3)) << 4))
                        : "memory");
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
