@@ -27,27 +27,31 @@ namespace hcmix {
 namespace sublayer {
 
 constexpr int kProductExperts = 4096;
-constexpr int kTileM = 128, kTileN = 256, kTileK = 64;  // kTileM: of one block
+constexpr int kTileM = 128, kTileK = 64;  // kTileM: of one block
 constexpr int kBoxBytes = 64 * 128;  // 64 rows of 64 16-bit elements
 enum class ProductMode { kRowsK, kRowsM, kWeight };  // A's contiguous index: k, m; dweight
 
 // kCtas, the blocks that work together:
-//   1  operands whose rows do not all start on 16 bytes, by plain loads;
+//   1  operands whose rows do not all start on 16 bytes, by plain loads and tiles of 128 x 128;
 //   2  a pair: tcgen05 cta_group::2 with 256 features, and half of B in each block, so that
 //      a multiprocessor's shared memory takes in and gives out two thirds of what a tile of
 //      128 x 256 would need;
 //   4  two pairs with neighbouring features and the same rows, each of which is read once and
 //      sent to both.
 constexpr int kABytes = kTileM * kTileK * 2;
+__host__ __device__ constexpr int kTileN(int ctas) { return ctas > 1 ? 256 : 128; }
+constexpr int kAccumulator = 256;  // TMEM columns
 __host__ __device__ constexpr int kMmaCtas(int ctas) { return ctas > 1 ? 2 : 1; }
-__host__ __device__ constexpr int kStageBytes(int ctas) { return kABytes + kTileN * kTileK * 2 / kMmaCtas(ctas); }
-__host__ __device__ constexpr int kStages(int ctas) { return ctas > 1 ? 6 : 4; }
+__host__ __device__ constexpr int kStageBytes(int ctas) {
+  return kABytes + kTileN(ctas) * kTileK * 2 / kMmaCtas(ctas);
+}
+__host__ __device__ constexpr int kStages(int ctas) { return ctas > 1 ? 6 : 2; }
 constexpr int kMostStages = 6;
 // Row tiles of a panel, whose rows are read again for each of the features' tiles: few enough to
 // stay in L2 (32 experts of 512 rows 5120 -> 4096: panels of 20 MB 409 us, 40 MB 424, 80 MB 455).
 constexpr int64_t kPanelBytes = 20 << 20;
 inline int panel_tiles(int64_t K) {
-  const int64_t n = kPanelBytes / (kTileN * K * 2);
+  const int64_t n = kPanelBytes / (kTileN(2) * K * 2);
   return (int)(n < 8 ? 8 : n > 64 ? 64 : n);
 }
 constexpr uint64_t kProductWaitNs = 2000000000ull;
@@ -89,6 +93,21 @@ struct alignas(16) ProductTile {
   int unused;
 };
 
+// Plain loads.  A warp copies 32 rows of 64 elements as the aligned 16-byte blocks that hold
+// them (at the matrix's two ends element by element) into a ring of its own, and when they
+// have come, shifts them into their places in the swizzled stage.
+constexpr int kProducers = 8;  // warps that load: 32 rows of a stage each
+constexpr int kRawDepth = 3, kRawPitch = 144, kRawBox = 32 * kRawPitch;
+__host__ __device__ constexpr int kRawBytes(int ctas) {
+  return ctas > 1 ? 0 : kProducers * kRawDepth * kRawBox;
+}
+struct RawRows {
+  const char* at;  // the first row's first element
+  int64_t pitch;   // bytes
+  int elements;    // of a row; the others are zeros
+  int rows;        // that there are; the others are zeros
+};
+
 constexpr int kQueue = 4;  // tiles told ahead
 struct ProductControl {
   ProductTile tile[kQueue];
@@ -101,6 +120,7 @@ struct ProductControl {
   uint32_t tmem;
   int abort;
   int scan[32];
+  RawRows raw[kProducers][kRawDepth];
 };
 constexpr int kStorers = 8;  // warps that store: two for each 32 lanes of TMEM
 // A storing warp's shared memory: half a chunk of 32 x 32 in fp32 or a rounded one; dweight: a
@@ -112,9 +132,11 @@ __host__ __device__ constexpr int kTurnBytes(ProductMode mode) {
 template <int kCtas, ProductMode kMode>
 constexpr size_t product_smem(int E) {
   return 1024 + (size_t)kStages(kCtas) * kStageBytes(kCtas) +
-         kStorers * kTurnBytes(kMode) + sizeof(ProductControl) + (kMode == ProductMode::kWeight ? 0 : ((size_t)E + 1) * 4);
+         kStorers * kTurnBytes(kMode) + kRawBytes(kCtas) + sizeof(ProductControl) + (kMode == ProductMode::kWeight ? 0 : ((size_t)E + 1) * 4);
 }
 static_assert(product_smem<2, ProductMode::kRowsK>(kProductExperts) <= 227 * 1024 &&
+                  product_smem<1, ProductMode::kRowsK>(kProductExperts) <= 227 * 1024 &&
+                  product_smem<1, ProductMode::kWeight>(kProductExperts) <= 227 * 1024 &&
                   product_smem<2, ProductMode::kWeight>(kProductExperts) <= 227 * 1024,
               "shared memory of a block");
 
@@ -129,6 +151,7 @@ __device__ __forceinline__ void expert_rows(const ProductArgs& A, int e, int& fi
 }
 
 // The number of row tiles of all experts before each, in `cum`.
+template <int kCtas>
 __device__ __forceinline__ void count_tiles(const ProductArgs& A, int* cum, int* scan) {
   const int threads = blockDim.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int per = (A.E + threads - 1) / threads;
@@ -137,7 +160,7 @@ __device__ __forceinline__ void count_tiles(const ProductArgs& A, int* cum, int*
   for (int e = e0; e < e1; ++e) {
     int first, count;
     expert_rows(A, e, first, count);
-    const int tiles = (count + kTileN - 1) / kTileN;
+    const int tiles = (count + kTileN(kCtas) - 1) / kTileN(kCtas);
     cum[e + 1] = tiles;
     sum += tiles;
   }
@@ -176,7 +199,7 @@ template <int kCtas, ProductMode kMode>
 __device__ __forceinline__ int64_t tile_count(const ProductArgs& A, const int* cum) {
   const int width = tile_width<kCtas>(A);
   const int64_t mt = (A.M + width - 1) / width;
-  if (kMode == ProductMode::kWeight) return A.E * mt * ((A.N + kTileN - 1) / kTileN);
+  if (kMode == ProductMode::kWeight) return A.E * mt * ((A.N + kTileN(kCtas) - 1) / kTileN(kCtas));
   return cum[A.E] * mt;
 }
 
@@ -190,12 +213,12 @@ __device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* 
   int64_t m;
   int first, count;
   if (kMode == ProductMode::kWeight) {
-    const int64_t nt = (A.N + kTileN - 1) / kTileN;
+    const int64_t nt = (A.N + kTileN(kCtas) - 1) / kTileN(kCtas);
     T.expert = (int)(t / (mt * nt));
     const int64_t rest = t - T.expert * (mt * nt);
     m = rest / nt;
-    T.n0 = (int)(rest - m * nt) * kTileN;
-    T.n = A.N - T.n0 < kTileN ? A.N - T.n0 : kTileN;
+    T.n0 = (int)(rest - m * nt) * kTileN(kCtas);
+    T.n = A.N - T.n0 < kTileN(kCtas) ? A.N - T.n0 : kTileN(kCtas);
     expert_rows(A, T.expert, first, count);
     T.k0 = first, T.depth = count;
   } else {
@@ -235,25 +258,56 @@ __device__ __forceinline__ int tail_place(int depth) {
   return blocks - 1 < kTailLead ? 0 : blocks - 1 - kTailLead;
 }
 
-// ---- plain loads: 64 x `rows` elements into the swizzled box at `dst`, element by
-// element, zeros outside of the matrix.  For matrices whose rows do not all start on
-// 16 bytes.
-__device__ __forceinline__ void load_box(uint32_t dst, const Matrix3& X, int expert, int64_t inner0,
-                                         int64_t outer0, int64_t outer_end, int rows, int tid,
-                                         int threads) {
-  const uint16_t* base = static_cast<const uint16_t*>(X.p) + expert * X.expert;
-  for (int i = tid; i < rows * 8; i += threads) {
-    const int r = i >> 3, c = i & 7;
-    const int64_t outer = outer0 + r, inner = inner0 + c * 8;
-    uint16_t v[8];
-    const bool row_in = outer < outer_end;
-    const uint16_t* p = base + outer * X.row + inner;
+// ---- plain loads, of matrices whose rows do not all start on 16 bytes.
+
+__device__ __forceinline__ void copy_raw(uint32_t raw, const RawRows& X, const char* low,
+                                         const char* high, int lane) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = row_in && inner + k < X.inner ? p[k] : (uint16_t)0;
-    uint4 w;
-    w.x = v[0] | (uint32_t)v[1] << 16, w.y = v[2] | (uint32_t)v[3] << 16;
-    w.z = v[4] | (uint32_t)v[5] << 16, w.w = v[6] | (uint32_t)v[7] << 16;
-    sm100::sts128(dst + r * 128 + ((c ^ (r & 7)) << 4), w);
+  for (int i = 0; i < 9; ++i) {  // nine blocks hold 128 bytes of any alignment
+    const int at = i * 32 + lane, row = at / 9, block = at - 9 * row;
+    const char* from = X.at + row * X.pitch;
+    const char* p = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(from) & ~(uintptr_t)15) +
+                    16 * block;
+    const uint32_t to = raw + row * kRawPitch + 16 * block;
+    if (row < X.rows && p < from + 2 * X.elements && p + 16 > from) {
+      if (p >= low && p + 16 <= high) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+      } else {
+        for (int k = 0; k < 16; k += 2) {
+          uint16_t v = 0;
+          if (p + k >= low && p + k < high) v = *reinterpret_cast<const uint16_t*>(p + k);
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + k), "h"(v) : "memory");
+        }
+      }
+    } else {
+      sm100::sts128(to, make_uint4(0, 0, 0, 0));
+    }
+  }
+}
+
+__device__ __forceinline__ void place_raw(uint32_t dst, uint32_t raw, const RawRows& X, int lane) {
+  const int c = lane % 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = 4 * i + lane / 8;
+    const uint32_t shift = (uint32_t)reinterpret_cast<uintptr_t>(X.at + row * X.pitch) & 15u;
+    const uint32_t from = raw + row * kRawPitch + 16 * c;
+    const uint4 a = sm100::lds128(from), b = sm100::lds128(from + 16);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = shift & 8 ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = shift & 4 ? w[k + 1] : w[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 8 * (shift & 2));
+    if (X.elements < kTileK) {  // what lies behind a row's end is the next one's
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int left = X.elements - 8 * c - 2 * k;
+        w[k] = left <= 0 ? 0 : left == 1 ? w[k] & 0xffffu : w[k];
+      }
+    }
+    sm100::sts128(dst + row * 128 + ((c ^ (row & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
   }
 }
 
@@ -608,7 +662,6 @@ __device__ __forceinline__ bool barrier_all(uint32_t id, uint32_t count, bool ye
 
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
-constexpr int kProducers = 4;  // warps that load, where loads are plain
 constexpr int kProductThreads(int ctas, ProductMode mode) {
   return (4 + kStorers +
           (ctas == 1 ? kProducers : mode == ProductMode::kWeight ? 1 : 0)) * 32;
@@ -632,8 +685,8 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   const uint32_t stages = (raw + 1023) & ~1023u;
   uint8_t* after = product_shared + (stages - raw) + kDepth * kStageBytes(kCtas);
   float* exchange = reinterpret_cast<float*>(after);
-  ProductControl& C = *reinterpret_cast<ProductControl*>(after + kTurns);
-  int* cum = reinterpret_cast<int*>(after + kTurns + sizeof(ProductControl));
+  ProductControl& C = *reinterpret_cast<ProductControl*>(after + kTurns + kRawBytes(kCtas));
+  int* cum = reinterpret_cast<int*>(&C + 1);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int rank = blockIdx.x % kCtas, half_rank = rank % kMma;
   const bool leader = half_rank == 0;  // of a pair
@@ -661,7 +714,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   // the cluster's barriers are there before its other blocks touch them
   if (kTma) cluster_sync();
   if (warp == 2) product_tmem_alloc<kTma>(smem_u32(&C.tmem));
-  if (!kWeight) count_tiles(A, cum, C.scan);
+  if (!kWeight) count_tiles<kCtas>(A, cum, C.scan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -690,7 +743,58 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   };
   ProductTile T;
 
-  if (kTma ? warp == 0 : warp >= 4 + kStorers) {
+  if (!kTma && warp >= 4 + kStorers) {
+    // ---- plain loads: rows 32 p .. 32 p + 31 of a stage's 128 of A and 128 of B
+    const int p = warp - (4 + kStorers), half = p / 2 % 2;
+    const bool of_a = p < 4, flat = of_a ? kAcross : kWeight;  // flat: rows are k
+    const uint32_t ring = smem_u32(after + kTurns) + p * (kRawDepth * kRawBox);
+    RawRows* slots = C.raw[p];
+    const Matrix3& X = of_a ? A.a : A.b;
+    const int64_t apart = of_a && !kWeight ? X.expert : 0;
+    const char* low = static_cast<const char*>(X.p);
+    const char* high = low + 2 * ((A.E - 1) * apart + (int64_t)(X.outer - 1) * X.row + X.inner);
+    uint32_t copied = 0, placed = 0;
+    int kb = 0, blocks = 0;
+    bool more = true;
+    const auto copy = [&]() {
+      while (more && kb == blocks) {
+        more = next(T);
+        kb = 0;
+        blocks = (T.depth + kTileK - 1) / kTileK;
+      }
+      if (more) {
+        const int k = T.k0 + kb++ * kTileK;
+        const int first = of_a ? (half ? T.m1 : T.m0) : T.n0 + 64 * half;  // feature or row
+        const int inner = flat ? first : k, outer = (flat ? k : first) + 32 * (p % 2);
+        const int end = flat ? T.k0 + T.depth : of_a ? X.outer : T.n0 + T.n;
+        RawRows R;
+        R.at = low + 2 * (T.expert * apart + outer * X.row + inner);
+        R.pitch = 2 * X.row;
+        R.elements = X.inner - inner < kTileK ? (X.inner > inner ? X.inner - inner : 0) : kTileK;
+        R.rows = end - outer < 32 ? (end > outer ? end - outer : 0) : 32;
+        const int slot = copied++ % kRawDepth;
+        copy_raw(ring + slot * kRawBox, R, low, high, lane);
+        if (lane == 0) slots[slot] = R;
+      }
+      async_commit();
+    };
+    for (int i = 0; i < kRawDepth - 1; ++i) copy();
+    for (;; ++placed) {
+      copy();
+      if (placed == copied) break;
+      async_wait<kRawDepth - 1>();
+      __syncwarp();
+      const int s = placed % kDepth, slot = placed % kRawDepth;
+      if (placed >= kDepth &&
+          !__all_sync(0xffffffffu, wait(C.empty[s], (placed / kDepth - 1) & 1)))
+        break;
+      place_raw(stages + s * kStageBytes(kCtas) + p * 4096, ring + slot * kRawBox, slots[slot], lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&C.full[s]));
+    }
+    async_wait<0>();
+  } else if (kTma && warp == 0) {
     // ---- producer
     uint32_t it = 0;  // stages filled
     uint32_t full_at = 0, tail_at = 0, tails = 0;  // a bit for each stage: phases, and the last use
@@ -762,26 +866,6 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
             }
           }
           __syncwarp();
-        } else {
-          const int ptid = tid - (4 + kStorers) * 32;
-          constexpr int pthreads = kProducers * 32;
-          const int k_end = T.k0 + T.depth;
-          for (int h = 0; h < 2; ++h) {
-            const int m = h ? T.m1 : T.m0;
-            if (kAcross)
-              load_box(a + h * kBoxBytes, A.a, T.expert, m, k, k_end, 64, ptid, pthreads);
-            else
-              load_box(a + h * kBoxBytes, A.a, T.expert, k, m, A.a.outer, 64, ptid, pthreads);
-          }
-          if (kWeight) {
-            for (int j = 0; j * 64 < n; ++j)
-              load_box(b + j * kBoxBytes, A.b, 0, n0 + j * 64, k, k_end, 64, ptid, pthreads);
-          } else {
-            load_box(b, A.b, 0, k, n0, T.n0 + T.n, n, ptid, pthreads);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&C.full[s]));
         }
       }
     }
@@ -838,7 +922,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       const int buf = acc & 1;
       if (acc >= 2) ok = __all_sync(0xffffffffu, wait(C.acc_empty[buf], (acc / 2 - 1) & 1));
       tc_fence_after();
-      const uint32_t d = tmem + buf * kTileN;
+      const uint32_t d = tmem + buf * kAccumulator;
       const int place = kTma && kWeight ? tail_place(T.depth) : blocks;
       for (int kb = 0; ok && kb < blocks; ++kb) {
         const bool tail = place < blocks && kb == blocks - 1;
@@ -893,7 +977,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       }
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + buf * kTileN;
+      const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + buf * kAccumulator;
       if constexpr (kWeight) {
         const int m0 = T.m0 + w * 32;
         for (int c = 64 * half; c < T.n && m0 < A.M; c += 128) {
@@ -1119,9 +1203,9 @@ template <int kCtas, ProductMode kMode>
 int64_t expected_tiles(const ProductArgs& A) {
   const int width = tile_width<kCtas>(A);
   const int64_t mt = (A.M + width - 1) / width;
-  if (kMode == ProductMode::kWeight) return A.E * mt * ((A.N + kTileN - 1) / kTileN);
+  if (kMode == ProductMode::kWeight) return A.E * mt * ((A.N + kTileN(kCtas) - 1) / kTileN(kCtas));
   const int64_t some = A.R < A.E ? A.R : A.E;
-  return mt * some * ((A.R / (some > 0 ? some : 1) + kTileN - 1) / kTileN);
+  return mt * some * ((A.R / (some > 0 ? some : 1) + kTileN(kCtas) - 1) / kTileN(kCtas));
 }
 
 template <int kCtas, ProductMode kMode>
@@ -1129,8 +1213,8 @@ hcmix_status launch_product(const ProductArgs& A, int clusters, cudaStream_t str
   const int width = tile_width<kCtas>(A);
   const int64_t mt = (A.M + width - 1) / width;
   const int64_t tiles = kMode == ProductMode::kWeight
-                            ? A.E * mt * ((A.N + kTileN - 1) / kTileN)
-                            : mt * (A.R / kTileN + (A.R < A.E ? A.R : A.E));
+                            ? A.E * mt * ((A.N + kTileN(kCtas) - 1) / kTileN(kCtas))
+                            : mt * (A.R / kTileN(kCtas) + (A.R < A.E ? A.R : A.E));
   const int64_t grid = tiles < clusters ? (tiles > 0 ? tiles : 1) : clusters;
   return launch(hcmix_product_kernel<kCtas, kMode>, dim3((unsigned)grid * kCtas),
                 dim3(kProductThreads(kCtas, kMode)), product_smem<kCtas, kMode>(A.E),
