@@ -93,11 +93,11 @@ struct alignas(16) ProductTile {
   int unused;
 };
 
-// Plain loads.  A warp copies 32 rows of 64 elements as the aligned 16-byte blocks that hold
+// Plain loads.  A warp copies 16 rows of 64 elements as the aligned 16-byte blocks that hold
 // them (at the matrix's two ends element by element) into a ring of its own, and when they
 // have come, shifts them into their places in the swizzled stage.
-constexpr int kProducers = 8;  // warps that load: 32 rows of a stage each
-constexpr int kRawDepth = 3, kRawPitch = 144, kRawBox = 32 * kRawPitch;
+constexpr int kRawRows = 16, kProducers = 256 / kRawRows;  // warps: a stage has 256 rows
+constexpr int kRawDepth = 3, kRawPitch = 144, kRawBox = kRawRows * kRawPitch;
 __host__ __device__ constexpr int kRawBytes(int ctas) {
   return ctas > 1 ? 0 : kProducers * kRawDepth * kRawBox;
 }
@@ -122,7 +122,8 @@ struct ProductControl {
   int scan[32];
   RawRows raw[kProducers][kRawDepth];
 };
-constexpr int kStorers = 8;  // warps that store: two for each 32 lanes of TMEM
+// Warps that store: one or two for each 32 lanes of TMEM.
+__host__ __device__ constexpr int kStorers(int ctas) { return ctas > 1 ? 8 : 4; }
 // A storing warp's shared memory: half a chunk of 32 x 32 in fp32 or a rounded one; dweight: a
 // box of 32 rows of 128 bytes.
 __host__ __device__ constexpr int kTurnBytes(ProductMode mode) {
@@ -132,7 +133,7 @@ __host__ __device__ constexpr int kTurnBytes(ProductMode mode) {
 template <int kCtas, ProductMode kMode>
 constexpr size_t product_smem(int E) {
   return 1024 + (size_t)kStages(kCtas) * kStageBytes(kCtas) +
-         kStorers * kTurnBytes(kMode) + kRawBytes(kCtas) + sizeof(ProductControl) + (kMode == ProductMode::kWeight ? 0 : ((size_t)E + 1) * 4);
+         kStorers(kCtas) * kTurnBytes(kMode) + kRawBytes(kCtas) + sizeof(ProductControl) + (kMode == ProductMode::kWeight ? 0 : ((size_t)E + 1) * 4);
 }
 static_assert(product_smem<2, ProductMode::kRowsK>(kProductExperts) <= 227 * 1024 &&
                   product_smem<1, ProductMode::kRowsK>(kProductExperts) <= 227 * 1024 &&
@@ -263,8 +264,9 @@ __device__ __forceinline__ int tail_place(int depth) {
 __device__ __forceinline__ void copy_raw(uint32_t raw, const RawRows& X, const char* low,
                                          const char* high, int lane) {
 #pragma unroll
-  for (int i = 0; i < 9; ++i) {  // nine blocks hold 128 bytes of any alignment
+  for (int i = 0; i * 32 < kRawRows * 9; ++i) {  // nine blocks hold 128 bytes of any alignment
     const int at = i * 32 + lane, row = at / 9, block = at - 9 * row;
+    if (kRawRows * 9 % 32 != 0 && row >= kRawRows) break;
     const char* from = X.at + row * X.pitch;
     const char* p = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(from) & ~(uintptr_t)15) +
                     16 * block;
@@ -285,12 +287,15 @@ __device__ __forceinline__ void copy_raw(uint32_t raw, const RawRows& X, const c
   }
 }
 
+// `dst`: the place of the first row, whose number in its box is a multiple of 8.
 __device__ __forceinline__ void place_raw(uint32_t dst, uint32_t raw, const RawRows& X, int lane) {
   const int c = lane % 8;
+  const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>(X.at), pitch = (uint32_t)X.pitch;
+  const bool whole = X.elements >= kTileK;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < kRawRows / 4; ++i) {
     const int row = 4 * i + lane / 8;
-    const uint32_t shift = (uint32_t)reinterpret_cast<uintptr_t>(X.at + row * X.pitch) & 15u;
+    const uint32_t shift = at + row * pitch;  // its lower four bits
     const uint32_t from = raw + row * kRawPitch + 16 * c;
     const uint4 a = sm100::lds128(from), b = sm100::lds128(from + 16);
     uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -300,7 +305,7 @@ __device__ __forceinline__ void place_raw(uint32_t dst, uint32_t raw, const RawR
     for (int k = 0; k < 5; ++k) w[k] = shift & 4 ? w[k + 1] : w[k];
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 8 * (shift & 2));
-    if (X.elements < kTileK) {  // what lies behind a row's end is the next one's
+    if (!whole) {  // what lies behind a row's end is the next one's
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int left = X.elements - 8 * c - 2 * k;
@@ -663,7 +668,7 @@ __device__ __forceinline__ bool barrier_all(uint32_t id, uint32_t count, bool ye
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 constexpr int kProductThreads(int ctas, ProductMode mode) {
-  return (4 + kStorers +
+  return (4 + kStorers(ctas) +
           (ctas == 1 ? kProducers : mode == ProductMode::kWeight ? 1 : 0)) * 32;
 }
 
@@ -679,7 +684,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   constexpr bool kAcross = kMode != ProductMode::kRowsK;   // A lies with m contiguous
   constexpr bool kWeight = kMode == ProductMode::kWeight;  // and B with n
   constexpr int kMma = kMmaCtas(kCtas), kDepth = kStages(kCtas);
-  constexpr int kTurns = kStorers * kTurnBytes(kMode);
+  constexpr int kStore = kStorers(kCtas), kTurns = kStore * kTurnBytes(kMode);
   extern __shared__ uint8_t product_shared[];
   const uint32_t raw = smem_u32(product_shared);
   const uint32_t stages = (raw + 1023) & ~1023u;
@@ -692,7 +697,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   const bool leader = half_rank == 0;  // of a pair
 
   if (tid == 0) {
-    const int takers = kStorers + (kTma ? 1 : kProducers) + leader + (kTma && kWeight ? 2 : 0);
+    const int takers = kStore + (kTma ? 1 : kProducers) + leader + (kTma && kWeight ? 2 : 0);
     for (int q = 0; q < kQueue; ++q) {
       mbar_init(smem_u32(&C.told[q]), 1);
       mbar_init(smem_u32(&C.taken[q]), takers);
@@ -705,7 +710,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&C.acc_full[b]), 1);
-      mbar_init(smem_u32(&C.acc_empty[b]), kStorers * kMma);
+      mbar_init(smem_u32(&C.acc_empty[b]), kStore * kMma);
     }
     mbar_init(smem_u32(&C.drain), 1);
     C.abort = 0;
@@ -743,10 +748,10 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   };
   ProductTile T;
 
-  if (!kTma && warp >= 4 + kStorers) {
-    // ---- plain loads: rows 32 p .. 32 p + 31 of a stage's 128 of A and 128 of B
-    const int p = warp - (4 + kStorers), half = p / 2 % 2;
-    const bool of_a = p < 4, flat = of_a ? kAcross : kWeight;  // flat: rows are k
+  if (!kTma && warp >= 4 + kStore) {
+    // ---- plain loads: rows 16 p .. 16 p + 15 of a stage's 128 of A and 128 of B
+    const int p = warp - (4 + kStore), half = p / 4 % 2;
+    const bool of_a = p < kProducers / 2, flat = of_a ? kAcross : kWeight;  // flat: rows are k
     const uint32_t ring = smem_u32(after + kTurns) + p * (kRawDepth * kRawBox);
     RawRows* slots = C.raw[p];
     const Matrix3& X = of_a ? A.a : A.b;
@@ -765,13 +770,13 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       if (more) {
         const int k = T.k0 + kb++ * kTileK;
         const int first = of_a ? (half ? T.m1 : T.m0) : T.n0 + 64 * half;  // feature or row
-        const int inner = flat ? first : k, outer = (flat ? k : first) + 32 * (p % 2);
+        const int inner = flat ? first : k, outer = (flat ? k : first) + kRawRows * (p % 4);
         const int end = flat ? T.k0 + T.depth : of_a ? X.outer : T.n0 + T.n;
         RawRows R;
         R.at = low + 2 * (T.expert * apart + outer * X.row + inner);
         R.pitch = 2 * X.row;
         R.elements = X.inner - inner < kTileK ? (X.inner > inner ? X.inner - inner : 0) : kTileK;
-        R.rows = end - outer < 32 ? (end > outer ? end - outer : 0) : 32;
+        R.rows = end - outer < kRawRows ? (end > outer ? end - outer : 0) : kRawRows;
         const int slot = copied++ % kRawDepth;
         copy_raw(ring + slot * kRawBox, R, low, high, lane);
         if (lane == 0) slots[slot] = R;
@@ -788,7 +793,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       if (placed >= kDepth &&
           !__all_sync(0xffffffffu, wait(C.empty[s], (placed / kDepth - 1) & 1)))
         break;
-      place_raw(stages + s * kStageBytes(kCtas) + p * 4096, ring + slot * kRawBox, slots[slot], lane);
+      place_raw(stages + s * kStageBytes(kCtas) + p * (kRawRows * 128), ring + slot * kRawBox, slots[slot], lane);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&C.full[s]));
@@ -879,7 +884,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
           finish(C.full[s], ~(full_at >> s) & 1);
       }
     }
-  } else if (kTma && kWeight && (warp == 3 || warp == 4 + kStorers)) {
+  } else if (kTma && kWeight && (warp == 3 || warp == 4 + kStore)) {
     // ---- the last stage of an expert took rows of the next one along: they count as zeros
     uint32_t it = 0, tail_at = 0, tails = 0;
     bool ok = true;
@@ -953,7 +958,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     // what was issued is done before the block ends
     mma_commit<kTma>(smem_u32(&C.drain), pair);
     finish(C.drain, 0);
-  } else if (warp >= 4 && warp < 4 + kStorers) {
+  } else if (warp >= 4 && warp < 4 + kStore) {
     // ---- epilogue: TMEM lanes 32 * w on, chunks of 32 columns in turn
     const int w = warp % 4, half = (warp - 4) / 4;
     const int bar = 1 + (w & 1) + 2 * half;  // of g's and u's warp
@@ -980,7 +985,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + buf * kAccumulator;
       if constexpr (kWeight) {
         const int m0 = T.m0 + w * 32;
-        for (int c = 64 * half; c < T.n && m0 < A.M; c += 128) {
+        for (int c = 64 * half; c < T.n && m0 < A.M; c += 16 * kStore) {
           if (A.vec) box_free(lane);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -1012,7 +1017,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
         }
       } else {
       const int64_t row = T.n0;
-      for (int c = 32 * half; c < T.n; c += 8 * kStorers) {
+      for (int c = 32 * half; c < T.n; c += 8 * kStore) {
         const int cols = T.n - c < 32 ? T.n - c : 32;
         float v[32];
         if (any)
