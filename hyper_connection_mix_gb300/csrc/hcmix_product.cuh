@@ -54,7 +54,7 @@ inline int panel_tiles(int64_t K) {
   const int64_t n = kPanelBytes / (kTileN(2) * K * 2);
   return (int)(n < 8 ? 8 : n > 64 ? 64 : n);
 }
-constexpr uint64_t kProductWaitNs = 2000000000ull;
+constexpr int64_t kProductWait = 4000000000ll;  // cycles: about two seconds
 
 // One operand as it lies in memory: rows of contiguous elements.
 struct Matrix3 {
@@ -261,15 +261,20 @@ __device__ __forceinline__ int tail_place(int depth) {
 
 // ---- plain loads, of matrices whose rows do not all start on 16 bytes.
 
+__device__ __forceinline__ const char* align16(const char* p) {
+  return reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15);
+}
+
+// The careful copy: no byte outside of low .. high - 1 is read, rows and elements that are not
+// there are zeros.  
 __device__ __forceinline__ void copy_raw(uint32_t raw, const RawRows& X, const char* low,
                                          const char* high, int lane) {
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i * 32 < kRawRows * 9; ++i) {  // nine blocks hold 128 bytes of any alignment
     const int at = i * 32 + lane, row = at / 9, block = at - 9 * row;
     if (kRawRows * 9 % 32 != 0 && row >= kRawRows) break;
     const char* from = X.at + row * X.pitch;
-    const char* p = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(from) & ~(uintptr_t)15) +
-                    16 * block;
+    const char* p = align16(from) + 16 * block;
     const uint32_t to = raw + row * kRawPitch + 16 * block;
     if (row < X.rows && p < from + 2 * X.elements && p + 16 > from) {
       if (p >= low && p + 16 <= high) {
@@ -491,9 +496,13 @@ __device__ __forceinline__ void pair_send_2d(uint32_t dst, const void* map, int 
       : "memory");
 }
 
-// Waits for phase `parity` of a barrier at which threads and copies of both blocks of a
-// pair arrive; false when *abort is set or the time is up.
-__device__ __forceinline__ bool pair_try(uint32_t bar, uint32_t parity) {
+// Waits for phase `parity` of a barrier; false when *abort is set or the time is up.  kOthers:
+// what threads of the pair's other block have written before they arrived is to be seen (an
+// acquire of the cluster's scope, which a wait for copies, MMAs or this block does without).
+// Time is counted in the multiprocessor's cycles, which take far less to read than the clock.
+template <bool kOthers>
+__device__ __forceinline__ bool product_try(uint32_t bar, uint32_t parity) {
+  if (!kOthers) return sm100::mbar_try_wait(bar, parity);
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -504,16 +513,14 @@ __device__ __forceinline__ bool pair_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, const volatile int* abort,
-                                          uint64_t limit_ns) {
-  if (pair_try(bar, parity)) return true;
-  const uint64_t t0 = sm100::global_timer_ns();
+template <bool kOthers = false>
+__device__ __forceinline__ bool product_wait(uint32_t bar, uint32_t parity,
+                                             const volatile int* abort, int64_t cycles) {
+  if (product_try<kOthers>(bar, parity)) return true;
+  const int64_t t0 = clock64();
   for (uint32_t i = 1;; ++i) {
-    if (pair_try(bar, parity)) return true;
-    if ((i & 3u) == 0) {
-      if (*abort) return false;
-      if (sm100::global_timer_ns() - t0 > limit_ns) return false;
-    }
+    if (product_try<kOthers>(bar, parity)) return true;
+    if ((i & 3u) == 0 && (*abort || clock64() - t0 > cycles)) return false;
   }
 }
 
@@ -725,15 +732,17 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   tc_fence_after();
   const uint32_t tmem = C.tmem;
   const volatile int* abort = &C.abort;
-  const auto wait = [&](uint64_t& bar, uint32_t parity) {
-    if (pair_wait(smem_u32(&bar), parity, abort, kProductWaitNs)) return true;
+  const auto gave_up = [&]() {
     record_device_error(&g_product_error, kDevWaitTimeout);
     *reinterpret_cast<volatile int*>(&C.abort) = 1;
     return false;
   };
+  const auto wait = [&](uint64_t& bar, uint32_t parity) {
+    return product_wait(smem_u32(&bar), parity, abort, kProductWait) || gave_up();
+  };
   const auto finish = [&](uint64_t& bar, uint32_t parity) {  // also after an abort
     const int none = 0;
-    pair_wait(smem_u32(&bar), parity, &none, kProductWaitNs / 4);
+    product_wait(smem_u32(&bar), parity, &none, kProductWait / 4);
   };
   // The next tile, by a whole warp; false behind the last, and after an abort.
   uint32_t turns = 0;
@@ -761,25 +770,65 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     uint32_t copied = 0, placed = 0;
     int kb = 0, blocks = 0;
     bool more = true;
+    // A stage's blocks lie `step` bytes behind the one's before, a multiple of 16 either way
+    // (128, or 64 rows of an even number of bytes), so that a tile's addresses are found once.
+    // Rows that are not there are features or rows whose results are not stored, unless they
+    // are k; elements behind a row's end are masked when they are placed.
+    constexpr int kTurnsOfCopy = (kRawRows * 9 + 31) / 32;
+    const char* from[kTurnsOfCopy];
+    RawRows R;
+    int64_t step = 0;
+    bool inside = false;  // all blocks of the tile's rows lie in the matrix
     const auto copy = [&]() {
       while (more && kb == blocks) {
         more = next(T);
         kb = 0;
         blocks = (T.depth + kTileK - 1) / kTileK;
-      }
-      if (more) {
-        const int k = T.k0 + kb++ * kTileK;
         const int first = of_a ? (half ? T.m1 : T.m0) : T.n0 + 64 * half;  // feature or row
-        const int inner = flat ? first : k, outer = (flat ? k : first) + kRawRows * (p % 4);
+        const int inner = flat ? first : T.k0, outer = (flat ? T.k0 : first) + kRawRows * (p % 4);
         const int end = flat ? T.k0 + T.depth : of_a ? X.outer : T.n0 + T.n;
-        RawRows R;
         R.at = low + 2 * (T.expert * apart + outer * X.row + inner);
         R.pitch = 2 * X.row;
-        R.elements = X.inner - inner < kTileK ? (X.inner > inner ? X.inner - inner : 0) : kTileK;
-        R.rows = end - outer < kRawRows ? (end > outer ? end - outer : 0) : kRawRows;
+        R.elements = X.inner - inner;
+        R.rows = end - outer;
+        step = flat ? kTileK * R.pitch : 2 * kTileK;
+        const char* base = align16(R.at);
+        const int rows = flat || R.rows > kRawRows ? kRawRows : R.rows;
+        inside = base >= low &&
+                 R.at + (blocks - 1 - flat) * step + (rows - 1) * R.pitch + kRawPitch <= high;
+#pragma unroll
+        for (int i = 0; i < kTurnsOfCopy; ++i) {
+          const int at = i * 32 + lane, row = at / 9;
+          from[i] = align16(R.at + row * R.pitch) + 16 * (at - 9 * row);
+          if (row >= kRawRows || (!flat && row >= R.rows)) from[i] = nullptr;
+        }
+      }
+      if (more) {
         const int slot = copied++ % kRawDepth;
-        copy_raw(ring + slot * kRawBox, R, low, high, lane);
-        if (lane == 0) slots[slot] = R;
+        const uint32_t raw = ring + slot * kRawBox;
+        if (inside && !(flat && kb == blocks - 1)) {
+          const int64_t off = kb * step;
+#pragma unroll
+          for (int i = 0; i < kTurnsOfCopy; ++i)
+            if (from[i] != nullptr)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                               raw + (i * 32 + lane) * 16),
+                           "l"(from[i] + off)
+                           : "memory");
+        } else {
+          RawRows now = R;
+          now.at += kb * step;
+          if (flat) now.rows -= kb * kTileK;
+          else now.elements -= kb * kTileK;
+          copy_raw(raw, now, low, high, lane);
+        }
+        if (lane == 0) {
+          RawRows& told = slots[slot];
+          told.at = R.at;
+          told.pitch = R.pitch;
+          told.elements = flat ? R.elements : R.elements - kb * kTileK;
+        }
+        ++kb;
       }
       async_commit();
     };
@@ -933,8 +982,10 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
         const bool tail = place < blocks && kb == blocks - 1;
         const int s = (it + (tail ? place : kb < place ? kb : kb + 1)) % kDepth;
         const int left = T.depth - kb * kTileK;
-        ok = __all_sync(0xffffffffu, tail ? wait(C.ready[s], tail_at >> s & 1)
-                                          : wait(C.full[s], full_at >> s & 1));
+        ok = tail ? product_wait<true>(smem_u32(&C.ready[s]), tail_at >> s & 1, abort, kProductWait) ||
+                        gave_up()
+                  : wait(C.full[s], full_at >> s & 1);
+        ok = __all_sync(0xffffffffu, ok);
         (tail ? tail_at : full_at) ^= 1u << s;
         if (!ok) break;
         tc_fence_after();
