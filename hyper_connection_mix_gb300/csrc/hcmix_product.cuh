@@ -301,13 +301,11 @@ __device__ __forceinline__ void place_raw(uint32_t dst, uint32_t raw, const RawR
   for (int i = 0; i < kRawRows / 4; ++i) {
     const int row = 4 * i + lane / 8;
     const uint32_t shift = at + row * pitch;  // its lower four bits
-    const uint32_t from = raw + row * kRawPitch + 16 * c;
-    const uint4 a = sm100::lds128(from), b = sm100::lds128(from + 16);
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const uint32_t from = raw + row * kRawPitch + 16 * c + (shift & 12);
+    uint32_t w[5];
 #pragma unroll
-    for (int k = 0; k < 6; ++k) w[k] = shift & 8 ? w[k + 2] : w[k];
-#pragma unroll
-    for (int k = 0; k < 5; ++k) w[k] = shift & 4 ? w[k + 1] : w[k];
+    for (int k = 0; k < 5; ++k)
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[k]) : "r"(from + 4 * k) : "memory");
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 8 * (shift & 2));
     if (!whole) {  // what lies behind a row's end is the next one's
@@ -610,14 +608,6 @@ __device__ __forceinline__ void store_chunk(const ProductArgs& A, const Turn& tu
   }
 }
 
-// A lane's 32 values as `cols` neighbours of a row, one by one.
-template <typename T>
-__device__ __forceinline__ void store_row(T* to, const float (&v)[32], int cols) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (i < cols) to[i] = from_f32<T>(v[i]);
-}
-
 // A lane's kCount values, 64 bytes, as a half of its row of the warp's box.
 template <typename T, int kCount>
 __device__ __forceinline__ void put_row(uint32_t box, const float (&v)[32], int first, int half,
@@ -632,6 +622,27 @@ __device__ __forceinline__ void put_row(uint32_t box, const float (&v)[32], int 
     p.pack(f);
     sm100::sts128(box + lane * 128 + ((4 * half + b ^ (lane & 7)) << 4),
                   *reinterpret_cast<const uint4*>(&p));
+  }
+}
+
+// Without the tensor memory accelerator: `rows` x `cols` of the chunk, turned by way of the box
+// (fp32) so that a warp's lanes store neighbours.
+template <typename T>
+__device__ __forceinline__ void store_rows(T* to, int64_t stride, uint32_t box, const float (&v)[32],
+                                           int rows, int cols, int lane) {
+  __syncwarp();
+  put_row<float, 16>(box, v, 0, 0, lane);
+  put_row<float, 16>(box, v, 16, 1, lane);
+  __syncwarp();
+  if (lane >= cols) return;
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r, to += stride) {
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];"
+                 : "=f"(f)
+                 : "r"(box + r * 128 + ((lane / 4 ^ (r & 7)) << 4) + lane % 4 * 4)
+                 : "memory");
+    to[lane] = from_f32<T>(f);
   }
 }
 
@@ -778,6 +789,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     const char* from[kTurnsOfCopy];
     RawRows R;
     int64_t step = 0;
+    bool idle = false;
     bool inside = false;  // all blocks of the tile's rows lie in the matrix
     const auto copy = [&]() {
       while (more && kb == blocks) {
@@ -791,6 +803,8 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
         R.pitch = 2 * X.row;
         R.elements = X.inner - inner;
         R.rows = end - outer;
+        // rows of B that nothing is computed from: a tile of few rows
+        idle = !of_a && !flat && R.rows <= 0;
         step = flat ? kTileK * R.pitch : 2 * kTileK;
         const char* base = align16(R.at);
         const int rows = flat || R.rows > kRawRows ? kRawRows : R.rows;
@@ -806,7 +820,8 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       if (more) {
         const int slot = copied++ % kRawDepth;
         const uint32_t raw = ring + slot * kRawBox;
-        if (inside && !(flat && kb == blocks - 1)) {
+        if (idle) {
+        } else if (inside && !(flat && kb == blocks - 1)) {
           const int64_t off = kb * step;
 #pragma unroll
           for (int i = 0; i < kTurnsOfCopy; ++i)
@@ -827,6 +842,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
           told.at = R.at;
           told.pitch = R.pitch;
           told.elements = flat ? R.elements : R.elements - kb * kTileK;
+          told.rows = !idle;
         }
         ++kb;
       }
@@ -842,8 +858,11 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       if (placed >= kDepth &&
           !__all_sync(0xffffffffu, wait(C.empty[s], (placed / kDepth - 1) & 1)))
         break;
-      place_raw(stages + s * kStageBytes(kCtas) + p * (kRawRows * 128), ring + slot * kRawBox, slots[slot], lane);
-      fence_proxy_async_smem();
+      if (slots[slot].rows != 0) {
+        place_raw(stages + s * kStageBytes(kCtas) + p * (kRawRows * 128), ring + slot * kRawBox,
+                  slots[slot], lane);
+        fence_proxy_async_smem();
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&C.full[s]));
     }
@@ -1048,13 +1067,13 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
               clear(v);
             }
             const int n = T.n0 + c + 32 * h, cols = A.N - n < 32 ? A.N - n : 32;
-            const int64_t at = ((int64_t)T.expert * A.M + m0 + lane) * A.N + n;
             if (!A.vec) {
-              if (m0 + lane >= A.M) continue;
+              const int64_t at = ((int64_t)T.expert * A.M + m0) * A.N + n;
+              const int rows = A.M - m0 < 32 ? A.M - m0 : 32;
               if (A.out_f32)
-                store_row(static_cast<float*>(A.out) + at, v, cols);
+                store_rows(static_cast<float*>(A.out) + at, A.N, turn.base, v, rows, cols, lane);
               else
-                store_row(static_cast<T16*>(A.out) + at, v, cols);
+                store_rows(static_cast<T16*>(A.out) + at, A.N, turn.base, v, rows, cols, lane);
             } else if (A.out_f32) {  // a box of 32 columns
               put_row<float, 16>(turn.base, v, 0, 0, lane);
               put_row<float, 16>(turn.base, v, 16, 1, lane);
