@@ -30,17 +30,31 @@ struct Q4Args {
   int vec;    // rows of xs start on 16 bytes
 };
 
+// (w & mask) | base in one operation, which takes one of the two from a register.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t base) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(base));
+  return r;
+}
+__device__ __forceinline__ uint32_t q4_constant(uint32_t v) {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %1;" : "=r"(r) : "r"(v));  // a register, whatever is known of it
+  return r;
+}
+
 template <typename T>
 struct Codes;
 template <>
 struct Codes<__nv_bfloat16> {
-  using Pair = __nv_bfloat162;
-  // codes i and i + 4 of a word, less 8
-  static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
-    uint32_t v = (w >> 4 * i & 0x000F000Fu) | 0x43004300u;
-    const uint32_t c = 0x43084308u;  // 136
-    Pair h = __hsub2(*reinterpret_cast<Pair*>(&v), *reinterpret_cast<const Pair*>(&c));
-    return *reinterpret_cast<uint32_t*>(&h);
+  uint32_t mask = q4_constant(0x000F000Fu), base = q4_constant(0x43004300u);
+  uint32_t one = q4_constant(0x3F803F80u), less = q4_constant(0xC308C308u);  // 1, -136
+  // codes i and i + 4 of a word, less 8 (by an fma: pairs of bf16 have no sum of their own)
+  __device__ __forceinline__ uint32_t pair(uint32_t w, int i) const {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+        : "=r"(r)
+        : "r"(and_or(w >> 4 * i, mask, base)), "r"(one), "r"(less));
+    return r;
   }
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
@@ -53,18 +67,18 @@ struct Codes<__nv_bfloat16> {
 };
 template <>
 struct Codes<__half> {
-  using Pair = __half2;
+  uint32_t even = q4_constant(0x000F000Fu), odd = q4_constant(0x00F000F0u);
+  uint32_t base = q4_constant(0x64006400u), over = q4_constant(0x2C002C00u);
+  uint32_t one = q4_constant(0x3C003C00u), less = q4_constant(0xE408E408u);  // 1, -1032
+  uint32_t less_odd = q4_constant(0xD480D480u);                              // -72
   // the odd i need no shift: 1024 + 16 code, over 16 and less 72
-  static __device__ __forceinline__ uint32_t pair(uint32_t w, int i) {
-    const uint32_t s = i < 2 ? w : w >> 8;
-    uint32_t v = (s & (i % 2 ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
-    Pair h = *reinterpret_cast<Pair*>(&v);
-    const uint32_t less = 0x64086408u, over = 0x2C002C00u, base = 0xD480D480u;  // 1032, 1/16, -72
-    if (i % 2)
-      h = __hfma2(h, *reinterpret_cast<const Pair*>(&over), *reinterpret_cast<const Pair*>(&base));
-    else
-      h = __hsub2(h, *reinterpret_cast<const Pair*>(&less));
-    return *reinterpret_cast<uint32_t*>(&h);
+  __device__ __forceinline__ uint32_t pair(uint32_t w, int i) const {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;"
+        : "=r"(r)
+        : "r"(and_or(i < 2 ? w : w >> 8, i % 2 ? odd : even, base)), "r"(i % 2 ? over : one),
+          "r"(i % 2 ? less_odd : less));
+    return r;
   }
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
@@ -175,6 +189,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 2 : 1)
   const int64_t steps = (u1 - u0) * turns;
   const int shift = 31 - __clz(A.group), groups = A.K >> shift;
   const T* scales = static_cast<const T*>(A.scales);
+  const Codes<T> code;
 
   if (steps > 0) {
     const Q4Place start = {start_of[0], start_of[1], start_of[2], start_of[3]};
@@ -190,11 +205,16 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 2 : 1)
     int ahead_turn = 0, slot = 0;
     int64_t sent = 0;
     const uint32_t to = ring + g * 64 + ((t ^ (g >> 1 & 3)) << 4);
-    const uint8_t* codes = nullptr;  // of ahead's expert
+    // a unit's features 8 on, and its tile of 16 on, where there are all of them
+    const int64_t code_row = A.K / 2, code_tile = (kGated ? plan.features : 16) * code_row;
+    const uint8_t* codes = nullptr;  // the lane's first
+    bool all_codes = false;
     const auto send = [&]() {
       if (sent < steps) {
         if (ahead_turn == 0) {
-          codes = A.codes + (int64_t)ahead.e * A.N * (A.K / 2) + 16 * t;
+          all_codes = ahead.f + plan.per <= plan.features;
+          codes = A.codes + 16 * t +
+                  ((int64_t)ahead.e * A.N + (all_codes ? feature(ahead.f, g) : 0)) * code_row;
           // the unit's scales will be asked for a chunk ahead only: they are on their way to L2
           // by then.  32 (16 and 16) neighbouring features' lie side by side.
 #pragma unroll
@@ -209,11 +229,14 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 2 : 1)
         const int k = (warp + ahead_turn * kQ4Warps) * kQ4Chunk;
         if (k + 32 * t < A.K) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i) {
+            const int64_t off = all_codes ? i % 2 * 8 * code_row + i / 2 * code_tile
+                                          : feature(ahead.f, 8 * i + g) * code_row;
             asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(
                              to + slot * kQ4Box + i * 512),
-                         "l"(codes + (int64_t)feature(ahead.f, 8 * i + g) * (A.K / 2) + k / 2)
+                         "l"(codes + k / 2 + off)
                          : "memory");
+          }
         }
         if (++slot == kQ4Depth) slot = 0;
         if (++ahead_turn == turns) {
@@ -228,39 +251,50 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 2 : 1)
     Q4Place near = start;
     int near_turn = 0;
     int64_t loaded = 0;
-    const T* of_expert = nullptr;  // scales
-    const T* of_row = nullptr;     // the lane's first row, its k of a chunk's first block
+    const int64_t scale_tile = (int64_t)(kGated ? plan.features : 16) * groups;
+    const T* of_unit = nullptr;     // scales of the lane's first feature
+    bool all_scales = false;
+    const T* of_row[kTiles] = {};   // the lane's rows; behind the last the last one's again, whose
+                                    // products are not stored
     const auto load = [&](Q4Operands<T, kTiles>& o) {
       if (loaded >= steps) return;
       if (near_turn == 0) {
-        of_expert = scales + (int64_t)near.e * A.N * groups;
-        of_row = static_cast<const T*>(A.xs) + (near.row + g) * A.xs_stride + 8 * t;
+        all_scales = near.f + plan.per <= plan.features;
+        of_unit = scales + ((int64_t)near.e * A.N + (all_scales ? feature(near.f, g) : 0)) * groups;
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+          const int row = near.row + 8 * n + g;
+          of_row[n] = static_cast<const T*>(A.xs) +
+                      (row < near.end ? row : near.end - 1) * A.xs_stride + 8 * t;
+        }
       }
       const int k = (warp + near_turn * kQ4Warps) * kQ4Chunk;
+      if (A.vec && k + kQ4Chunk <= A.K) {
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) {
-        const bool has = near.row + 8 * n + g < near.end;
-        const T* x = of_row + (int64_t)(8 * n) * A.xs_stride + k;
+        for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (has && k + 32 * b < A.K) {
-            if (A.vec) {
-              v = *reinterpret_cast<const uint4*>(x + 32 * b);
-            } else {
-              const uint16_t* p = reinterpret_cast<const uint16_t*>(x + 32 * b);
-              v.x = p[0] | (uint32_t)p[1] << 16, v.y = p[2] | (uint32_t)p[3] << 16;
-              v.z = p[4] | (uint32_t)p[5] << 16, v.w = p[6] | (uint32_t)p[7] << 16;
-            }
+          for (int b = 0; b < 4; ++b)
+            o.x[n][b] = *reinterpret_cast<const uint4*>(of_row[n] + k + 32 * b);
+      } else {
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            if (k + 32 * b >= A.K) break;
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(of_row[n] + k + 32 * b);
+            uint4& v = o.x[n][b];
+            v.x = p[0] | (uint32_t)p[1] << 16, v.y = p[2] | (uint32_t)p[3] << 16;
+            v.z = p[4] | (uint32_t)p[5] << 16, v.w = p[6] | (uint32_t)p[7] << 16;
           }
-          o.x[n][b] = v;
-        }
       }
       int q = (k + 32 * t) >> shift;
       q = q < groups ? q : groups - 1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o.scale[i] = of_expert[(int64_t)feature(near.f, 8 * i + g) * groups + q];
+      for (int i = 0; i < 4; ++i) {
+        const int64_t off = all_scales ? i % 2 * 8 * groups + i / 2 * scale_tile
+                                       : (int64_t)feature(near.f, 8 * i + g) * groups;
+        o.scale[i] = of_unit[off + q];
+      }
       if (++near_turn == turns) {
         near_turn = 0;
         plan.next(near);
@@ -304,9 +338,9 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 2 : 1)
           uint32_t a[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            a[h][0] = Codes<T>::pair(w[2 * h], 2 * s), a[h][1] = Codes<T>::pair(w[2 * h + 1], 2 * s);
-            a[h][2] = Codes<T>::pair(w[2 * h], 2 * s + 1);
-            a[h][3] = Codes<T>::pair(w[2 * h + 1], 2 * s + 1);
+            a[h][0] = code.pair(w[2 * h], 2 * s), a[h][1] = code.pair(w[2 * h + 1], 2 * s);
+            a[h][2] = code.pair(w[2 * h], 2 * s + 1);
+            a[h][3] = code.pair(w[2 * h + 1], 2 * s + 1);
           }
 #pragma unroll
           for (int n = 0; n < kTiles; ++n) {
