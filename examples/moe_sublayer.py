@@ -2,13 +2,13 @@
 
     python examples/moe_sublayer.py [--rows 256] [--width 512] [--experts 16] [--top 2] [--steps 20]
 
-Every step but the experts' own matrix products runs in the library's kernels:
+Every step but the router's product and choice runs in the library's kernels:
 
     hc_mix_fused            pre, post, comb from the streams x[M, 4 * D]
     hc_mix_collapse_norm    the sublayer's normalised input
     hc_mix_expert_sort      the (token, choice) pairs by expert
     hc_mix_expert_dispatch  the tokens' rows at their experts
-    (experts)               one torch matrix product for each expert
+    hc_mix_expert_product   the rows through their experts' weights
     hc_mix_expert_combine   the weighted rows back at their tokens
     hc_mix_expand           the next streams
 
@@ -26,7 +26,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import torch
 
-from hyper_connection_mix_gb300 import binding, sublayer as sub
+from hyper_connection_mix_gb300 import binding, experts, sublayer as sub
 
 HC = 4
 
@@ -47,13 +47,6 @@ class Sublayer:
         self.weight, self.bias = torch.ones(width, device=device), torch.zeros(width, device=device)
         self.up = rand(experts, width, width, std=width ** -0.5)
 
-    def experts(self, xs, offsets, f):
-        """f(expert, its rows) for every expert that has rows; where they are is read once."""
-        at = offsets.tolist()
-        for e in range(self.n_experts):
-            if at[e] < at[e + 1]:
-                f(e, slice(at[e], at[e + 1]))
-
     def forward(self, x, keep: bool = False):
         """The next streams [M, 4 * width], and with `keep` what backward needs."""
         pre, post, comb = binding.hc_mix_fused(x, self.mix, self.hc_scale, self.hc_base)
@@ -62,12 +55,8 @@ class Sublayer:
         chosen = torch.softmax(scores, 1)
         offsets, slots, _ = sub.hc_mix_expert_sort(ids, self.n_experts)
         xs = sub.hc_mix_expert_dispatch(n, slots, offsets)
-        ys = torch.zeros_like(xs)
-
-        def product(e, rows):
-            ys[rows] = xs[rows] @ self.up[e].to(xs.dtype)
-
-        self.experts(xs, offsets, product)
+        # the weights are kept in fp32 and written for xs @ up: [expert, in, out]
+        ys = experts.hc_mix_expert_product(xs, self.up.to(xs.dtype), offsets, transposed=True)
         y = sub.hc_mix_expert_combine(ys, slots, chosen)
         out = sub.hc_mix_expand(x, y, post, comb)
         return (out, (x, pre, post, comb, h, mean, rstd, n, ids, chosen, offsets, slots, xs, ys, y)
@@ -79,13 +68,9 @@ class Sublayer:
         x, pre, post, comb, h, mean, rstd, n, ids, chosen, offsets, slots, xs, ys, y = kept
         dx, dy, _, _ = sub.hc_mix_expand_backward(dout, x, y, post, comb)
         dys, dchosen = sub.hc_mix_expert_combine_backward(dy, ys, slots, offsets, chosen)
-        dup, dxs = torch.zeros_like(self.up), torch.zeros_like(xs)
-
-        def product(e, rows):
-            dup[e] = xs[rows].float().t() @ dys[rows].float()
-            dxs[rows] = dys[rows] @ self.up[e].to(xs.dtype).t()
-
-        self.experts(xs, offsets, product)
+        dxs, dup = experts.hc_mix_expert_product_backward(dys, xs, self.up.to(xs.dtype), offsets,
+                                                          transposed=True,
+                                                          weight_dtype=torch.float32)
         dscores = chosen * (dchosen - (chosen * dchosen).sum(1, keepdim=True))
         dlogits = torch.zeros(x.shape[0], self.n_experts, device=x.device).scatter_(1, ids, dscores)
         drouter = n.float().t() @ dlogits

@@ -146,7 +146,7 @@ hcmix_status hc_mix_expert_gate_backward(const void* dh, int64_t dh_stride, cons
   HCMIX_TRY(check_matrix(dh, dh_stride, F, size));
   HCMIX_TRY(check_matrix(gu, gu_stride, 2 * F, size));
   HCMIX_TRY(check_matrix(dgu, 2 * F, 2 * F, size));
-  return run_gate_backward(GateArgs{dh, gu, dh_stride, gu_stride, dgu, R, F}, type,
+  return run_gate_backward(GateArgs{dh, gu, dh_stride, gu_stride, dgu, R, F, 0}, type,
                            as_stream(stream));
 }
 
