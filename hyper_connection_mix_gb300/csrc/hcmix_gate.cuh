@@ -17,41 +17,57 @@ struct GateArgs {
   int across;  // log2 of a block's threads along a row
 };
 
-template <typename T, int kVec>
-__device__ __forceinline__ void gate_vector(const GateArgs& A, int64_t r, int64_t f) {
-  using V = Packed<T, kVec>;
-  const T* gu = static_cast<const T*>(A.gu) + r * A.gu_stride + f;
-  float dh[kVec], g[kVec], u[kVec];
-  reinterpret_cast<const V*>(static_cast<const T*>(A.dh) + r * A.dh_stride + f)->unpack(dh);
-  reinterpret_cast<const V*>(gu)->unpack(g);
-  reinterpret_cast<const V*>(gu + A.F)->unpack(u);
-#pragma unroll
-  for (int k = 0; k < kVec; ++k) {
-    const float q = 1.0f / (1.0f + expf(-g[k]));
-    const float s = dh[k] * q;
-    u[k] *= s * (1.0f + g[k] * (1.0f - q));
-    g[k] *= s;
-  }
-  V dg, du;
-  dg.pack(u);
-  du.pack(g);
-  T* out = static_cast<T*>(A.dgu) + r * 2 * A.F + f;
-  *reinterpret_cast<V*>(out) = dg;
-  *reinterpret_cast<V*>(out + A.F) = du;
-}
-
-// A vector a thread.  A block is across x down of them, so that no thread divides by the
-// width: `across` a power of two as large as a row's vectors, at most the block's threads.
+// A block is across x down threads, so that none divides by the width: `across` a power of two
+// as large as a row's vectors, at most the block's threads.  A thread takes kRows rows' vectors at
+// a time, one of 16 bytes or four smaller ones, and loads all of them first.
 constexpr int kGateThreads = 256;
+template <typename T, int kVec>
+constexpr int kGateRows = kVec * sizeof(T) == 16 ? 1 : 4;
+
 template <typename T, int kVec>
 __global__ void __launch_bounds__(kGateThreads) hcmix_gate_backward_kernel(const GateArgs A) {
   begin_kernel();
+  using V = Packed<T, kVec>;
+  constexpr int kRows = kGateRows<T, kVec>;
   const int down = kGateThreads >> A.across;
-  const int64_t f = ((int64_t)blockIdx.x << A.across) + (threadIdx.x & ((1 << A.across) - 1));
-  if (f * kVec >= A.F) return;
-  for (int64_t r = (int64_t)blockIdx.y * down + (threadIdx.x >> A.across); r < A.R;
-       r += (int64_t)gridDim.y * down)
-    gate_vector<T, kVec>(A, r, f * kVec);
+  const int64_t column = ((int64_t)blockIdx.x << A.across) + (threadIdx.x & ((1 << A.across) - 1));
+  const int64_t f = column * kVec;
+  if (f >= A.F) return;
+  for (int64_t r0 = (int64_t)blockIdx.y * kRows * down + (threadIdx.x >> A.across); r0 < A.R;
+       r0 += (int64_t)gridDim.y * kRows * down) {
+    V in[kRows][3];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t r = r0 + i * down;
+      if (r >= A.R) continue;
+      const T* gu = static_cast<const T*>(A.gu) + r * A.gu_stride + f;
+      in[i][0] = *reinterpret_cast<const V*>(static_cast<const T*>(A.dh) + r * A.dh_stride + f);
+      in[i][1] = *reinterpret_cast<const V*>(gu);
+      in[i][2] = *reinterpret_cast<const V*>(gu + A.F);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t r = r0 + i * down;
+      if (r >= A.R) continue;
+      float dh[kVec], g[kVec], u[kVec];
+      in[i][0].unpack(dh);
+      in[i][1].unpack(g);
+      in[i][2].unpack(u);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) {
+        const float q = 1.0f / (1.0f + expf(-g[k]));
+        const float s = dh[k] * q;
+        u[k] *= s * (1.0f + g[k] * (1.0f - q));
+        g[k] *= s;
+      }
+      V dg, du;
+      dg.pack(u);
+      du.pack(g);
+      T* out = static_cast<T*>(A.dgu) + r * 2 * A.F + f;
+      *reinterpret_cast<V*>(out) = dg;
+      *reinterpret_cast<V*>(out + A.F) = du;
+    }
+  }
 }
 
 inline hcmix_status run_gate_backward(GateArgs A, hcmix_type type, cudaStream_t stream) {
@@ -64,7 +80,8 @@ inline hcmix_status run_gate_backward(GateArgs A, hcmix_type type, cudaStream_t 
     const int64_t per = (A.F + kVec - 1) / kVec;
     A.across = 0;
     while ((1 << A.across) < per && (1 << A.across) < kGateThreads) ++A.across;
-    const int64_t down = kGateThreads >> A.across, rows = (A.R + down - 1) / down;
+    const int64_t down = (kGateThreads >> A.across) * kGateRows<decltype(z), kVec>;
+    const int64_t rows = (A.R + down - 1) / down;
     const dim3 grid((unsigned)((per + (1 << A.across) - 1) >> A.across),
                     (unsigned)(rows < 65535 ? rows : 65535));
     return launch(hcmix_gate_backward_kernel<decltype(z), kVec>, grid, dim3(kGateThreads), 0, 0,
