@@ -15,7 +15,8 @@ using namespace hcmix::sublayer;
 
 namespace {
 
-constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
+// a tile's rows behind the last are counted in 32 bits too
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 4096;
 constexpr int64_t kMaxWidth = (int64_t)1 << 24;
 
 #define HCMIX_TRY(expr)                                  \

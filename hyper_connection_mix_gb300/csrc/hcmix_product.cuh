@@ -669,6 +669,17 @@ __device__ __forceinline__ void box_end(int lane) {
   if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// Zeros in elements first .. end - 1, by all threads; vec: both are multiples of 8, and the
+// first element starts on 16 bytes.
+__device__ __forceinline__ void clear_elements(void* out, int64_t first, int64_t end, bool vec,
+                                               int64_t thread, int64_t threads) {
+  if (vec)
+    for (int64_t i = first / 8 + thread; i < end / 8; i += threads)
+      static_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
+  else
+    for (int64_t i = first + thread; i < end; i += threads) static_cast<uint16_t*>(out)[i] = 0;
+}
+
 // Barrier `id` over `count` threads of whole warps, and whether all of them say yes.
 __device__ __forceinline__ bool barrier_all(uint32_t id, uint32_t count, bool yes) {
   uint32_t r;
@@ -1157,13 +1168,10 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   // rows that no expert has
   if (!kWeight) {
     const int64_t end = clamp_offset(A.offsets[A.E], A.R);
-    const int64_t from = (int64_t)blockIdx.x * blockDim.x + tid,
-                  step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = end * A.M + from; i < A.R * A.M; i += step)
-      static_cast<uint16_t*>(A.out)[i] = 0;
-    if (A.saved != nullptr)
-      for (int64_t i = end * 2 * A.M + from; i < A.R * 2 * A.M; i += step)
-        static_cast<uint16_t*>(A.saved)[i] = 0;
+    const int64_t from = (int64_t)blockIdx.x * blockDim.x + tid;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    clear_elements(A.out, end * A.M, A.R * A.M, A.vec, from, step);
+    if (A.saved != nullptr) clear_elements(A.saved, end * 2 * A.M, A.R * 2 * A.M, A.vec, from, step);
   }
   tc_fence_before();
   __syncthreads();
@@ -1305,9 +1313,9 @@ hcmix_status launch_product(const ProductArgs& A, int clusters, cudaStream_t str
 template <ProductMode kMode>
 hcmix_status launch_clusters(const ProductArgs& A, cudaStream_t stream) {
   int twos = 0, fours = 0;
-  hcmix_status st = resident_clusters<2, kMode>(&twos);
-  if (st == HCMIX_OK) st = resident_clusters<4, kMode>(&fours);
+  const hcmix_status st = resident_clusters<2, kMode>(&twos);
   if (st != HCMIX_OK) return st;
+  if (resident_clusters<4, kMode>(&fours) != HCMIX_OK) return launch_product<2, kMode>(A, twos, stream);
   constexpr int kPercent = kMode == ProductMode::kWeight ? 92 : 87;
   const int64_t by_two = (expected_tiles<2, kMode>(A) + twos - 1) / twos;
   const int64_t by_four = (expected_tiles<4, kMode>(A) + fours - 1) / fours;

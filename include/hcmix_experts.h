@@ -21,7 +21,7 @@
  *     is accepted; operands whose rows (and experts) all start on 16 bytes are
  *     copied by the tensor memory accelerator and run fastest.
  *   - offsets[E + 1] is int32, on the device, offsets[0] = 0, not falling, its last
- *     at most R; 1 <= E <= 4096, 0 <= R < 2^31.  Offsets outside 0 .. R are taken as
+ *     at most R; 1 <= E <= 4096, 0 <= R <= 2^31 - 4096.  Offsets outside 0 .. R are taken as
  *     0 or R: no access is out of bounds whatever they hold, but results are then
  *     unspecified.
  *   - Rows from offsets[E] on belong to no expert.  Their results are zero, and what

@@ -45,7 +45,7 @@ def check_matrix_refusals(call, pointer, stride, width):
 
 def check_common(call):
     assert call(R=-1) == INVALID
-    assert call(R=1 << 31) == UNSUPPORTED
+    assert call(R=(1 << 31) - 4095) == UNSUPPORTED
     assert call(type=F32) == UNSUPPORTED
     assert call(type=3) == INVALID
     assert call(type=-1) == INVALID

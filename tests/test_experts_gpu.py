@@ -339,6 +339,22 @@ def test_same_bits_and_graph():
     assert experts.hc_mix_expert_device_status() == 0
 
 
+@pytest.mark.parametrize("K,N", [(64, 40), (33, 7)])
+def test_no_rows_and_rows_of_no_expert(K, N):
+    """No rows at all; and many rows that no expert has, whose results are zero."""
+    w, codes = weights(3, N, K, BF16, False), quantised(3, 40, 64, 32, BF16)
+    for R in (0, 5000):
+        xs, offsets = torch.full((R, K), NAN, dtype=BF16, device="cuda"), offsets_of([0, 0, 0])
+        ys = experts.hc_mix_expert_product(xs, w, offsets)
+        assert ys.shape == (R, N) and not ys.any()
+        h, gu = experts.hc_mix_expert_product_gated(xs, weights(3, 2 * N, K, BF16, False), offsets, want_saved=True)
+        assert h.shape == (R, N) and gu.shape == (R, 2 * N) and not h.any() and not gu.any()
+        dxs, dw = experts.hc_mix_expert_product_backward(torch.full((R, N), NAN, dtype=BF16, device="cuda"), xs, w, offsets)
+        assert dxs.shape == xs.shape and dw.shape == w.shape and not dxs.any() and not dw.any()
+        q = experts.hc_mix_expert_product_q4(torch.full((R, 64), NAN, dtype=BF16, device="cuda"), *codes[:2], offsets)
+        assert q.shape == (R, 40) and not q.any()
+
+
 def test_offsets_out_of_range_are_safe():
     """Unspecified results, but every access within the operands."""
     K, N = 64, 48
