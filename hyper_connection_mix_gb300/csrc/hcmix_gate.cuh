@@ -1,7 +1,8 @@
 // The gate of an expert's feed-forward network, backward: with (g, u) the halves of a
 // row of gu and q = 1 / (1 + exp(-g)),
 //   dg = dh u q (1 + g (1 - q)),  du = dh g q.
-// Elementwise, bound by HBM: dh, g and u are read once, dg and du written once.
+// Elementwise, bound by HBM: dh, g and u are read once, dg and du written once (32768 x 2048 bf16
+// 104 us, 6.4 TB/s; 3001 x 1001 fp32, whose rows are read element by element, 14.2 us).
 #pragma once
 
 #include "hcmix_vec.cuh"

@@ -8,11 +8,22 @@
 //   its dxs            m: width of W[e]         n: rows of dys    k: features
 //   its dweight        m: outer index of dW[e]  n: its inner one  k: rows of the expert
 //
-// With the rows as the MMA's N, which may be any multiple of 16, an expert of few rows
-// costs few columns and not a whole tile of 128.  The products' tiles are turned over in shared
-// memory on their way out; dweight's leave as they are, in boxes of 64 columns.  fp32 accumulation in TMEM over all of k, one rounding at the
-// store.  Blocks are persistent: a producer fills a ring of 64-wide slices of A and B,
-// one thread issues the MMAs, and four warps store a tile while the next is computed.
+// With the rows as the MMA's N, which may be any multiple of 16 (of 32 for a pair of blocks),
+// an expert of few rows costs few columns and not a whole tile of 128.  fp32 accumulation in
+// TMEM over all of k, one rounding at the store.  The products' tiles are turned over in shared
+// memory on their way out; dweight's leave as they are, in boxes by the tensor memory accelerator.
+//
+// Blocks are resident: one warp fills a ring of 64-wide slices of A and B, one issues the MMAs,
+// others store a tile while the next is computed.  What bounds it, measured on one GB300
+// (L2 gives the multiprocessors at most about 15 TB/s together):
+//   many rows   16384 rows 5120 -> 5120 bf16: 431 to 458 us, 1990 to 1870 TFLOP/s; the MMAs
+//               alone 386 us, the copies alone 467 us by pairs, which is why two pairs share rows
+//   some        128 experts of 256 rows 2048 -> 5120: 480 us; the weights' bytes at 6.8 TB/s: 396
+//   one         128 experts of one row: 391 us, 6.9 TB/s
+//   dweight     16384 rows 5120 x 5120: 460 us; 32 experts of 512 rows 5120 x 4096: 467 us, where
+//               the stores meet the copies in L2; 128 experts of one row: 393 us, 6.8 TB/s
+//   plain loads 61 experts of 72 rows 1023 -> 1001 fp16: 86 to 94 us, bound by the instructions
+//               that shift rows into place
 #pragma once
 
 #include <cuda.h>
@@ -28,7 +39,7 @@ namespace sublayer {
 
 constexpr int kProductExperts = 4096;
 constexpr int kTileM = 128, kTileK = 64;  // kTileM: of one block
-constexpr int kBoxBytes = 64 * 128;  // 64 rows of 64 16-bit elements
+constexpr int kBoxBytes = 64 * 128;               // 64 rows of 64 16-bit elements
 enum class ProductMode { kRowsK, kRowsM, kWeight };  // A's contiguous index: k, m; dweight
 
 // kCtas, the blocks that work together:
@@ -79,7 +90,7 @@ struct ProductArgs {
   int vec;            // rows of out (and saved) start on 16 bytes
 };
 
-
+// Set by a wait that was given up, on the device that it happened on.
 static __device__ uint32_t g_product_error;
 
 // A tile, as the scheduling warp tells the others.
@@ -133,7 +144,8 @@ __host__ __device__ constexpr int kTurnBytes(ProductMode mode) {
 template <int kCtas, ProductMode kMode>
 constexpr size_t product_smem(int E) {
   return 1024 + (size_t)kStages(kCtas) * kStageBytes(kCtas) +
-         kStorers(kCtas) * kTurnBytes(kMode) + kRawBytes(kCtas) + sizeof(ProductControl) + (kMode == ProductMode::kWeight ? 0 : ((size_t)E + 1) * 4);
+         kStorers(kCtas) * kTurnBytes(kMode) + kRawBytes(kCtas) + sizeof(ProductControl) +
+         (kMode == ProductMode::kWeight ? 0 : ((size_t)E + 1) * 4);
 }
 static_assert(product_smem<2, ProductMode::kRowsK>(kProductExperts) <= 227 * 1024 &&
                   product_smem<1, ProductMode::kRowsK>(kProductExperts) <= 227 * 1024 &&
@@ -1049,94 +1061,94 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     const float* other = exchange + (half * 4 + (w ^ 2)) * (kTurnBytes(kMode) / 4);
     const Turn turn(smem_u32(mine), lane);
     const auto store_tiles = [&](auto zero) {
-    using T16 = decltype(zero);
-    for (;;) {
-      // g's and u's warps go on together, or both leave
-      bool have = next(T);
-      if (A.gated) have = barrier_all(bar, 64, have);
-      if (!have) break;
-      const int buf = acc & 1;
-      const bool any = T.depth > 0;
-      if (any) {
-        ok = wait(C.acc_full[buf], (acc / 2) & 1);
-        ok = A.gated ? barrier_all(bar, 64, ok) : __all_sync(0xffffffffu, ok);
-      }
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + buf * kAccumulator;
-      if constexpr (kWeight) {
-        const int m0 = T.m0 + w * 32;
-        for (int c = 64 * half; c < T.n && m0 < A.M; c += 16 * kStore) {
-          if (A.vec) box_free(lane);
+      using T16 = decltype(zero);
+      for (;;) {
+        // g's and u's warps go on together, or both leave
+        bool have = next(T);
+        if (A.gated) have = barrier_all(bar, 64, have);
+        if (!have) break;
+        const int buf = acc & 1;
+        const bool any = T.depth > 0;
+        if (any) {
+          ok = wait(C.acc_full[buf], (acc / 2) & 1);
+          ok = A.gated ? barrier_all(bar, 64, ok) : __all_sync(0xffffffffu, ok);
+        }
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + buf * kAccumulator;
+        if constexpr (kWeight) {
+          const int m0 = T.m0 + w * 32;
+          for (int c = 64 * half; c < T.n && m0 < A.M; c += 16 * kStore) {
+            if (A.vec) box_free(lane);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float v[32];
-            if (any) {
-              tmem_ld32(d + c + 32 * h, reinterpret_cast<uint32_t(&)[32]>(v));
-              tmem_wait_ld();
-            } else {
-              clear(v);
-            }
-            const int n = T.n0 + c + 32 * h, cols = A.N - n < 32 ? A.N - n : 32;
-            if (!A.vec) {
-              const int64_t at = ((int64_t)T.expert * A.M + m0) * A.N + n;
-              const int rows = A.M - m0 < 32 ? A.M - m0 : 32;
-              if (A.out_f32)
-                store_rows(static_cast<float*>(A.out) + at, A.N, turn.base, v, rows, cols, lane);
-              else
-                store_rows(static_cast<T16*>(A.out) + at, A.N, turn.base, v, rows, cols, lane);
-            } else if (A.out_f32) {  // a box of 32 columns
-              put_row<float, 16>(turn.base, v, 0, 0, lane);
-              put_row<float, 16>(turn.base, v, 16, 1, lane);
-              if (cols > 0) box_store(&A.out_map, turn.base, n, m0, T.expert, lane);
-              if (h == 0) box_free(lane);
-            } else {
-              put_row<T16, 32>(turn.base, v, 0, h, lane);
-              if (h == 1) box_store(&A.out_map, turn.base, n - 32, m0, T.expert, lane);
+            for (int h = 0; h < 2; ++h) {
+              float v[32];
+              if (any) {
+                tmem_ld32(d + c + 32 * h, reinterpret_cast<uint32_t(&)[32]>(v));
+                tmem_wait_ld();
+              } else {
+                clear(v);
+              }
+              const int n = T.n0 + c + 32 * h, cols = A.N - n < 32 ? A.N - n : 32;
+              if (!A.vec) {
+                const int64_t at = ((int64_t)T.expert * A.M + m0) * A.N + n;
+                const int rows = A.M - m0 < 32 ? A.M - m0 : 32;
+                if (A.out_f32)
+                  store_rows(static_cast<float*>(A.out) + at, A.N, turn.base, v, rows, cols, lane);
+                else
+                  store_rows(static_cast<T16*>(A.out) + at, A.N, turn.base, v, rows, cols, lane);
+              } else if (A.out_f32) {  // a box of 32 columns
+                put_row<float, 16>(turn.base, v, 0, 0, lane);
+                put_row<float, 16>(turn.base, v, 16, 1, lane);
+                if (cols > 0) box_store(&A.out_map, turn.base, n, m0, T.expert, lane);
+                if (h == 0) box_free(lane);
+              } else {
+                put_row<T16, 32>(turn.base, v, 0, h, lane);
+                if (h == 1) box_store(&A.out_map, turn.base, n - 32, m0, T.expert, lane);
+              }
             }
           }
-        }
-      } else {
-      const int64_t row = T.n0;
-      for (int c = 32 * half; c < T.n; c += 8 * kStore) {
-        const int cols = T.n - c < 32 ? T.n - c : 32;
-        float v[32];
-        if (any)
-          tmem_ld_fragments(d + c, v);
-        else
-          clear(v);
-        if (!A.gated) {
-          store_chunk<T16>(A, turn, v, static_cast<uint16_t*>(A.out), A.M, row + c, cols,
-                      T.m0 + w * 32, A.M, lane);
         } else {
-          const int f = T.m0 + (w & 1) * 32;
-          if (A.saved != nullptr)
-            store_chunk<T16>(A, turn, v, static_cast<uint16_t*>(A.saved) + (w < 2 ? 0 : A.M),
-                        2 * (int64_t)A.M, row + c, cols, f, A.M, lane);
-          // g's warps give their upper 16 columns to u's, and get the lower ones of u
-          __syncwarp();
+          const int64_t row = T.n0;
+          for (int c = 32 * half; c < T.n; c += 8 * kStore) {
+            const int cols = T.n - c < 32 ? T.n - c : 32;
+            float v[32];
+            if (any)
+              tmem_ld_fragments(d + c, v);
+            else
+              clear(v);
+            if (!A.gated) {
+              store_chunk<T16>(A, turn, v, static_cast<uint16_t*>(A.out), A.M, row + c, cols,
+                          T.m0 + w * 32, A.M, lane);
+            } else {
+              const int f = T.m0 + (w & 1) * 32;
+              if (A.saved != nullptr)
+                store_chunk<T16>(A, turn, v, static_cast<uint16_t*>(A.saved) + (w < 2 ? 0 : A.M),
+                            2 * (int64_t)A.M, row + c, cols, f, A.M, lane);
+              // g's warps give their upper 16 columns to u's, and get the lower ones of u
+              __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = w < 2 ? v[16 + i] : v[i];
-          named_bar_sync(bar, 64);
+              for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = w < 2 ? v[16 + i] : v[i];
+              named_bar_sync(bar, 64);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float o = other[i * 32 + lane];
-            v[i] = w < 2 ? silu(v[i]) * o : silu(o) * v[16 + i];
+              for (int i = 0; i < 16; ++i) {
+                const float o = other[i * 32 + lane];
+                v[i] = w < 2 ? silu(v[i]) * o : silu(o) * v[16 + i];
+              }
+              named_bar_sync(bar, 64);  // both have read
+              const int c0 = w < 2 ? 0 : 16;
+              store_chunk<T16, 2>(A, turn, reinterpret_cast<float(&)[16]>(v),
+                             static_cast<uint16_t*>(A.out), A.M, row + c + c0, cols - c0, f, A.M, lane);
+            }
           }
-          named_bar_sync(bar, 64);  // both have read
-          const int c0 = w < 2 ? 0 : 16;
-          store_chunk<T16, 2>(A, turn, reinterpret_cast<float(&)[16]>(v),
-                         static_cast<uint16_t*>(A.out), A.M, row + c + c0, cols - c0, f, A.M, lane);
+        }
+        if (any) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_leader_read<kTma>(smem_u32(&C.acc_empty[buf]));
+          ++acc;
         }
       }
-      }
-      if (any) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_leader_read<kTma>(smem_u32(&C.acc_empty[buf]));
-        ++acc;
-      }
-    }
     };
     if (A.f16)
       store_tiles(__half{});
