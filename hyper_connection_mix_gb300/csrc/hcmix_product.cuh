@@ -59,11 +59,12 @@ __host__ __device__ constexpr int kStageBytes(int ctas) {
 __host__ __device__ constexpr int kStages(int ctas) { return ctas > 1 ? 6 : 2; }
 constexpr int kMostStages = 6;
 // Row tiles of a panel, whose rows are read again for each of the features' tiles: few enough to
-// stay in L2 (32 experts of 512 rows 5120 -> 4096: panels of 20 MB 409 us, 40 MB 424, 80 MB 455).
-constexpr int64_t kPanelBytes = 20 << 20;
+// stay in L2 beside the weights (32768 rows of 128 experts 2048 -> 5120: panels of 5 MB 687 us,
+// 10 MB 682, 20 MB 699; 32 experts of 512 rows 5120 -> 4096: 20 MB 409, 40 MB 424, 80 MB 455).
+constexpr int64_t kPanelBytes = 10 << 20;
 inline int panel_tiles(int64_t K) {
   const int64_t n = kPanelBytes / (kTileN(2) * K * 2);
-  return (int)(n < 8 ? 8 : n > 64 ? 64 : n);
+  return (int)(n < 4 ? 4 : n > 64 ? 64 : n);
 }
 constexpr int64_t kProductWait = 4000000000ll;  // cycles: about two seconds
 

@@ -173,3 +173,25 @@ def test_memory_beside_the_operands_is_left_alone(dtype):
             call(out)
             assert torch.equal(out.nan_to_num(), want.nan_to_num())
             assert buf[:32 + shift].isnan().all() and buf[32 + shift + n:].isnan().all()
+
+
+@pytest.mark.parametrize("K,N", [(64, 24), (33, 17)])
+def test_the_most_experts(K, N):
+    """4096 experts, most of few rows and many of none: more of them than threads."""
+    counts = [(i * 7) % 3 for i in range(4095)] + [41]
+    offsets, E = offsets_of(counts), 4096
+    xs, w = rows_of(counts, K, BF16, 40), weights(E, N, K, BF16, False)
+    expert = torch.repeat_interleave(torch.arange(E, device="cuda"), torch.tensor(counts, device="cuda"))
+    x = xs[:expert.numel()].double()
+    y, size = ((a[:, None] @ b[expert].mT).squeeze(1) for a, b in ((x, w.double()), (x.abs(), w.double().abs())))
+    close(experts.hc_mix_expert_product(xs, w, offsets)[:expert.numel()], y, chain(K) * size, "ys")
+    dys = rows_of(counts, N, BF16, 41)
+    d = dys[:expert.numel()].double()
+    dw, dsize = (torch.zeros(E, N, K, dtype=torch.float64, device="cuda").index_add(0, expert, a[:, :, None] * b[:, None])
+                 for a, b in ((d, x), (d.abs(), x.abs())))
+    close(experts.hc_mix_expert_product_weight_backward(dys, xs, offsets), dw, chain(41) * dsize, "dweight")
+    codes, scales, q = quantised(E, N, 64, 32, BF16)
+    xs = rows_of(counts, 64, BF16, 42)
+    x = xs[:expert.numel()].double()
+    y, size = ((a[:, None] @ b[expert].mT).squeeze(1) for a, b in ((x, q), (x.abs(), q.abs())))
+    close(experts.hc_mix_expert_product_q4(xs, codes, scales, offsets)[:expert.numel()], y, chain(64) * size, "4 bits")
