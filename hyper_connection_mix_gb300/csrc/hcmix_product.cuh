@@ -264,7 +264,8 @@ __device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* 
 // dweight by pairs: an expert's last 64 rows, if they are fewer, are zeroed behind before they
 // are multiplied, which takes about 2 us from their arrival.  So they are copied up to
 // kTailLead stages early and still multiplied last.  Their place among the tile's stages; the
-// number of stages where there are none such.
+// number of stages where there are none such.  (32 experts of 256 to 767 rows 5120 x 4096: 588 us
+// in their turn, 555 three stages early, the same two or four.)
 constexpr int kTailLead = 3;
 __device__ __forceinline__ int tail_place(int depth) {
   const int blocks = (depth + kTileK - 1) / kTileK;
