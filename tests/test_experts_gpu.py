@@ -278,6 +278,24 @@ def test_product_q4(K, N, group, dtype, gated):
         close(got, y, chain(K) * size, "ys")
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("counts", [[9], [40], [33, 1, 64], [1000, 0, 77]])
+@pytest.mark.parametrize("K,N,group,pad", [(64, 34, 32, 0), (1152, 66, 64, 3), (2304, 130, 128, 8)])
+def test_product_q4_of_many_rows(K, N, group, pad, counts, dtype, gated):
+    """More than eight rows an expert on average: four tiles of rows at a time, several times over."""
+    xs = rows_of(counts, K, dtype, 50)
+    codes, scales, w = quantised(len(counts), N, K, group, dtype)
+    got = experts.hc_mix_expert_product_q4(strided(xs, pad), codes, scales, offsets_of(counts), gated)
+    y, size = product_of(xs, w, counts, False)
+    if gated:
+        close(got, *gate_of(y, size, K), "h")
+    else:
+        close(got, y, chain(K) * size, "ys")
+    few = experts.hc_mix_expert_product_q4(xs[:1], codes, scales, offsets_of([1] + [0] * (len(counts) - 1)), gated)
+    assert torch.equal(few, got[:1])
+
+
 @pytest.mark.parametrize("pad,shift", [(8, 0), (3, 0), (0, 1), (8, 4)])
 def test_product_q4_strides(pad, shift):
     counts, K, N = [2, 11], 192, 48
