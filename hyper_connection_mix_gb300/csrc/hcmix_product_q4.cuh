@@ -210,16 +210,15 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
     int ahead_turn = 0, slot = 0;
     int64_t sent = 0;
     const uint32_t to = ring + g * 64 + ((t ^ (g >> 1 & 3)) << 4);
-    // a unit's features 8 on, and its tile of 16 on, where there are all of them
-    const int64_t code_row = A.K / 2, code_tile = (kGated ? plan.features : 16) * code_row;
-    const uint8_t* codes = nullptr;  // the lane's first
-    bool all_codes = false;
+    const uint32_t code_row = A.K / 2;
+    const uint8_t* codes = nullptr;  // of ahead's expert, the lane's 16 bytes of a chunk
+    uint32_t ahead_feature[4];       // the lane's
     const auto send = [&]() {
       if (sent < steps) {
         if (ahead_turn == 0) {
-          all_codes = ahead.f + plan.per <= plan.features;
-          codes = A.codes + 16 * t +
-                  ((int64_t)ahead.e * A.N + (all_codes ? feature(ahead.f, g) : 0)) * code_row;
+          codes = A.codes + 16 * t + (int64_t)ahead.e * A.N * code_row;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ahead_feature[i] = feature(ahead.f, 8 * i + g);
           // the unit's scales will be asked for when they are needed: they are on their way to L2
           // by then.  32 (16 and 16) neighbouring features' lie side by side.
 #pragma unroll
@@ -234,14 +233,11 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
         const int k = (warp + ahead_turn * kQ4Warps) * kQ4Chunk;
         if (k + 32 * t < A.K) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int64_t off = all_codes ? i % 2 * 8 * code_row + i / 2 * code_tile
-                                          : feature(ahead.f, 8 * i + g) * code_row;
+          for (int i = 0; i < 4; ++i)
             asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(
                              to + slot * kQ4Box + i * 512),
-                         "l"(codes + k / 2 + off)
+                         "l"(codes + k / 2 + (uint64_t)ahead_feature[i] * code_row)
                          : "memory");
-          }
         }
         if (++slot == kQ4Depth) slot = 0;
         if (++ahead_turn == turns) {
@@ -256,16 +252,16 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
     Q4Place near = start;
     int near_turn = 0;
     int64_t loaded = 0;
-    const int64_t scale_tile = (int64_t)(kGated ? plan.features : 16) * groups;
-    const T* of_unit = nullptr;     // scales of the lane's first feature
-    bool all_scales = false;
+    const T* of_expert = nullptr;   // scales
+    uint32_t near_feature[4];       // the lane's
     const T* of_row[kTiles] = {};   // the lane's rows; behind the last the last one's again, whose
                                     // products are not stored
     const auto load = [&](Q4Operands<T, kTiles>& o) {
       if (loaded >= steps) return;
       if (near_turn == 0) {
-        all_scales = near.f + plan.per <= plan.features;
-        of_unit = scales + ((int64_t)near.e * A.N + (all_scales ? feature(near.f, g) : 0)) * groups;
+        of_expert = scales + (int64_t)near.e * A.N * groups;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) near_feature[i] = feature(near.f, 8 * i + g);
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
           const int row = near.row + 8 * n + g;
@@ -295,11 +291,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
       int q = (k + 32 * t) >> shift;
       q = q < groups ? q : groups - 1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t off = all_scales ? i % 2 * 8 * groups + i / 2 * scale_tile
-                                       : (int64_t)feature(near.f, 8 * i + g) * groups;
-        o.scale[i] = of_unit[off + q];
-      }
+      for (int i = 0; i < 4; ++i)
+        o.scale[i] = (of_expert + q)[(uint64_t)near_feature[i] * (uint32_t)groups];
       if (++near_turn == turns) {
         near_turn = 0;
         plan.next(near);
@@ -310,7 +303,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
     Q4Operands<T, kTiles> now;
     for (int i = 0; i < kQ4Depth - 1; ++i) send();
     Q4Place at = start;
-    const bool per_block = A.group == 32, per_two = A.group == 64;
+// the blocks of a chunk with which a group (or the chunk) ends; k ends with a group
+    const int ends = A.group == 32 ? 15 : A.group == 64 ? 10 : 8;
     float total[2][kTiles][4];
     int turn = 0, buf = 0, from = 0;
     const uint32_t words = ring + g * 64 + 4 * t;
@@ -355,7 +349,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
             for (int h = 0; h < 2; ++h) Codes<T>::mma(acc[h][n], a[h], b0, b1);
           }
         }
-        if (b == 3 || k + 32 * (b + 1) >= A.K || per_block || (per_two && b == 1)) {
+        if (ends >> b & 1) {
           // a group ends, or the chunk
 #pragma unroll
           for (int h = 0; h < 2; ++h)
