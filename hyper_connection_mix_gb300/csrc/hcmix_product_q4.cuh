@@ -12,10 +12,11 @@
 // code's bits under 128's (bf16) or 1024's (fp16) exponent are 128 + code, and less 136 they are
 // code - 8, exactly.  Sums of a group are fp32, and are scaled and added in fp32.
 //
-// Measured: 16 tokens to 8 of 128 experts 5120 -> 2 x 2048 bf16 314 us (2.8 TB/s, 42 % of the copy
-// rate), one token 2048 -> 5120 fp16 27.4 us.  The copies alone take 163 us: what bounds it is
-// instructions, 571 of a warp for 2 KB of codes.  Three blocks a multiprocessor with one set of
-// registers for the rows do better than two with two sets (326 us); 64 features a unit do worse.
+// Measured: 16 tokens to 8 of 128 experts 5120 -> 2 x 2048 bf16 293 us (3.1 TB/s, 45 % of the copy
+// rate), one token 2048 -> 5120 fp16 27.3 us.  The copies alone take 163 us: what bounds it is
+// instructions (571 of a warp for 2 KB of codes when it took 314 us).  Three blocks a
+// multiprocessor with one set of registers for the rows did better than two with two sets (314 and
+// 326 us); 64 features a unit did worse.
 #pragma once
 
 #include "hcmix_vec.cuh"
@@ -191,12 +192,13 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
   __syncthreads();
   const int chunks = (A.K + kQ4Chunk - 1) / kQ4Chunk;
   const int turns = (chunks + kQ4Warps - 1) / kQ4Warps;  // of a warp at a unit
-  const int64_t steps = (u1 - u0) * turns;
+  // (results of more than 2^31 units a block would not fit any memory)
+  const int own = (int)(u1 - u0);
   const int shift = 31 - __clz(A.group), groups = A.K >> shift;
   const T* scales = static_cast<const T*>(A.scales);
   const Codes<T> code;
 
-  if (steps > 0) {
+  if (own > 0) {
     const Q4Place start = {start_of[0], start_of[1], start_of[2], start_of[3]};
     // Feature r of a unit's 32 among its expert's, clamped to those that there are.
     const int most = plan.features - 1;
@@ -208,13 +210,13 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
     // 16, exchanged so that eight features' words of a block lie in different banks
     Q4Place ahead = start;
     int ahead_turn = 0, slot = 0;
-    int64_t sent = 0;
+    int ahead_left = own;
     const uint32_t to = ring + g * 64 + ((t ^ (g >> 1 & 3)) << 4);
     const uint32_t code_row = A.K / 2;
     const uint8_t* codes = nullptr;  // of ahead's expert, the lane's 16 bytes of a chunk
     uint32_t ahead_feature[4];       // the lane's
     const auto send = [&]() {
-      if (sent < steps) {
+      if (ahead_left > 0) {
         if (ahead_turn == 0) {
           codes = A.codes + 16 * t + (int64_t)ahead.e * A.N * code_row;
 #pragma unroll
@@ -242,22 +244,22 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
         if (++slot == kQ4Depth) slot = 0;
         if (++ahead_turn == turns) {
           ahead_turn = 0;
+          --ahead_left;
           plan.next(ahead);
         }
-        ++sent;
       }
       async_commit();
     };
     // ---- rows and scales of one chunk into registers
     Q4Place near = start;
     int near_turn = 0;
-    int64_t loaded = 0;
+    int near_left = own;
     const T* of_expert = nullptr;   // scales
     uint32_t near_feature[4];       // the lane's
     const T* of_row[kTiles] = {};   // the lane's rows; behind the last the last one's again, whose
                                     // products are not stored
     const auto load = [&](Q4Operands<T, kTiles>& o) {
-      if (loaded >= steps) return;
+      if (near_left <= 0) return;
       if (near_turn == 0) {
         of_expert = scales + (int64_t)near.e * A.N * groups;
 #pragma unroll
@@ -295,9 +297,9 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
         o.scale[i] = (of_expert + q)[(uint64_t)near_feature[i] * (uint32_t)groups];
       if (++near_turn == turns) {
         near_turn = 0;
+        --near_left;
         plan.next(near);
       }
-      ++loaded;
     };
 
     Q4Operands<T, kTiles> now;
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
     float total[2][kTiles][4];
     int turn = 0, buf = 0, from = 0;
     const uint32_t words = ring + g * 64 + 4 * t;
-    for (int64_t step = 0; step < steps; ++step) {
+    for (int left = own; left > 0;) {
       send();
       if (turn == 0) {
 #pragma unroll
@@ -369,6 +371,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
       __syncwarp();
       if (++turn < turns) continue;
       turn = 0;
+      --left;
       // ---- the warps' sums: value v = (h, n, i) of a lane
       constexpr int kValues = 2 * kTiles * 4;
       float* part = parts + buf * (kQ4Warps * kValues * 32);
