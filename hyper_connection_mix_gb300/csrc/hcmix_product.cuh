@@ -22,7 +22,7 @@
 //   one         128 experts of one row: 391 us, 6.9 TB/s
 //   dweight     16384 rows 5120 x 5120: 460 us; 32 experts of 512 rows 5120 x 4096: 467 us, where
 //               the stores meet the copies in L2; 128 experts of one row: 393 us, 6.8 TB/s
-//   plain loads 61 experts of 72 rows 1023 -> 1001 fp16: 86 to 94 us, bound by the instructions
+//   plain loads 61 experts of 72 rows 1023 -> 1001 fp16: 96 to 104 us, bound by the instructions
 //               that shift rows into place
 #pragma once
 
@@ -131,7 +131,7 @@ struct ProductControl {
   uint64_t drain;
   uint32_t tmem;
   int abort;
-  int scan[32];
+  int64_t scan[32];
   RawRows raw[kProducers][kRawDepth];
 };
 // Warps that store: one or two for each 32 lanes of TMEM.
@@ -164,13 +164,14 @@ __device__ __forceinline__ void expert_rows(const ProductArgs& A, int e, int& fi
   count = last > first ? last - first : 0;
 }
 
-// The number of row tiles of all experts before each, in `cum`.
+// The number of row tiles of all experts before each, in `cum`, at most 2^31 - 1 (which only
+// offsets that fall can pass: they may count rows many times over).
 template <int kCtas>
-__device__ __forceinline__ void count_tiles(const ProductArgs& A, int* cum, int* scan) {
+__device__ __forceinline__ void count_tiles(const ProductArgs& A, int* cum, int64_t* scan) {
   const int threads = blockDim.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int per = (A.E + threads - 1) / threads;
   const int e0 = tid * per < A.E ? tid * per : A.E, e1 = e0 + per < A.E ? e0 + per : A.E;
-  int sum = 0;
+  int64_t sum = 0;
   for (int e = e0; e < e1; ++e) {
     int first, count;
     expert_rows(A, e, first, count);
@@ -178,10 +179,10 @@ __device__ __forceinline__ void count_tiles(const ProductArgs& A, int* cum, int*
     cum[e + 1] = tiles;
     sum += tiles;
   }
-  int before = sum;
+  int64_t before = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, before, o);
+    const int64_t t = __shfl_up_sync(0xffffffffu, before, o);
     if (lane >= o) before += t;
   }
   if (lane == 31) scan[warp] = before;
@@ -191,7 +192,7 @@ __device__ __forceinline__ void count_tiles(const ProductArgs& A, int* cum, int*
   if (tid == 0) cum[0] = 0;
   for (int e = e0; e < e1; ++e) {
     before += cum[e + 1];
-    cum[e + 1] = before;
+    cum[e + 1] = before < 0x7fffffff ? (int)before : 0x7fffffff;
   }
   __syncthreads();
 }
@@ -254,6 +255,7 @@ __device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* 
     const int size = round_rows<kCtas>((count + nt - 1) / nt);
     T.n0 = first + j * size;
     T.n = count - j * size < size ? count - j * size : size;
+    if (T.n > kTileN(kCtas)) T.n = kTileN(kCtas);  // (see count_tiles)
     T.depth = A.K;
   }
   T.m0 = (int)m * width + rank * (width / kCtas);
@@ -648,9 +650,8 @@ __device__ __forceinline__ void store_rows(T* to, int64_t stride, uint32_t box, 
   put_row<float, 16>(box, v, 0, 0, lane);
   put_row<float, 16>(box, v, 16, 1, lane);
   __syncwarp();
-  if (lane >= cols) return;
 #pragma unroll 4
-  for (int r = 0; r < rows; ++r, to += stride) {
+  for (int r = 0; r < rows && lane < cols; ++r, to += stride) {
     float f;
     asm volatile("ld.shared.f32 %0, [%1];"
                  : "=f"(f)
@@ -658,6 +659,7 @@ __device__ __forceinline__ void store_rows(T* to, int64_t stride, uint32_t box, 
                  : "memory");
     to[lane] = from_f32<T>(f);
   }
+  __syncwarp();  // the next load from TMEM is the whole warp's
 }
 
 // By a whole warp: its box in shared memory as rows m .. m + 31 of an expert's result, from
@@ -816,9 +818,15 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     int64_t step = 0;
     bool idle = false;
     bool inside = false;  // all blocks of the tile's rows lie in the matrix
-    const auto copy = [&]() {
-      while (more && kb == blocks) {
+    // Copies one stage; false where there is none, or where its tile has not been told yet and
+    // `may_wait` is not set: the tile is told when the MMA and storing warps have taken earlier
+    // ones, for which they may need a stage that this warp has copied and not yet placed.
+    const auto copy = [&](bool may_wait) {
+      while (kb == blocks) {
+        const bool told = mbar_test_wait(smem_u32(&C.told[turns % kQueue]), (turns / kQueue) & 1);
+        if (!may_wait && !__all_sync(0xffffffffu, told)) return false;
         more = next(T);
+        if (!more) return false;
         kb = 0;
         blocks = (T.depth + kTileK - 1) / kTileK;
         const int first = of_a ? (half ? T.m1 : T.m0) : T.n0 + 64 * half;  // feature or row
@@ -842,7 +850,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
           if (row >= kRawRows || (!flat && row >= R.rows)) from[i] = nullptr;
         }
       }
-      if (more) {
+      {
         const int slot = copied++ % kRawDepth;
         const uint32_t raw = ring + slot * kRawBox;
         if (idle) {
@@ -872,12 +880,16 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
         ++kb;
       }
       async_commit();
+      return true;
     };
-    for (int i = 0; i < kRawDepth - 1; ++i) copy();
     for (;; ++placed) {
-      copy();
+      while (more && copied - placed < kRawDepth && copy(copied == placed)) {
+      }
       if (placed == copied) break;
-      async_wait<kRawDepth - 1>();
+      if (copied - placed == kRawDepth)
+        async_wait<kRawDepth - 1>();
+      else
+        async_wait<0>();
       __syncwarp();
       const int s = placed % kDepth, slot = placed % kRawDepth;
       if (placed >= kDepth &&

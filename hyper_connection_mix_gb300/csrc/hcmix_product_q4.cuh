@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
   begin_kernel();
   constexpr int kRows = 8 * kTiles;
   extern __shared__ __align__(16) uint8_t q4_shared[];
-  __shared__ int sums[kQ4Warps], start_of[4];
+  __shared__ int64_t sums[kQ4Warps];
+  __shared__ int start_of[4];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t = lane % 4;
   const uint32_t ring =
       (uint32_t)__cvta_generic_to_shared(q4_shared) + warp * (kQ4Depth * kQ4Box);
@@ -163,37 +164,41 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
   // ---- the block's range of units, and the place where it begins
   const int each = (A.E + kQ4Warps * 32 - 1) / (kQ4Warps * 32);
   const int e0 = tid * each < A.E ? tid * each : A.E, e1 = e0 + each < A.E ? e0 + each : A.E;
-  int here = 0;
+  // (64 bits: offsets that fall may count rows many times over)
+  int64_t here = 0;
   for (int e = e0; e < e1; ++e) here += plan.blocks(e);
-  int upto = here;
+  int64_t upto = here;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int s = __shfl_up_sync(0xffffffffu, upto, o);
+    const int64_t s = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += s;
   }
   if (lane == 31) sums[warp] = upto;
   __syncthreads();
-  int all = 0;
+  int64_t all = 0;
   for (int w = 0; w < kQ4Warps; ++w) {
     if (w < warp) upto += sums[w];
     all += sums[w];
   }
-  const int64_t units = (int64_t)all * plan.across;
-  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-  const int block0 = (int)(u0 / plan.across);
+  const int64_t units = all * plan.across, per_block = units / gridDim.x;
+  const int more = (int)(units % gridDim.x);
+  const int64_t u0 = per_block * blockIdx.x + (blockIdx.x < more ? blockIdx.x : more);
+  const int64_t u1 = u0 + per_block + (blockIdx.x < more);
+  const int64_t block0 = u0 / plan.across;
   if (u0 < u1 && block0 >= upto - here && block0 < upto) {
-    int left = block0 - (upto - here), e = e0;
+    int64_t left = block0 - (upto - here);
+    int e = e0;
     for (; left >= plan.blocks(e); ++e) left -= plan.blocks(e);
     start_of[0] = e;
-    start_of[1] = q4_offset(A.offsets[e], A.R) + left * kRows;
+    start_of[1] = q4_offset(A.offsets[e], A.R) + (int)left * kRows;
     start_of[2] = q4_offset(A.offsets[e + 1], A.R);
-    start_of[3] = (int)(u0 - (int64_t)block0 * plan.across) * plan.per;
+    start_of[3] = (int)(u0 - block0 * plan.across) * plan.per;
   }
   __syncthreads();
   const int chunks = (A.K + kQ4Chunk - 1) / kQ4Chunk;
   const int turns = (chunks + kQ4Warps - 1) / kQ4Warps;  // of a warp at a unit
-  // (results of more than 2^31 units a block would not fit any memory)
-  const int own = (int)(u1 - u0);
+  // results of more than 2^31 units a block would not fit any memory
+  const int own = u1 - u0 < 0x7fffffff ? (int)(u1 - u0) : 0x7fffffff;
   const int shift = 31 - __clz(A.group), groups = A.K >> shift;
   const T* scales = static_cast<const T*>(A.scales);
   const Codes<T> code;

@@ -175,6 +175,23 @@ def test_memory_beside_the_operands_is_left_alone(dtype):
             assert buf[:32 + shift].isnan().all() and buf[32 + shift + n:].isnan().all()
 
 
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("K,N", [(365, 1824), (1824, 365), (368, 1824)])
+@pytest.mark.parametrize("every", [1, 3, 11])
+def test_weight_gradients_of_experts_without_rows(K, N, every, transposed):
+    """Runs of tiles that have nothing to multiply, longer than the tiles that are told ahead."""
+    counts = [i % 3 + 1 if i % every == 0 else 0 for i in range(24)]
+    xs, dys = rows_of(counts, K, F16, 60), rows_of(counts, N, F16, 61)
+    got = experts.hc_mix_expert_product_weight_backward(dys, xs, offsets_of(counts), transposed)
+    at = 0
+    for e, n in enumerate(counts):
+        x, d = xs[at:at + n].double(), dys[at:at + n].double()
+        a, b = (x, d) if transposed else (d, x)
+        close(got[e], a.t() @ b, chain(n) * (a.t().abs() @ b.abs()), f"dweight[{e}] of {n} rows")
+        at += n
+    assert experts.hc_mix_expert_device_status() == 0
+
+
 @pytest.mark.parametrize("K,N", [(64, 24), (33, 17)])
 def test_the_most_experts(K, N):
     """4096 experts, most of few rows and many of none: more of them than threads."""

@@ -270,3 +270,107 @@ def test_a_warp_that_does_not_wait_for_the_others_stages_is_found():
         except AssertionError:
             found += 1
     assert found
+
+
+# ------------------------------------------------------------------------------- plain loads
+
+
+class Plain(Cluster):
+    """One block whose producers copy rows ahead of the stage that they place: up to RAW stages, and
+    only of tiles that have been told, while they have one to place."""
+    RAW, WARPS = 3, 2
+
+    def __init__(self, depths, seed, planted=None):
+        self.rnd, self.tiles, self.weight, self.planted = random.Random(seed), depths, False, planted
+        self.errors, self.pipe, self.filled = [], [], [0, 0]
+        mk = lambda n, count, what: [Bar(count, f"{what}{i}") for i in range(n)]  # noqa: E731
+        self.b = {"told": mk(QUEUE, 1, "told"), "taken": mk(QUEUE, 1 + STORERS + self.WARPS, "taken"),
+                  "full": mk(2, self.WARPS, "full"), "empty": mk(2, 1, "empty"),
+                  "acc_full": mk(2, 1, "acc_full"), "acc_empty": mk(2, STORERS, "acc_empty")}
+        self.bars = [self.b]
+
+    def plain_producer(self):
+        copied = placed = left = turn = 0
+        more = True
+        while True:
+            while more and copied - placed < self.RAW:
+                while left == 0 and more:
+                    told = self.b["told"][turn % QUEUE].phase > turn // QUEUE
+                    if not told and copied > placed and self.planted is None:
+                        break
+                    yield from self.next(0, turn)
+                    more = turn < len(self.tiles)
+                    left = int(self.tiles[turn]) if more else 0
+                    turn += 1
+                if left == 0:
+                    break
+                left, copied = left - 1, copied + 1
+            if copied == placed:
+                return
+            if placed >= 2:
+                yield from self.wait(self.b["empty"][placed % 2], placed // 2 - 1)
+            yield None
+            self.b["full"][placed % 2].arrive()
+            placed += 1
+
+    def plain_mma(self):
+        it = acc = 0
+        for turn, depth in enumerate(self.tiles):
+            yield from self.next(0, turn)
+            if depth == 0:
+                continue
+            if acc >= 2:
+                yield from self.wait(self.b["acc_empty"][acc % 2], acc // 2 - 1)
+            for _ in range(int(depth)):
+                yield from self.wait(self.b["full"][it % 2], it // 2)
+                self.b["empty"][it % 2].arrive()
+                it += 1
+            self.b["acc_full"][acc % 2].arrive()
+            acc += 1
+        yield from self.next(0, len(self.tiles))
+
+    def plain_storer(self):
+        acc = 0
+        for turn, depth in enumerate(self.tiles):
+            yield from self.next(0, turn)
+            if depth == 0:
+                continue
+            yield from self.wait(self.b["acc_full"][acc % 2], acc // 2)
+            self.b["acc_empty"][acc % 2].arrive()
+            acc += 1
+        yield from self.next(0, len(self.tiles))
+
+    def run(self):
+        at = [(r, None) for r in [self.scheduler(0), self.plain_mma()] + [self.plain_storer() for _ in range(STORERS)]
+              + [self.plain_producer() for _ in range(self.WARPS)]]
+        while at and not self.errors:
+            ready = [i for i, (_, w) in enumerate(at) if w is None or (w[0].phase & 1) != (w[1] & 1)]
+            assert ready, "deadlock: " + ", ".join(f"{w[0].name} phase {w[1]}" for _, w in at)
+            i = self.rnd.choice(ready)
+            try:
+                at[i] = (at[i][0], next(at[i][0]))
+            except StopIteration:
+                at.pop(i)
+        return self.errors
+
+
+def plain_depths(rnd):
+    """Runs of tiles without anything to multiply among others."""
+    return [d for _ in range(rnd.randint(1, 8)) for d in [0] * rnd.choice([0, 0, 1, 5, 9]) + [rnd.choice([1, 1, 2, 7])]]
+
+
+def test_plain_loads():
+    for seed in range(200):
+        tiles = plain_depths(random.Random(seed))
+        errors = Plain(tiles, seed).run()
+        assert not errors, (seed, tiles, errors[:3])
+
+
+def test_plain_loads_that_wait_for_a_tile_with_a_stage_in_hand_are_found():
+    found = 0
+    for seed in range(50):
+        try:
+            found += bool(Plain(plain_depths(random.Random(seed)), seed, planted="wait").run())
+        except AssertionError:
+            found += 1
+    assert found
