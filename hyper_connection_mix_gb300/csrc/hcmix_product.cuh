@@ -16,11 +16,11 @@
 // Blocks are resident: one warp fills a ring of 64-wide slices of A and B, one issues the MMAs,
 // others store a tile while the next is computed.  What bounds it, measured on one GB300
 // (L2 gives the multiprocessors at most about 15 TB/s together):
-//   many rows   16384 rows 5120 -> 5120 bf16: 431 to 458 us, 1990 to 1870 TFLOP/s; the MMAs
-//               alone 386 us, the copies alone 467 us by pairs, which is why two pairs share rows
+//   many rows   16384 rows 5120 -> 5120 bf16: 469 us, 1830 TFLOP/s; the MMAs alone 386 us, the
+//               copies alone 467 us
 //   some        128 experts of 256 rows 2048 -> 5120: 480 us; the weights' bytes at 6.8 TB/s: 396
 //   one         128 experts of one row: 391 us, 6.9 TB/s
-//   dweight     16384 rows 5120 x 5120: 460 us; 32 experts of 512 rows 5120 x 4096: 467 us, where
+//   dweight     16384 rows 5120 x 5120: 522 us; 32 experts of 512 rows 5120 x 4096: 467 us, where
 //               the stores meet the copies in L2; 128 experts of one row: 393 us, 6.8 TB/s
 //   plain loads 61 experts of 72 rows 1023 -> 1001 fp16: 96 to 104 us, bound by the instructions
 //               that shift rows into place
@@ -46,15 +46,13 @@ enum class ProductMode { kRowsK, kRowsM, kWeight };  // A's contiguous index: k,
 //   1  operands whose rows do not all start on 16 bytes, by plain loads and tiles of 128 x 128;
 //   2  a pair: tcgen05 cta_group::2 with 256 features, and half of B in each block, so that
 //      a multiprocessor's shared memory takes in and gives out two thirds of what a tile of
-//      128 x 256 would need;
-//   4  two pairs with neighbouring features and the same rows, each of which is read once and
-//      sent to both.
+//      128 x 256 would need.
+// No copy is sent to several blocks: operands may lie in a peer's memory.
 constexpr int kABytes = kTileM * kTileK * 2;
 __host__ __device__ constexpr int kTileN(int ctas) { return ctas > 1 ? 256 : 128; }
 constexpr int kAccumulator = 256;  // TMEM columns
-__host__ __device__ constexpr int kMmaCtas(int ctas) { return ctas > 1 ? 2 : 1; }
 __host__ __device__ constexpr int kStageBytes(int ctas) {
-  return kABytes + kTileN(ctas) * kTileK * 2 / kMmaCtas(ctas);
+  return kABytes + kTileN(ctas) * kTileK * 2 / ctas;
 }
 __host__ __device__ constexpr int kStages(int ctas) { return ctas > 1 ? 6 : 2; }
 constexpr int kMostStages = 6;
@@ -200,7 +198,7 @@ __device__ __forceinline__ void count_tiles(const ProductArgs& A, int* cum, int6
 // The MMA's N: a multiple of 16 for each block.
 template <int kCtas>
 __device__ __forceinline__ int round_rows(int n) {
-  constexpr int to = 16 * kMmaCtas(kCtas);
+  constexpr int to = 16 * kCtas;
   return (n + to - 1) / to * to;
 }
 
@@ -443,16 +441,10 @@ __device__ __forceinline__ void product_tmem_dealloc(uint32_t tmem) {
     sm100::tmem_dealloc(tmem, 512);
 }
 
-// The address, in the cluster's shared memory, of what the first block of this block's pair
-// has at `addr`.
+// The address, in the cluster's shared memory, of what the pair's first block has at `addr`.
 __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
   uint32_t r;
-  asm("{\n\t.reg .u32 c;\n\t"
-      "mov.u32 c, %%cluster_ctarank;\n\t"
-      "and.b32 c, c, 0xfffffffe;\n\t"
-      "mapa.shared::cluster.u32 %0, %1, c;\n\t}"
-      : "=r"(r)
-      : "r"(addr));
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
 }
 // One arrival at a barrier of that block.
@@ -495,18 +487,6 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const void* map, int 
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
-      : "memory");
-}
-
-// A box for the same place in all blocks of `mask`, complete at the same barrier of each (of
-// each one's pair, where `bar` is the leader's).
-__device__ __forceinline__ void pair_send_2d(uint32_t dst, const void* map, int c0, int c1,
-                                             uint32_t bar, uint32_t mask, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".multicast::cluster.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "h"((uint16_t)mask),
-      "l"(policy)
       : "memory");
 }
 
@@ -728,7 +708,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   constexpr bool kTma = kCtas > 1;
   constexpr bool kAcross = kMode != ProductMode::kRowsK;   // A lies with m contiguous
   constexpr bool kWeight = kMode == ProductMode::kWeight;  // and B with n
-  constexpr int kMma = kMmaCtas(kCtas), kDepth = kStages(kCtas);
+  constexpr int kDepth = kStages(kCtas);
   constexpr int kStore = kStorers(kCtas), kTurns = kStore * kTurnBytes(kMode);
   extern __shared__ uint8_t product_shared[];
   const uint32_t raw = smem_u32(product_shared);
@@ -738,8 +718,8 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   ProductControl& C = *reinterpret_cast<ProductControl*>(after + kTurns + kRawBytes(kCtas));
   int* cum = reinterpret_cast<int*>(&C + 1);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int rank = blockIdx.x % kCtas, half_rank = rank % kMma;
-  const bool leader = half_rank == 0;  // of a pair
+  const int rank = blockIdx.x % kCtas;
+  const bool leader = rank == 0;  // of a pair
 
   if (tid == 0) {
     const int takers = kStore + (kTma ? 1 : kProducers) + leader + (kTma && kWeight ? 2 : 0);
@@ -749,19 +729,19 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     }
     for (int s = 0; s < kDepth; ++s) {
       mbar_init(smem_u32(&C.full[s]), kTma ? 1 : kProducers);
-      mbar_init(smem_u32(&C.empty[s]), kCtas / kMma);
+      mbar_init(smem_u32(&C.empty[s]), 1);
       mbar_init(smem_u32(&C.tail[s]), 1);
-      mbar_init(smem_u32(&C.ready[s]), 2 * kMma);
+      mbar_init(smem_u32(&C.ready[s]), 2 * kCtas);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&C.acc_full[b]), 1);
-      mbar_init(smem_u32(&C.acc_empty[b]), kStore * kMma);
+      mbar_init(smem_u32(&C.acc_empty[b]), kStore * kCtas);
     }
     mbar_init(smem_u32(&C.drain), 1);
     C.abort = 0;
     fence_mbarrier_init();
   }
-  // the cluster's barriers are there before its other blocks touch them
+  // the pair's barriers are there before its other block touches them
   if (kTma) cluster_sync();
   if (warp == 2) product_tmem_alloc<kTma>(smem_u32(&C.tmem));
   if (!kWeight) count_tiles<kCtas>(A, cum, C.scan);
@@ -911,8 +891,8 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     bool ok = true;
     while (ok && next(T)) {
       const int blocks = (T.depth + kTileK - 1) / kTileK;
-      const int n = round_rows<kCtas>(T.n) / kMma;  // this block's share of B
-      const int n0 = T.n0 + half_rank * n;
+      const int n = round_rows<kCtas>(T.n) / kCtas;  // this block's share of B
+      const int n0 = T.n0 + rank * n;
       const int place = kTma && kWeight ? tail_place(T.depth) : blocks;
       for (int i = 0; ok && i < blocks; ++i, ++it) {
         const int s = it % kDepth;
@@ -946,33 +926,15 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
               else
                 pair_load_3d(a + h * kBoxBytes, &A.a_map, k, m, T.expert, bar, keep);
             }
-            if constexpr (kCtas == 2) {
-              if (kWeight) {
-                for (int j = 0; j < boxes; ++j)
-                  pair_load_2d(b + j * kBoxBytes, &A.b_map, n0 + j * 64, k, bar, keep);
-              } else {
-                int r = 0;
-                for (; r + 64 <= n; r += 64)
-                  pair_load_2d(b + r * 128, &A.b_map, k, n0 + r, bar, keep);
-                for (; r < n; r += 16)
-                  pair_load_2d(b + r * 128, &A.b16_map, k, n0 + r, bar, keep);
-              }
+            if (kWeight) {
+              for (int j = 0; j < boxes; ++j)
+                pair_load_2d(b + j * kBoxBytes, &A.b_map, n0 + j * 64, k, bar, keep);
             } else {
-              // the block of the other pair that needs the same share sends the rest of it
-              const uint32_t mask = 5u << half_rank;
-              const int second = rank / 2;
-              if (kWeight) {
-                const int most = (boxes + 1) / 2;
-                for (int j = second ? most : 0; j < (second ? boxes : most); ++j)
-                  pair_send_2d(b + j * kBoxBytes, &A.b_map, n0 + j * 64, k, bar, mask, keep);
-              } else {
-                const int most = (n / 16 + 1) / 2 * 16, end = second ? n : most;
-                int r = second ? most : 0;
-                for (; r + 64 <= end; r += 64)
-                  pair_send_2d(b + r * 128, &A.b_map, k, n0 + r, bar, mask, keep);
-                for (; r < end; r += 16)
-                  pair_send_2d(b + r * 128, &A.b16_map, k, n0 + r, bar, mask, keep);
-              }
+              int r = 0;
+              for (; r + 64 <= n; r += 64)
+                pair_load_2d(b + r * 128, &A.b_map, k, n0 + r, bar, keep);
+              for (; r < n; r += 16)
+                pair_load_2d(b + r * 128, &A.b16_map, k, n0 + r, bar, keep);
             }
           }
           __syncwarp();
@@ -1006,7 +968,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
         if (lane == 0) arrive_leader_read<kTma>(smem_u32(&C.ready[s]));
         continue;
       }
-      const int boxes = 2 + (round_rows<kCtas>(T.n) / kMma + 63) / 64;
+      const int boxes = 2 + (round_rows<kCtas>(T.n) / kCtas + 63) / 64;
       // of the last 16 rows that the MMA reads
       const uint32_t from = left * 128 + lane * 16, to = (left + 15) / 16 * 16 * 128;
       for (int i = 0; i < boxes; ++i)
@@ -1019,7 +981,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   } else if (warp == 1 && leader) {
     // ---- MMA
     uint32_t it = 0, acc = 0, full_at = 0, tail_at = 0;
-    const uint32_t pair = 3u << (rank & ~1);
+    constexpr uint32_t kPair = (1u << kCtas) - 1;
     bool ok = true;
     const uint32_t kind = A.f16 ? 0u : (1u << 7) | (1u << 10);
     while (ok && next(T)) {
@@ -1028,7 +990,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       const uint32_t idesc = (1u << 4) | kind | (kAcross ? 1u << 15 : 0u) |
                              (kWeight ? 1u << 16 : 0u) |
                              ((uint32_t)(round_rows<kCtas>(T.n) >> 3) << 17) |
-                             ((uint32_t)(kTileM * kMma >> 4) << 24);
+                             ((uint32_t)(kTileM * kCtas >> 4) << 24);
       const int buf = acc & 1;
       if (acc >= 2) ok = __all_sync(0xffffffffu, wait(C.acc_empty[buf], (acc / 2 - 1) & 1));
       tc_fence_after();
@@ -1056,14 +1018,14 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
           for (int i = 0; i * 16 < left; ++i)
             mma_16<kTma>(d, da + i * kA, db + i * kB, idesc, kb > 0 || i > 0);
         }
-        mma_commit<kTma>(smem_u32(&C.empty[s]), (1u << kCtas) - 1);
-        if (kb == blocks - 1) mma_commit<kTma>(smem_u32(&C.acc_full[buf]), pair);
+        mma_commit<kTma>(smem_u32(&C.empty[s]), kPair);
+        if (kb == blocks - 1) mma_commit<kTma>(smem_u32(&C.acc_full[buf]), kPair);
       }
       it += blocks;
       ++acc;
     }
     // what was issued is done before the block ends
-    mma_commit<kTma>(smem_u32(&C.drain), pair);
+    mma_commit<kTma>(smem_u32(&C.drain), kPair);
     finish(C.drain, 0);
   } else if (warp >= 4 && warp < 4 + kStore) {
     // ---- epilogue: TMEM lanes 32 * w on, chunks of 32 columns in turn
@@ -1268,8 +1230,7 @@ inline bool make_out_map(ProductArgs& A) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The clusters that the current device runs at a time (of four blocks fewer than a quarter of
-// its multiprocessors: 36 on 152).  Asked for once a device.
+// The clusters that the current device runs at a time.  Asked for once a device.
 template <int kCtas, ProductMode kMode>
 hcmix_status resident_clusters(int* clusters) {
   constexpr int kDevices = 64;
@@ -1306,19 +1267,11 @@ hcmix_status resident_clusters(int* clusters) {
   return HCMIX_OK;
 }
 
-// The tiles that a call's clusters have to expect: the experts' rows are known on the device
-// only, and are taken to be shared out evenly.
 template <int kCtas, ProductMode kMode>
-int64_t expected_tiles(const ProductArgs& A) {
-  const int width = tile_width<kCtas>(A);
-  const int64_t mt = (A.M + width - 1) / width;
-  if (kMode == ProductMode::kWeight) return A.E * mt * ((A.N + kTileN(kCtas) - 1) / kTileN(kCtas));
-  const int64_t some = A.R < A.E ? A.R : A.E;
-  return mt * some * ((A.R / (some > 0 ? some : 1) + kTileN(kCtas) - 1) / kTileN(kCtas));
-}
-
-template <int kCtas, ProductMode kMode>
-hcmix_status launch_product(const ProductArgs& A, int clusters, cudaStream_t stream) {
+hcmix_status launch_product(const ProductArgs& A, cudaStream_t stream) {
+  int clusters = 0;
+  const hcmix_status st = resident_clusters<kCtas, kMode>(&clusters);
+  if (st != HCMIX_OK) return st;
   const int width = tile_width<kCtas>(A);
   const int64_t mt = (A.M + width - 1) / width;
   const int64_t tiles = kMode == ProductMode::kWeight
@@ -1328,25 +1281,6 @@ hcmix_status launch_product(const ProductArgs& A, int clusters, cudaStream_t str
   return launch(hcmix_product_kernel<kCtas, kMode>, dim3((unsigned)grid * kCtas),
                 dim3(kProductThreads(kCtas, kMode)), product_smem<kCtas, kMode>(A.E),
                 product_smem<kCtas, kMode>(kProductExperts), stream, A, kCtas);
-}
-
-// Clusters of four blocks read the rows once for two pairs: a full tile takes them 0.87 of the
-// time (16384 rows 5120 -> 5120: 431 us, pairs 469 us; 8 experts of 4096 rows 2048 -> 5120: 370 us
-// and 399 us), though the device runs 36 of them on 144 of its 152 multiprocessors.  Their
-// tiles are twice as wide, so that a call of few tiles may take more rounds of them
-// (19456 rows 5120 -> 512: 84 us, pairs 69 us).  dweight: 0.92 (16384 rows: 483 us, pairs 522 us);
-// with few rows an expert its stores count, and pairs do as well.
-template <ProductMode kMode>
-hcmix_status launch_clusters(const ProductArgs& A, cudaStream_t stream) {
-  int twos = 0, fours = 0;
-  const hcmix_status st = resident_clusters<2, kMode>(&twos);
-  if (st != HCMIX_OK) return st;
-  if (resident_clusters<4, kMode>(&fours) != HCMIX_OK) return launch_product<2, kMode>(A, twos, stream);
-  constexpr int kPercent = kMode == ProductMode::kWeight ? 92 : 87;
-  const int64_t by_two = (expected_tiles<2, kMode>(A) + twos - 1) / twos;
-  const int64_t by_four = (expected_tiles<4, kMode>(A) + fours - 1) / fours;
-  return by_four * kPercent <= by_two * 100 ? launch_product<4, kMode>(A, fours, stream)
-                                            : launch_product<2, kMode>(A, twos, stream);
 }
 
 // a, b, offsets, R, E, M, N, K, gated, out and types are set.
@@ -1363,10 +1297,8 @@ hcmix_status run_product(ProductArgs& A, cudaStream_t stream) {
   if (A.R > 0 && starts && tma_readable(A.a, experts) && tma_readable(A.b, 0) &&
       make_box_map(&A.a_map, A.a, experts, A.f16, 64) &&
       make_box_map(&A.b_map, A.b, 0, A.f16, 64) && make_box_map(&A.b16_map, A.b, 0, A.f16, 16))
-    return launch_clusters<kMode>(A, stream);
-  int ones = 0;
-  const hcmix_status st = resident_clusters<1, kMode>(&ones);
-  return st == HCMIX_OK ? launch_product<1, kMode>(A, ones, stream) : st;
+    return launch_product<2, kMode>(A, stream);
+  return launch_product<1, kMode>(A, stream);
 }
 
 }  // namespace sublayer
