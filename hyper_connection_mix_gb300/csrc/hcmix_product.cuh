@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   };
   const auto finish = [&](uint64_t& bar, uint32_t parity) {  // also after an abort
     const int none = 0;
-    product_wait(smem_u32(&bar), parity, &none, kProductWait / 4);
+    return product_wait(smem_u32(&bar), parity, &none, kProductWait / 4);
   };
   // The next tile, by a whole warp; false behind the last, and after an abort.
   uint32_t turns = 0;
@@ -950,6 +950,12 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
         else if (leader)
           finish(C.full[s], ~(full_at >> s) & 1);
       }
+      // and so do the MMAs' arrivals here, which are on their own when the leader's warp is done:
+      // each one's, since none orders the others (after an abort as far as there are any)
+      bool come = true;
+      for (uint32_t last = it > kDepth ? it - kDepth : 0; come && last < it; ++last)
+        come = finish(C.empty[last % kDepth], (last / kDepth) & 1);
+      finish(C.drain, 0);
     }
   } else if (kTma && kWeight && (warp == 3 || warp == 4 + kStore)) {
     // ---- the last stage of an expert took rows of the next one along: they count as zeros
@@ -981,6 +987,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   } else if (warp == 1 && leader) {
     // ---- MMA
     uint32_t it = 0, acc = 0, full_at = 0, tail_at = 0;
+    uint32_t empty_at = 0, used = 0;  // a bit for each stage: its arrivals so far, and whether any
     constexpr uint32_t kPair = (1u << kCtas) - 1;
     bool ok = true;
     const uint32_t kind = A.f16 ? 0u : (1u << 7) | (1u << 10);
@@ -1019,13 +1026,16 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
             mma_16<kTma>(d, da + i * kA, db + i * kB, idesc, kb > 0 || i > 0);
         }
         mma_commit<kTma>(smem_u32(&C.empty[s]), kPair);
+        empty_at ^= 1u << s, used |= 1u << s;
         if (kb == blocks - 1) mma_commit<kTma>(smem_u32(&C.acc_full[buf]), kPair);
       }
       it += blocks;
       ++acc;
     }
-    // what was issued is done before the block ends
+    // what was issued is done, and has arrived here, before the block ends
     mma_commit<kTma>(smem_u32(&C.drain), kPair);
+    for (int s = 0; s < kDepth; ++s)
+      if (used >> s & 1) finish(C.empty[s], ~(empty_at >> s) & 1);
     finish(C.drain, 0);
   } else if (warp >= 4 && warp < 4 + kStore) {
     // ---- epilogue: TMEM lanes 32 * w on, chunks of 32 columns in turn
@@ -1163,7 +1173,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   }
   tc_fence_before();
   __syncthreads();
-  // no block ends while others may still arrive at its barriers or send to it
+  // no block ends while the other's threads may still arrive at its barriers
   if (kTma) cluster_sync();
   tc_fence_after();
   if (warp == 2) product_tmem_dealloc<kTma>(tmem);
