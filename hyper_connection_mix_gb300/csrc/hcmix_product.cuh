@@ -1296,11 +1296,12 @@ hcmix_status launch_product(const ProductArgs& A, cudaStream_t stream) {
 // a, b, offsets, R, E, M, N, K, gated, out and types are set.
 template <ProductMode kMode>
 hcmix_status run_product(ProductArgs& A, cudaStream_t stream) {
-  if (kMode == ProductMode::kWeight)
+  if (kMode == ProductMode::kWeight) {
     A.vec = make_out_map(A);
-  else
+  } else {
     A.vec = vector_bytes(2, {{A.out, A.M}, {A.saved, A.M}}) == 16;
-  A.panel = panel_tiles(A.K);
+    A.panel = panel_tiles(A.K);
+  }
   const int experts = kMode == ProductMode::kWeight ? 0 : A.E;  // 0: a is a matrix as b is
   // a box starts on 16 bytes: u's features, too, where they lie along the rows
   const bool starts = kMode != ProductMode::kRowsM || !A.gated || A.M % 8 == 0;
