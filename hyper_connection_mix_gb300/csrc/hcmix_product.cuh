@@ -64,7 +64,7 @@ inline int panel_tiles(int64_t K) {
   const int64_t n = kPanelBytes / (kTileN(2) * K * 2);
   return (int)(n < 4 ? 4 : n > 64 ? 64 : n);
 }
-constexpr int64_t kProductWait = 4000000000ll;  // cycles: about two seconds
+constexpr int64_t kProductWait = 4000000000ll;  // cycles without a stage: about two seconds
 
 // One operand as it lies in memory: rows of contiguous elements.
 struct Matrix3 {
@@ -129,6 +129,7 @@ struct ProductControl {
   uint64_t drain;
   uint32_t tmem;
   int abort;
+  uint32_t copied;  // stages that the block's (first) copying warp has done with
   int64_t scan[32];
   RawRows raw[kProducers][kRawDepth];
 };
@@ -490,10 +491,9 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const void* map, int 
       : "memory");
 }
 
-// Waits for phase `parity` of a barrier; false when *abort is set or the time is up.  kOthers:
-// what threads of the pair's other block have written before they arrived is to be seen (an
-// acquire of the cluster's scope, which a wait for copies, MMAs or this block does without).
-// Time is counted in the multiprocessor's cycles, which take far less to read than the clock.
+// One look at phase `parity` of a barrier.  kOthers: what threads of the pair's other block have
+// written before they arrived is to be seen (an acquire of the cluster's scope, which a wait for
+// copies, MMAs or this block does without).
 template <bool kOthers>
 __device__ __forceinline__ bool product_try(uint32_t bar, uint32_t parity) {
   if (!kOthers) return sm100::mbar_try_wait(bar, parity);
@@ -507,15 +507,36 @@ __device__ __forceinline__ bool product_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// Looks until `look` finds what it waits for; false when *abort is set, or when *progress has stood
+// still for `cycles` of `clock`.  A wait may last as long as a tile, whose depth is an expert's rows
+// (2^27 rows of 7 elements by plain loads: 3.7 s), so that time alone says nothing.
+#pragma nv_exec_check_disable
+template <typename Look, typename Clock>
+__host__ __device__ __forceinline__ bool wait_while_moving(Look look, Clock clock,
+                                                           const volatile int* abort,
+                                                           const volatile uint32_t* progress,
+                                                           int64_t cycles) {
+  if (look()) return true;
+  int64_t t0 = clock();
+  uint32_t seen = *progress;
+  for (uint32_t i = 1;; ++i) {
+    if (look()) return true;
+    if ((i & 3u) != 0) continue;
+    if (*abort) return false;
+    const int64_t t = clock();
+    if (t - t0 <= cycles) continue;
+    const uint32_t now = *progress;
+    if (now == seen) return false;
+    seen = now, t0 = t;
+  }
+}
+// Time is counted in the multiprocessor's cycles, which take far less to read than the clock.
 template <bool kOthers = false>
 __device__ __forceinline__ bool product_wait(uint32_t bar, uint32_t parity,
-                                             const volatile int* abort, int64_t cycles) {
-  if (product_try<kOthers>(bar, parity)) return true;
-  const int64_t t0 = clock64();
-  for (uint32_t i = 1;; ++i) {
-    if (product_try<kOthers>(bar, parity)) return true;
-    if ((i & 3u) == 0 && (*abort || clock64() - t0 > cycles)) return false;
-  }
+                                             const volatile int* abort,
+                                             const volatile uint32_t* progress, int64_t cycles) {
+  return wait_while_moving([&] { return product_try<kOthers>(bar, parity); },
+                           [] { return (int64_t)clock64(); }, abort, progress, cycles);
 }
 
 // ---- the epilogue's chunks: 32 lanes (features) x 32 columns (rows) of a tile.
@@ -739,6 +760,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     }
     mbar_init(smem_u32(&C.drain), 1);
     C.abort = 0;
+    C.copied = 0;
     fence_mbarrier_init();
   }
   // the pair's barriers are there before its other block touches them
@@ -750,17 +772,19 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
   tc_fence_after();
   const uint32_t tmem = C.tmem;
   const volatile int* abort = &C.abort;
+  const volatile uint32_t* progress = &C.copied;
+  const auto moved = [&](uint32_t n) { *const_cast<volatile uint32_t*>(progress) = n; };
   const auto gave_up = [&]() {
     record_device_error(&g_product_error, kDevWaitTimeout);
     *reinterpret_cast<volatile int*>(&C.abort) = 1;
     return false;
   };
   const auto wait = [&](uint64_t& bar, uint32_t parity) {
-    return product_wait(smem_u32(&bar), parity, abort, kProductWait) || gave_up();
+    return product_wait(smem_u32(&bar), parity, abort, progress, kProductWait) || gave_up();
   };
   const auto finish = [&](uint64_t& bar, uint32_t parity) {  // also after an abort
     const int none = 0;
-    return product_wait(smem_u32(&bar), parity, &none, kProductWait / 4);
+    return product_wait(smem_u32(&bar), parity, &none, progress, kProductWait / 4);
   };
   // The next tile, by a whole warp; false behind the last, and after an abort.
   uint32_t turns = 0;
@@ -882,6 +906,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&C.full[s]));
+      if (p == 0 && lane == 0) moved(placed + 1);
     }
     async_wait<0>();
   } else if (kTma && warp == 0) {
@@ -903,6 +928,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
         if (!ok) break;
         if constexpr (kTma) {
           if (lane == 0) {
+            moved(it + 1);
             const int boxes = (n + 63) / 64;
             const uint32_t bytes = kABytes + (kWeight ? boxes * kBoxBytes : n * 128);
             const uint64_t keep = l2_policy_evict_last();
@@ -1007,7 +1033,8 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
         const bool tail = place < blocks && kb == blocks - 1;
         const int s = (it + (tail ? place : kb < place ? kb : kb + 1)) % kDepth;
         const int left = T.depth - kb * kTileK;
-        ok = tail ? product_wait<true>(smem_u32(&C.ready[s]), tail_at >> s & 1, abort, kProductWait) ||
+        ok = tail ? product_wait<true>(smem_u32(&C.ready[s]), tail_at >> s & 1, abort, progress,
+                                       kProductWait) ||
                         gave_up()
                   : wait(C.full[s], full_at >> s & 1);
         ok = __all_sync(0xffffffffu, ok);

@@ -87,7 +87,8 @@ hcmix_status hc_mix_expert_product_q4(const void* xs, int64_t xs_stride, hcmix_t
 
 /* Waits for `stream` and reports, once, whether a kernel of this header gave up a wait
  * on the current device since the last call (HCMIX_ERR_DEVICE: its outputs are
- * incomplete).  Every wait inside the kernels is bounded. */
+ * incomplete).  Every wait inside the kernels is bounded: it is given up when its block has
+ * copied nothing for about two seconds, however long a call takes. */
 hcmix_status hc_mix_expert_device_status(void* stream);
 
 #ifdef __cplusplus
