@@ -31,6 +31,7 @@
 #include <atomic>
 
 #include "hcmix_common.cuh"
+#include "hcmix_gate.cuh"
 #include "hcmix_sm100.cuh"
 #include "hcmix_vec.cuh"
 
@@ -711,8 +712,6 @@ __device__ __forceinline__ bool barrier_all(uint32_t id, uint32_t count, bool ye
   return r != 0;
 }
 
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
-
 constexpr int kProductThreads(int ctas, ProductMode mode) {
   return (4 + kStorers(ctas) +
           (ctas == 1 ? kProducers : mode == ProductMode::kWeight ? 1 : 0)) * 32;
@@ -1146,7 +1145,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const float o = other[i * 32 + lane];
-                v[i] = w < 2 ? silu(v[i]) * o : silu(o) * v[16 + i];
+                v[i] = w < 2 ? gate(v[i], o) : gate(o, v[16 + i]);
               }
               named_bar_sync(bar, 64);  // both have read
               const int c0 = w < 2 ? 0 : 16;

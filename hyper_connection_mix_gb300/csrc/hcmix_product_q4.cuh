@@ -19,6 +19,7 @@
 // 326 us); 64 features a unit did worse.
 #pragma once
 
+#include "hcmix_gate.cuh"
 #include "hcmix_vec.cuh"
 
 namespace hcmix {
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, kTiles == 1 ? 3 : 1)
         const int f = at.f + (kGated ? 0 : 16 * h) + g + 8 * (i / 2);
         const int row = at.row + 8 * n + 2 * t + i % 2;
         float y = sum(v);
-        if (kGated) y = __fdividef(y, 1.0f + __expf(-y)) * sum(v + 4 * kTiles);
+        if (kGated) y = gate(y, sum(v + 4 * kTiles));
         if (f < plan.features && row < at.end)
           static_cast<T*>(A.out)[(int64_t)row * plan.features + f] = from_f32<T>(y);
       }
