@@ -10,8 +10,9 @@
 //
 // With the rows as the MMA's N, which may be any multiple of 16 (of 32 for a pair of blocks),
 // an expert of few rows costs few columns and not a whole tile of 128.  fp32 accumulation in
-// TMEM over all of k, one rounding at the store.  The products' tiles are turned over in shared
-// memory on their way out; dweight's leave as they are, in boxes by the tensor memory accelerator.
+// TMEM, of a long k in parts (kPartK), and one rounding at the store.  The products' tiles are
+// turned over in shared memory on their way out; dweight's leave as they are, in boxes by the
+// tensor memory accelerator.
 //
 // Blocks are resident: one warp fills a ring of 64-wide slices of A and B, one issues the MMAs,
 // others store a tile while the next is computed.  What bounds it, measured on one GB300
@@ -65,6 +66,15 @@ inline int panel_tiles(int64_t K) {
   const int64_t n = kPanelBytes / (kTileN(2) * K * 2);
   return (int)(n < 4 ? 4 : n > 64 ? 64 : n);
 }
+// The MMAs' sums drop what lies below the last place of the running sum at each step of 16 k,
+// always towards zero, which adds up where roundings would average out (of 131072 rows: 1.5e-4 of
+// a sum of random terms, 7.9e-4 of positive ones).  So a tile of a long k is computed in parts,
+// each from zero, that the storing warps add up in fp32.  Parts of 16384 for a result of a 16-bit
+// type drop at most 7.9e-5, a sixth of fp16's half step.  Parts of 1024 for an fp32 result leave
+// 1.0e-6 (2.1e-6 of positive terms) at any length, a sum of 16384 fp32 roundings 1.5e-6 (1.9e-6).
+// 16384 rows 5120 x 5120 fp32: parts of 1024 548 us, of 2048 526 (2.1e-6, 5.3e-6), in one go 511
+// (1.9e-5, 7.9e-5).
+constexpr int kPartK = 16384, kPartK32 = 1024;
 constexpr int64_t kProductWait = 4000000000ll;  // cycles without a stage: about two seconds
 
 // One operand as it lies in memory: rows of contiguous elements.
@@ -83,6 +93,7 @@ struct ProductArgs {
   int E;
   int M, N, K;        // extents of m, n and k; product: N unused, dweight: K unused
   int panel;          // product: row tiles that take turns at the same features
+  int part;           // k that are summed in one go, a multiple of 64
   int gated;          // A's rows M .. 2 M - 1 are u's features, those before g's
   void* out;          // product: [R, M]; dweight: [E, M, N]
   void* saved;        // gated: [R, 2 M] or null
@@ -93,16 +104,17 @@ struct ProductArgs {
 // Set by a wait that was given up, on the device that it happened on.
 static __device__ uint32_t g_product_error;
 
-// A tile, as the scheduling warp tells the others.
+// A tile, or a part of one along k, as the scheduling warp tells the others.
 struct alignas(16) ProductTile {
   int expert;
   int m0, m1;  // origins of the two halves (64 lanes each) of the block's A
   int n;       // valid rows of B; 0: no more tiles
   int n0;      // the first, or the first outer feature
-  int k0;      // dweight: the expert's first row
+  int k0;      // the first k; dweight: the expert's first row
   int depth;   // of k
-  int unused;
+  int part;    // kFirstPart, kLastPart or both
 };
+constexpr int kFirstPart = 1, kLastPart = 2;
 
 // Plain loads.  A warp copies 16 rows of 64 elements as the aligned 16-byte blocks that hold
 // them (at the matrix's two ends element by element) into a ring of its own, and when they
@@ -260,6 +272,7 @@ __device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* 
   }
   T.m0 = (int)m * width + rank * (width / kCtas);
   T.m1 = A.gated ? A.M + T.m0 : T.m0 + kTileM / 2;
+  T.part = kFirstPart | kLastPart;
   return T;
 }
 
@@ -508,9 +521,10 @@ __device__ __forceinline__ bool product_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Looks until `look` finds what it waits for; false when *abort is set, or when *progress has stood
-// still for `cycles` of `clock`.  A wait may last as long as a tile, whose depth is an expert's rows
-// (2^27 rows of 7 elements by plain loads: 3.7 s), so that time alone says nothing.
+// Looks until `look` finds what it waits for; false when *abort is set, or when *progress has
+// stood still for `cycles` of `clock`.  A wait may last as long as a tile or, for a turn in the
+// queue, several, and a tile's depth is an expert's rows (2^27 rows of 7 elements by plain loads:
+// 3.7 s), so that time alone says nothing.
 #pragma nv_exec_check_disable
 template <typename Look, typename Clock>
 __host__ __device__ __forceinline__ bool wait_while_moving(Look look, Clock clock,
@@ -557,6 +571,34 @@ __device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, float (&v)[32]
         : "r"(taddr + ((uint32_t)(16 * h) << 16))
         : "memory");
   sm100::tmem_wait_ld();
+}
+// Adds the accumulator `from` to `to`, for the lanes and the chunks of columns (kChunk of them,
+// kStep apart) that a warp stores; kAtATime columns in registers.
+template <int kAtATime, int kChunk, int kStep>
+__device__ __forceinline__ void add_part(uint32_t to, uint32_t from, int first, int n) {
+  for (int c = first; c < n; c += kStep) {
+#pragma unroll 1
+    for (int i = 0; i < kChunk; i += kAtATime) {
+      float a[kAtATime], b[kAtATime];
+      uint32_t* x = reinterpret_cast<uint32_t*>(a);
+      uint32_t* y = reinterpret_cast<uint32_t*>(b);
+      if constexpr (kAtATime == 16) {
+        sm100::tmem_ld16(to + c + i, x);
+        sm100::tmem_ld16(from + c + i, y);
+      } else {
+        sm100::tmem_ld8(to + c + i, x);
+        sm100::tmem_ld8(from + c + i, y);
+      }
+      sm100::tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < kAtATime; ++k) a[k] += b[k];
+      if constexpr (kAtATime == 16)
+        sm100::tmem_st16(to + c + i, x);
+      else
+        sm100::tmem_st8(to + c + i, x);
+    }
+  }
+  sm100::tmem_wait_st();
 }
 __device__ __forceinline__ void clear(float (&v)[32]) {
 #pragma unroll
@@ -1011,7 +1053,8 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     }
   } else if (warp == 1 && leader) {
     // ---- MMA
-    uint32_t it = 0, acc = 0, full_at = 0, tail_at = 0;
+    uint32_t it = 0, full_at = 0, tail_at = 0;
+    uint32_t first = 1, acc_at = 0, acc_used = 0;  // accumulators: see the epilogue
     uint32_t empty_at = 0, used = 0;  // a bit for each stage: its arrivals so far, and whether any
     constexpr uint32_t kPair = (1u << kCtas) - 1;
     bool ok = true;
@@ -1023,8 +1066,11 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
                              (kWeight ? 1u << 16 : 0u) |
                              ((uint32_t)(round_rows<kCtas>(T.n) >> 3) << 17) |
                              ((uint32_t)(kTileM * kCtas >> 4) << 24);
-      const int buf = acc & 1;
-      if (acc >= 2) ok = __all_sync(0xffffffffu, wait(C.acc_empty[buf], (acc / 2 - 1) & 1));
+      if (T.part & kFirstPart) first ^= 1;
+      const uint32_t buf = T.part & kFirstPart ? first : first ^ 1;
+      if (acc_used >> buf & 1)
+        ok = __all_sync(0xffffffffu, wait(C.acc_empty[buf], ~(acc_at >> buf) & 1));
+      acc_at ^= 1u << buf, acc_used |= 1u << buf;
       tc_fence_after();
       const uint32_t d = tmem + buf * kAccumulator;
       const int place = kTma && kWeight ? tail_place(T.depth) : blocks;
@@ -1056,7 +1102,6 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
         if (kb == blocks - 1) mma_commit<kTma>(smem_u32(&C.acc_full[buf]), kPair);
       }
       it += blocks;
-      ++acc;
     }
     // what was issued is done, and has arrived here, before the block ends
     mma_commit<kTma>(smem_u32(&C.drain), kPair);
@@ -1064,10 +1109,12 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
       if (used >> s & 1) finish(C.empty[s], ~(empty_at >> s) & 1);
     finish(C.drain, 0);
   } else if (warp >= 4 && warp < 4 + kStore) {
-    // ---- epilogue: TMEM lanes 32 * w on, chunks of 32 columns in turn
+    // ---- epilogue: TMEM lanes 32 * w on, chunks of 32 columns in turn.  A tile's first part is in
+    // the accumulator that the tile before did not begin with, and is stored from there with the
+    // others, which come one after the other in the other one, added.
     const int w = warp % 4, half = (warp - 4) / 4;
     const int bar = 1 + (w & 1) + 2 * half;  // of g's and u's warp
-    uint32_t acc = 0;
+    uint32_t first = 1, acc_at = 0;
     bool ok = true;
     float* mine = exchange + (warp - 4) * (kTurnBytes(kMode) / 4);
     const float* other = exchange + (half * 4 + (w ^ 2)) * (kTurnBytes(kMode) / 4);
@@ -1079,15 +1126,31 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
         bool have = next(T);
         if (A.gated) have = barrier_all(bar, 64, have);
         if (!have) break;
-        const int buf = acc & 1;
         const bool any = T.depth > 0;
+        uint32_t buf = 0;
         if (any) {
-          ok = wait(C.acc_full[buf], (acc / 2) & 1);
+          if (T.part & kFirstPart) first ^= 1;
+          buf = T.part & kFirstPart ? first : first ^ 1;
+          ok = wait(C.acc_full[buf], acc_at >> buf & 1);
+          acc_at ^= 1u << buf;
           ok = A.gated ? barrier_all(bar, 64, ok) : __all_sync(0xffffffffu, ok);
         }
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + buf * kAccumulator;
+        const auto give_back = [&](uint32_t which) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_leader_read<kTma>(smem_u32(&C.acc_empty[which]));
+        };
+        const uint32_t lanes = tmem + ((uint32_t)(w * 32) << 16);
+        const uint32_t d = lanes + first * kAccumulator;
+        if (!(T.part & kFirstPart)) {
+          constexpr int kChunk = kWeight ? 64 : 32;
+          add_part<kTma ? 16 : 8, kChunk, kChunk * kStore / 4>(d, lanes + buf * kAccumulator,
+                                                                kChunk * half, T.n);
+          give_back(buf);
+        }
+        if (!(T.part & kLastPart)) continue;
         if constexpr (kWeight) {
           const int m0 = T.m0 + w * 32;
           for (int c = 64 * half; c < T.n && m0 < A.M; c += 16 * kStore) {
@@ -1154,12 +1217,7 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
             }
           }
         }
-        if (any) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_leader_read<kTma>(smem_u32(&C.acc_empty[buf]));
-          ++acc;
-        }
+        if (any) give_back(first);
       }
     };
     if (A.f16)
@@ -1175,15 +1233,24 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
     for (int64_t t0 = blockIdx.x / kCtas; ok && more; t0 += 32 * step) {
       const int64_t t = t0 + lane * step;
       if (t < tiles) T = tile_at<kCtas, kMode>(A, cum, t, rank);
-      else T.n = 0;
-      for (int i = 0; ok && more && i < 32; ++i, ++turns) {
-        const int q = turns % kQueue;
-        if (turns >= kQueue)
-          ok = __all_sync(0xffffffffu, wait(C.taken[q], (turns / kQueue - 1) & 1));
-        if (!ok) break;
-        if (lane == i) {
-          C.tile[q] = T;
-          mbar_arrive(smem_u32(&C.told[q]));
+      else T = {};
+      const int parts = T.depth > 0 ? (T.depth - 1) / A.part + 1 : 1;
+      for (int i = 0; ok && more && i < 32; ++i) {
+        const int of = __shfl_sync(0xffffffffu, parts, i);
+        for (int p = 0; ok && p < of; ++p, ++turns) {
+          const int q = turns % kQueue;
+          if (turns >= kQueue)
+            ok = __all_sync(0xffffffffu, wait(C.taken[q], (turns / kQueue - 1) & 1));
+          if (!ok) break;
+          if (lane == i) {
+            C.tile[q] = T;
+            C.tile[q].part = (p == 0 ? kFirstPart : 0) | (p == of - 1 ? kLastPart : 0);
+            if (T.depth > A.part) {
+              C.tile[q].depth = A.part;
+              T.k0 += A.part, T.depth -= A.part;  // of the next part
+            }
+            mbar_arrive(smem_u32(&C.told[q]));
+          }
         }
         more = __shfl_sync(0xffffffffu, T.n, i) > 0;
       }
@@ -1322,6 +1389,7 @@ hcmix_status launch_product(const ProductArgs& A, cudaStream_t stream) {
 // a, b, offsets, R, E, M, N, K, gated, out and types are set.
 template <ProductMode kMode>
 hcmix_status run_product(ProductArgs& A, cudaStream_t stream) {
+  A.part = A.out_f32 ? kPartK32 : kPartK;
   if (kMode == ProductMode::kWeight) {
     A.vec = make_out_map(A);
   } else {

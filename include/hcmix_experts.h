@@ -14,7 +14,9 @@
  * on the host before any launch, no trap):
  *   - `type` is the type of rows and weights.  The products take HCMIX_BF16 and
  *     HCMIX_F16 (HCMIX_F32 is refused: HCMIX_ERR_UNSUPPORTED), the gate's gradient
- *     all three.  Sums are fp32; a result of a 16-bit type is rounded once.
+ *     all three.  Sums are fp32 (of the tensor cores, which drop what lies below a sum's
+ *     last place; a sum of more than 16384 terms, or of more than 1024 for an fp32 result,
+ *     is added up of such parts); a result of a 16-bit type is rounded once.
  *   - Matrices are row-major with inner stride 1.  Inputs have a row stride in
  *     elements, at least their width, weights a stride between experts too; outputs
  *     are contiguous.  Any width from 1 to 2^24 and any alignment of the type itself
@@ -26,8 +28,8 @@
  *     unspecified.
  *   - Rows from offsets[E] on belong to no expert.  Their results are zero, and what
  *     they hold is not used.  An expert without rows reads no weights.
- *   - The same call gives the same bits every time (no atomics on values).  A row's
- *     result is a sum in the order of k, whatever other rows its expert has.
+ *   - The same call gives the same bits every time (no atomics on values).  The order of
+ *     a row's sums depends on k and the type alone, not on what other rows its expert has.
  *   - Outputs may not overlap inputs.
  */
 #ifndef HCMIX_EXPERTS_H
