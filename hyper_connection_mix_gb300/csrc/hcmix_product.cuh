@@ -17,13 +17,13 @@
 // Blocks are resident: one warp fills a ring of 64-wide slices of A and B, one issues the MMAs,
 // others store a tile while the next is computed.  What bounds it, measured on one GB300
 // (L2 gives the multiprocessors at most about 15 TB/s together):
-//   many rows   16384 rows 5120 -> 5120 bf16: 469 us, 1830 TFLOP/s; the MMAs alone 386 us, the
-//               copies alone 467 us
-//   some        128 experts of 256 rows 2048 -> 5120: 480 us; the weights' bytes at 6.8 TB/s: 396
-//   one         128 experts of one row: 391 us, 6.9 TB/s
-//   dweight     16384 rows 5120 x 5120: 522 us; 32 experts of 512 rows 5120 x 4096: 467 us, where
-//               the stores meet the copies in L2; 128 experts of one row: 393 us, 6.8 TB/s
-//   plain loads 61 experts of 72 rows 1023 -> 1001 fp16: 96 to 104 us, bound by the instructions
+//   many rows   16384 rows 5120 -> 5120 bf16: 467 to 483 us, 1840 to 1780 TFLOP/s; the MMAs alone
+//               386 us, the copies alone 467 us
+//   some        128 experts of 256 rows 2048 -> 5120: 488 us; the weights' bytes at 6.8 TB/s: 396
+//   one         128 experts of one row: 382 us, 7.0 TB/s
+//   dweight     16384 rows 5120 x 5120: 496 to 524 us; 32 experts of 512 rows 5120 x 4096: 515 us,
+//               where the stores meet the copies in L2; 128 experts of one row: 385 us, 7.0 TB/s
+//   plain loads 61 experts of 72 rows 1023 -> 1001 fp16: 82 to 87 us, bound by the instructions
 //               that shift rows into place
 #pragma once
 
@@ -59,8 +59,9 @@ __host__ __device__ constexpr int kStageBytes(int ctas) {
 __host__ __device__ constexpr int kStages(int ctas) { return ctas > 1 ? 6 : 2; }
 constexpr int kMostStages = 6;
 // Row tiles of a panel, whose rows are read again for each of the features' tiles: few enough to
-// stay in L2 beside the weights (32768 rows of 128 experts 2048 -> 5120: panels of 5 MB 687 us,
-// 10 MB 682, 20 MB 699; 32 experts of 512 rows 5120 -> 4096: 20 MB 409, 40 MB 424, 80 MB 455).
+// stay in L2 beside the weights (128 experts of 256 rows 2048 -> 5120: panels of 5 MB 474 us, 10 MB
+// 488, 20 MB 522, 40 MB 592; of like rows on average, but skewed, 685, 665, 682, 659; 32 experts
+// of 256 to 767 rows 5120 -> 4096: 585, 585, 571, 558).
 constexpr int64_t kPanelBytes = 10 << 20;
 inline int panel_tiles(int64_t K) {
   const int64_t n = kPanelBytes / (kTileN(2) * K * 2);
@@ -263,7 +264,8 @@ __device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* 
     T.expert = lo;
     expert_rows(A, lo, first, count);
     const int nt = cum[lo + 1] - cum[lo], j = q - cum[lo];
-    // the expert's tiles are of like size, so that none of them is nearly empty
+    // the expert's tiles are of like size, as far as the MMA's multiples allow: 300 rows are 160 and
+    // 140, 513 are 192, 192 and 129, but 2049 still eight tiles of 256 and one of a row
     const int size = round_rows<kCtas>((count + nt - 1) / nt);
     T.n0 = first + j * size;
     T.n = count - j * size < size ? count - j * size : size;
@@ -279,8 +281,8 @@ __device__ __forceinline__ ProductTile tile_at(const ProductArgs& A, const int* 
 // dweight by pairs: an expert's last 64 rows, if they are fewer, are zeroed behind before they
 // are multiplied, which takes about 2 us from their arrival.  So they are copied up to
 // kTailLead stages early and still multiplied last.  Their place among the tile's stages; the
-// number of stages where there are none such.  (32 experts of 256 to 767 rows 5120 x 4096: 588 us
-// in their turn, 555 three stages early, the same two or four.)
+// number of stages where there are none such.  (32 experts of 256 to 767 rows 5120 x 4096: 602 us
+// in their turn, 580 three stages early.)
 constexpr int kTailLead = 3;
 __device__ __forceinline__ int tail_place(int depth) {
   const int blocks = (depth + kTileK - 1) / kTileK;
@@ -522,9 +524,8 @@ __device__ __forceinline__ bool product_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Looks until `look` finds what it waits for; false when *abort is set, or when *progress has
-// stood still for `cycles` of `clock`.  A wait may last as long as a tile or, for a turn in the
-// queue, several, and a tile's depth is an expert's rows (2^27 rows of 7 elements by plain loads:
-// 3.7 s), so that time alone says nothing.
+// stood still for `cycles` of `clock`.  What is waited for may take any number of stages (a part of
+// a tile, or for a turn in the queue several), so that time alone says nothing.
 #pragma nv_exec_check_disable
 template <typename Look, typename Clock>
 __host__ __device__ __forceinline__ bool wait_while_moving(Look look, Clock clock,
@@ -972,6 +973,8 @@ __global__ void __launch_bounds__(kProductThreads(kCtas, kMode), 1)
             moved(it + 1);
             const int boxes = (n + 63) / 64;
             const uint32_t bytes = kABytes + (kWeight ? boxes * kBoxBytes : n * 128);
+            // (without the hint these copies, and what runs behind them, take the same time
+            // within 2 %: 128 experts of 256 rows 488 us either way, a call behind 2.7 GB 96 us)
             const uint64_t keep = l2_policy_evict_last();
             // block 0 waits for both blocks' copies at once, but for the last rows of an expert,
             // behind which each block has to zero its own

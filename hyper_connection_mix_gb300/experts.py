@@ -14,6 +14,9 @@ Rows are 2-D CUDA tensors of bf16 or fp16 (the gate's gradient: fp32 too) with u
 inner stride; weights are 3-D of the same type, [expert, ., .], with unit inner
 stride and any stride between rows and experts that leaves them apart.  `offsets`
 is int32 [E + 1], as `sublayer.hc_mix_expert_sort` gives it.
+
+A product whose kernel gives up a wait leaves its results incomplete, and no call says
+so: ask hc_mix_expert_device_status where the host waits for the results anyway.
 """
 from __future__ import annotations
 
@@ -191,7 +194,8 @@ def hc_mix_expert_product_q4(xs: torch.Tensor, codes: torch.Tensor, scales: torc
     """hc_mix_expert_product (with `gated` hc_mix_expert_product_gated) with weights of 4 bits,
     w = (code - 8) * scale: codes[E, N, K // 2] uint8, the lower four bits of a byte for the
     even k, and scales[E, N, K // group] of xs's type, both contiguous; group is 32, 64, 128
-    or 256.  Meant for few rows an expert."""
+    or 256.  Meant for up to eight rows an expert: with more, hc_mix_expert_product with weights of
+    16 bits takes less time."""
     px, sx, code, R, K, dtype, device = _matrix(xs, "xs")
     if stream is not None or device.index != _device():
         return _there(stream, device, hc_mix_expert_product_q4, xs, codes, scales, offsets, gated,
